@@ -454,6 +454,134 @@ svdq_status svdq_score_modal_rel_l2_ref(const uint16_t* Y, int64_t ldy, const ui
                                         const int8_t* row_group, int64_t n_rows, double* sums,
                                         svdq_stream_t stream);
 
+/*
+ * The attention half of the block around the projections: norm in front of a projection, rotary
+ * positions, the 8-bit key / value cache and attention over it.  The pages fix none of these;
+ * each is defined by its formulas below.
+ */
+
+/*
+ * Residual addition, root-mean-square norm, smoothing and MXFP8 quantisation of each row, fused
+ * with the low-rank down-projection: the activations of an MXFP8 svdq_w4a4_gemm straight from
+ * the residual stream.
+ *
+ *   h   = bf16(x + residual)                             (fp32 sum; h = x when residual is NULL)
+ *   inv = fl32(1 / sqrt(mean_k h² + eps))                (sum, mean and root in fp64)
+ *   x̂   = fl32(fl32(fl32(h·inv)·gamma)·fl32(1/λ))        (gamma NULL: 1; lambda NULL: λ = 1)
+ *   codes, scales: MXFP8 of x̂ (see svdq_format);  D = bf16(x̂)·lora_downᵀ, fp32 [M, r]
+ * X, residual and H [M, K] bf16 with leading dimensions ldx, ldr, ldh; gamma [K] bf16; eps > 0.
+ * H receives h and is required with a residual (ignored without one); it may be X or residual
+ * itself (in place), but must not overlap them otherwise.  codes [M, K], scales [M, K/32].  D may
+ * be NULL iff r == 0.  Codes and scales bit-exact: the fp64 sum leaves inv independent of the
+ * order of summation except where a sum of squares spanning more than 2^24 in magnitude lies
+ * next to a rounding border.
+ */
+svdq_status svdq_rmsnorm_quant_act(const uint16_t* X, int64_t M, int64_t K, int64_t ldx,
+                                   const uint16_t* residual, int64_t ldr, uint16_t* H,
+                                   int64_t ldh, const uint16_t* gamma, float eps,
+                                   const float* lambda, const uint16_t* lora_down, int64_t r,
+                                   uint8_t* codes, uint8_t* scales, float* D,
+                                   svdq_stream_t stream);
+
+/*
+ * Rotary positions with several axes (time, height, width of a video row, or one axis of text).
+ * Each of `heads` consecutive heads of `dim` channels of a row has its first
+ * rot = sum(axis_dims) channels turned; the others are copied.  The rot/2 pairs belong to the
+ * axes in order, axis_dims[a]/2 to axis a, and pair i turns by θ = pos[m, axis(i)]·freq[i]:
+ *
+ *   (u, v) -> (u·cos θ − v·sin θ, u·sin θ + v·cos θ)       (inverse != 0: by −θ)
+ * interleaved != 0: pair i is channels (2i, 2i + 1); else channels (i, i + rot/2).
+ * X, Y [M, heads·dim] bf16 with leading dimensions ldx, ldy (a packed q|k|v row holds its query
+ * and key heads side by side); Y may be X itself, but must not overlap it otherwise.  pos: device
+ * int32 [M, n_axes], any values; freq: device fp64 [rot/2], radians per position
+ * (svdq_rope_frequencies).  θ is formed and reduced to a turn in fp64.  dim a multiple of 16 in
+ * [16, 256]; axis_dims (host int64[n_axes]) even and >= 0, their sum a multiple of 16 in
+ * [16, dim]; n_axes in [1, 4].  inverse != 0 is also the gradient of the forward turn.
+ */
+svdq_status svdq_rope_axes(const uint16_t* X, int64_t M, int64_t ldx, int64_t heads, int64_t dim,
+                           const int32_t* pos, const double* freq, int64_t n_axes,
+                           const int64_t* axis_dims, int interleaved, int inverse, uint16_t* Y,
+                           int64_t ldy, svdq_stream_t stream);
+
+/*
+ * Frequencies for svdq_rope_axes, HOST function: axis a's pair j of axis_dims[a]/2 gets
+ * theta^(−2j/axis_dims[a]).  freq: host fp64 [sum(axis_dims)/2].  theta > 1; axis_dims even.
+ */
+svdq_status svdq_rope_frequencies(int64_t n_axes, const int64_t* axis_dims, double theta,
+                                  double* freq);
+
+/*
+ * Paged 8-bit key / value cache.  A page holds SVDQ_KV_PAGE tokens of every head: for each head
+ * 64·dim E4M3 codes of K, as many of V and one exponent byte of each (value = code·2^(byte−127)).
+ *   k_codes, v_codes: device uint8 [n_pages, heads, 64·dim]
+ *   k_scales, v_scales: device uint8 [n_pages, heads]
+ * The codes of a page are in the attention kernel's operand order, not in [token, channel] order:
+ *   K (token t, channel d): byte (((t/32·(dim/64) + d/64)·2 + d/16%2)·64 + d/32%2·32 + t%32)·16
+ *                                 + d%16
+ *   V (token t, channel d): byte ((d/32·2 + t/32)·64 + t/4%2·32 + d%32)·16
+ *                                 + t/16%2·8 + t/8%2·4 + t%4
+ * block_table: device int32 [B, max_blocks], the page of each run of 64 tokens of a sequence.
+ * cu_rows: device int32 [B + 1], non-decreasing from 0: sequence b owns the packed rows
+ * [cu_rows[b], cu_rows[b+1]) of the tensors, tokens start[b] onward of the sequence (start:
+ * device int32 [B]).  max_rows: host bound of the rows of one sequence (rows past it are not
+ * handled).  Tokens whose block_table entry is missing (past max_blocks) or outside
+ * [0, n_pages) are skipped, as are sequences whose cu_rows leave [0, rows].  dim 64 or 128;
+ * heads and B at most 65535.  rows == 0 or max_rows == 0: nothing to do.
+ *
+ * svdq_kv_write appends rows of K and V (bf16 [rows, heads·dim], leading dimensions ldk, ldv).
+ * Per page and head, for K and V each: a = max|new values of the page|; e = the smallest exponent
+ * with a <= 448·2^e, within [−110, 119] (−110 for a == 0); if the page already holds tokens
+ * before start[b], e is at least the stored exponent, and where it grows the earlier codes are
+ * rounded again, E4M3(code·2^(e_old − e)).  code = E4M3(x·2^−e), nearest even, saturating;
+ * scale byte = e + 127.  The page's later slots keep their bytes.  Bit-exact.  Two sequences
+ * must not write the same page in one call.
+ *
+ * svdq_kv_read writes the values of tokens start[b] .. of each sequence to K and V (bf16, exact).
+ * Rows of skipped tokens are left as they were.
+ */
+#define SVDQ_KV_PAGE 64
+svdq_status svdq_kv_write(const uint16_t* K, int64_t ldk, const uint16_t* V, int64_t ldv,
+                          int64_t rows, int64_t heads, int64_t dim, const int32_t* cu_rows,
+                          const int32_t* start, int64_t B, int64_t max_rows,
+                          const int32_t* block_table, int64_t max_blocks, int64_t n_pages,
+                          uint8_t* k_codes, uint8_t* v_codes, uint8_t* k_scales,
+                          uint8_t* v_scales, svdq_stream_t stream);
+svdq_status svdq_kv_read(uint16_t* K, int64_t ldk, uint16_t* V, int64_t ldv, int64_t rows,
+                         int64_t heads, int64_t dim, const int32_t* cu_rows, const int32_t* start,
+                         int64_t B, int64_t max_rows, const int32_t* block_table,
+                         int64_t max_blocks, int64_t n_pages, const uint8_t* k_codes,
+                         const uint8_t* v_codes, const uint8_t* k_scales, const uint8_t* v_scales,
+                         svdq_stream_t stream);
+
+/*
+ * Softmax attention over the paged 8-bit cache.
+ *
+ *   O = softmax(scale·Q·Kᵀ)·V over the tokens each row sees,  lse = ln Σ exp(scale·q·k)
+ * Q, O [rows, q_heads·dim] bf16 with leading dimensions ldq, ldo (O must not overlap Q); query head
+ * j reads key head j/(q_heads/kv_heads) (q_heads a multiple of
+ * kv_heads).  cu_rows, block_table as at svdq_kv_write; kv_len: device int32 [B], cached tokens of
+ * each sequence (limited to 64·max_blocks).  Row i of a sequence of n rows sees tokens
+ * [0, kv_len), with causal != 0 [0, kv_len − n + i + 1): the last row sees every token.  A row
+ * that sees none gets O = 0 and lse = −inf.  Tokens in pages outside [0, n_pages) are masked.
+ * Rows of no sequence are left as they were.  lse: fp32 [rows, q_heads], may be NULL.
+ * scale > 0 and finite.  max_rows, max_kv: host bounds of one sequence's rows and of kv_len (they
+ * size the grid and the split; rows past max_rows are not computed, kv_len itself is not
+ * limited by max_kv).  workspace: at least svdq_attn_kv8_workspace_bytes(...) bytes (0 when the
+ * page range is not split; −1: unsupported), 256-byte aligned, the caller's, not shared with a
+ * call that may run at the same time.  dim 64 or 128.  fp32 statistics and accumulation, the
+ * weights rounded once to bf16; no atomics, results repeat bit for bit.
+ */
+int64_t svdq_attn_kv8_workspace_bytes(int64_t rows, int64_t q_heads, int64_t kv_heads,
+                                      int64_t dim, int64_t B, int64_t max_rows, int64_t max_kv);
+svdq_status svdq_attn_kv8(const uint16_t* Q, int64_t ldq, int64_t rows, int64_t q_heads,
+                          int64_t kv_heads, int64_t dim, const int32_t* cu_rows,
+                          const int32_t* kv_len, int64_t B, int64_t max_rows, int64_t max_kv,
+                          const int32_t* block_table, int64_t max_blocks, int64_t n_pages,
+                          const uint8_t* k_codes, const uint8_t* v_codes, const uint8_t* k_scales,
+                          const uint8_t* v_scales, float scale, int causal, uint16_t* O,
+                          int64_t ldo, float* lse, void* workspace, int64_t workspace_bytes,
+                          svdq_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

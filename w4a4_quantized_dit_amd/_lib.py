@@ -5,6 +5,7 @@ memory owned by the caller) plus sizes; it checks dtypes / devices / shapes, pas
 and the current torch stream, and raises SvdqError on a non-zero status.  No step of the layer
 runs in Python: when the library is missing, loading fails loudly.
 """
+import contextlib
 import ctypes
 import os
 import re
@@ -70,6 +71,21 @@ _SIGS = {
                                                  _i64, _c_p, _i64, _c_p]),
     "svdq_score_modal_rel_l2_ref": (ctypes.c_int, [_c_p, _i64, _c_p, _i64, _i64, _i64, _c_p, _c_p,
                                                    _i64, _c_p, _c_p]),
+    "svdq_rmsnorm_quant_act": (ctypes.c_int, [_c_p, _i64, _i64, _i64, _c_p, _i64, _c_p, _i64, _c_p,
+                                              ctypes.c_float, _c_p, _c_p, _i64, _c_p, _c_p, _c_p,
+                                              _c_p]),
+    "svdq_rope_axes": (ctypes.c_int, [_c_p, _i64, _i64, _i64, _i64, _c_p, _c_p, _i64, _c_p,
+                                      ctypes.c_int, ctypes.c_int, _c_p, _i64, _c_p]),
+    "svdq_rope_frequencies": (ctypes.c_int, [_i64, _c_p, ctypes.c_double, _c_p]),
+    "svdq_kv_write": (ctypes.c_int, [_c_p, _i64, _c_p, _i64, _i64, _i64, _i64, _c_p, _c_p, _i64,
+                                     _i64, _c_p, _i64, _i64, _c_p, _c_p, _c_p, _c_p, _c_p]),
+    "svdq_kv_read": (ctypes.c_int, [_c_p, _i64, _c_p, _i64, _i64, _i64, _i64, _c_p, _c_p, _i64,
+                                    _i64, _c_p, _i64, _i64, _c_p, _c_p, _c_p, _c_p, _c_p]),
+    "svdq_attn_kv8_workspace_bytes": (_i64, [_i64] * 7),
+    "svdq_attn_kv8": (ctypes.c_int, [_c_p, _i64, _i64, _i64, _i64, _i64, _c_p, _c_p, _i64, _i64,
+                                     _i64, _c_p, _i64, _i64, _c_p, _c_p, _c_p, _c_p,
+                                     ctypes.c_float, ctypes.c_int, _c_p, _i64, _c_p, _c_p, _i64,
+                                     _c_p]),
 }
 
 _lib = None
@@ -497,3 +513,167 @@ def svdq_score_modal_rel_l2(Y, X, W, rows, row_group, sums, stream=None):
         _ptr(W, _bf16(), "W", rows=True), _ld(W), M, N, K, _ptr(rows, torch.int32, "rows"),
         _ptr(row_group, torch.int8, "row_group"), rows.numel(),
         _ptr(sums, torch.float64, "sums", 8), _stream(stream)))
+
+
+# ------------------------------------------------------------------------------------------
+# the attention half: norm, rotary positions, the 8-bit cache and attention over it
+# ------------------------------------------------------------------------------------------
+
+def _on_device(*tensors):
+    """A guard for the device of the tensors (which must all be on one), so that a call on
+    tensors of another device than the current one runs there, on that device's stream."""
+    torch = _torch()
+    dev = None
+    for t in tensors:
+        if t is not None:
+            if dev is None:
+                dev = t.device
+            elif t.device != dev:
+                raise ValueError(f"tensors on {dev} and {t.device}: one device is needed")
+    if dev is None or dev.type != "cuda" or dev.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(dev)
+
+
+def _rows_of(t, rows, cols, name):
+    """A matrix of at least `rows` rows and exactly `cols` columns."""
+    if t is not None and (t.dim() != 2 or t.shape[0] < rows or t.shape[1] != cols):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [{rows}, {cols}]")
+    return t
+
+
+def svdq_rmsnorm_quant_act(X, residual, H, gamma, eps, lam, lora_down, r, codes, scales, D,
+                           stream=None):
+    """Residual + RMS norm + smoothing + MXFP8 codes / scales + D; X, residual, H [M, K] bf16,
+    gamma [K] bf16, lam [K] fp32; H receives the sum (required with a residual)."""
+    torch = _torch()
+    if X.dim() != 2:
+        raise ValueError("X must be a 2-D matrix with contiguous rows")
+    M, K = X.shape
+    f32, bf = torch.float32, _bf16()
+    if r:
+        _rows_of(lora_down, r, K, "lora_down")
+    with _on_device(X, residual, H, gamma, lam, lora_down if r else None, codes, scales,
+                    D if r else None):
+        _check(load().svdq_rmsnorm_quant_act(
+            _ptr(X, bf, "X", rows=True), M, K, _ld(X),
+            _ptr(_rows_of(residual, M, K, "residual"), bf, "residual", rows=True),
+            _ld(residual) if residual is not None else K,
+            _ptr(_rows_of(H, M, K, "H"), bf, "H", rows=True), _ld(H) if H is not None else K,
+            _ptr(gamma, bf, "gamma", K), float(eps), _ptr(lam, f32, "lambda", K),
+            _ptr(lora_down if r else None, bf, "lora_down", r * K), int(r),
+            _ptr(codes, torch.uint8, "codes", M * K),
+            _ptr(scales, torch.uint8, "scales", M * K // 32),
+            _ptr(D if r else None, f32, "D", M * r), _stream(stream)))
+
+
+def svdq_rope_frequencies(axis_dims, theta):
+    """Host: numpy float64 frequencies (radians per position) of the axes' pairs."""
+    import numpy as np
+    dims = [int(d) for d in axis_dims]
+    out = np.zeros(max(1, sum(max(0, d) for d in dims) // 2))
+    arr = (ctypes.c_int64 * max(1, len(dims)))(*dims)
+    _check(load().svdq_rope_frequencies(len(dims), ctypes.cast(arr, _c_p), float(theta),
+                                        out.ctypes.data))
+    return out
+
+
+def svdq_rope_axes(X, heads, dim, pos, freq, axis_dims, interleaved, inverse, Y, stream=None):
+    """Rotary positions of `heads` heads of each row of X into Y (X itself: in place); pos int32
+    [M, n_axes], freq fp64 [sum(axis_dims)/2]."""
+    torch = _torch()
+    M = X.shape[0]
+    n = len(axis_dims)
+    arr = (ctypes.c_int64 * max(1, n))(*[int(d) for d in axis_dims])
+    _rows_of(X, M, heads * dim, "X")
+    _rows_of(Y, M, heads * dim, "Y")
+    with _on_device(X, pos, freq, Y):
+        _check(load().svdq_rope_axes(
+            _ptr(X, _bf16(), "X", rows=True), M, _ld(X), int(heads), int(dim),
+            _ptr(_rows_of(pos, M, n, "pos"), torch.int32, "pos"),
+            _ptr(freq, torch.float64, "freq", sum(int(d) for d in axis_dims) // 2), n,
+            ctypes.cast(arr, _c_p), int(bool(interleaved)), int(bool(inverse)),
+            _ptr(Y, _bf16(), "Y", rows=True), _ld(Y), _stream(stream)))
+
+
+def _cache_args(k_codes, v_codes, k_scales, v_scales, dim, block_table, cu_rows, per_seq, what):
+    """Checked pointers and sizes of the cache operands: (codes and scales pointers), heads,
+    n_pages, B, max_blocks and the pointers of block_table, cu_rows and per_seq."""
+    torch = _torch()
+    u8, i32 = torch.uint8, torch.int32
+    if k_codes.dim() != 3 or k_codes.shape[2] != 64 * dim:
+        raise ValueError(f"k_codes has shape {tuple(k_codes.shape)}, expected "
+                         f"[pages, heads, {64 * dim}]")
+    n_pages, heads = k_codes.shape[:2]
+    if v_codes.shape != k_codes.shape:
+        raise ValueError("v_codes must have the shape of k_codes")
+    for t, name in ((k_scales, "k_scales"), (v_scales, "v_scales")):
+        if tuple(t.shape) != (n_pages, heads):
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [{n_pages}, {heads}]")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_blocks]")
+    B, blocks = block_table.shape
+    ptrs = [_ptr(k_codes, u8, "k_codes"), _ptr(v_codes, u8, "v_codes"),
+            _ptr(k_scales, u8, "k_scales"), _ptr(v_scales, u8, "v_scales")]
+    return (ptrs, heads, n_pages, B, blocks, _ptr(block_table, i32, "block_table"),
+            _ptr(cu_rows, i32, "cu_rows", B + 1), _ptr(per_seq, i32, what, B))
+
+
+def _kv_call(name, K, V, dim, cu_rows, start, max_rows, block_table, k_codes, v_codes, k_scales,
+             v_scales, stream):
+    with _on_device(K, V, cu_rows, start, block_table, k_codes, v_codes, k_scales, v_scales):
+        ptrs, heads, n_pages, B, blocks, table, cu, st = _cache_args(
+            k_codes, v_codes, k_scales, v_scales, dim, block_table, cu_rows, start, "start")
+        rows = K.shape[0]
+        _rows_of(K, rows, heads * dim, "K")
+        if V.shape != K.shape:
+            raise ValueError("V must have the shape of K")
+        if rows == 0:   # an empty tensor has no address
+            return
+        _check(getattr(load(), name)(
+            _ptr(K, _bf16(), "K", rows=True), _ld(K), _ptr(V, _bf16(), "V", rows=True), _ld(V),
+            rows, heads, int(dim), cu, st, B, int(max_rows), table, blocks, n_pages, *ptrs,
+            _stream(stream)))
+
+
+def svdq_kv_write(K, V, dim, cu_rows, start, max_rows, block_table, k_codes, v_codes, k_scales,
+                  v_scales, stream=None):
+    """Append the packed rows K, V [rows, heads·dim] bf16 to the paged 8-bit cache."""
+    _kv_call("svdq_kv_write", K, V, dim, cu_rows, start, max_rows, block_table, k_codes, v_codes,
+             k_scales, v_scales, stream)
+
+
+def svdq_kv_read(K, V, dim, cu_rows, start, max_rows, block_table, k_codes, v_codes, k_scales,
+                 v_scales, stream=None):
+    """Read tokens of the paged 8-bit cache back into K, V [rows, heads·dim] bf16."""
+    _kv_call("svdq_kv_read", K, V, dim, cu_rows, start, max_rows, block_table, k_codes, v_codes,
+             k_scales, v_scales, stream)
+
+
+def svdq_attn_kv8_workspace_bytes(rows, q_heads, kv_heads, dim, B, max_rows, max_kv):
+    return int(load().svdq_attn_kv8_workspace_bytes(int(rows), int(q_heads), int(kv_heads),
+                                                    int(dim), int(B), int(max_rows), int(max_kv)))
+
+
+def svdq_attn_kv8(Q, dim, cu_rows, kv_len, max_rows, max_kv, block_table, k_codes, v_codes,
+                  k_scales, v_scales, scale, causal, O, lse=None, workspace=None, stream=None):
+    """Attention of Q [rows, q_heads·dim] bf16 over the paged 8-bit cache into O and lse (fp32
+    [rows, q_heads] or None); workspace uint8 (svdq_attn_kv8_workspace_bytes) or None."""
+    torch = _torch()
+    with _on_device(Q, cu_rows, kv_len, block_table, k_codes, v_codes, k_scales, v_scales, O, lse,
+                    workspace):
+        ptrs, heads, n_pages, B, blocks, table, cu, ln = _cache_args(
+            k_codes, v_codes, k_scales, v_scales, dim, block_table, cu_rows, kv_len, "kv_len")
+        if Q.dim() != 2 or Q.shape[1] % dim != 0:
+            raise ValueError(f"Q has shape {tuple(Q.shape)}, expected [rows, heads·{dim}]")
+        rows, q_heads = Q.shape[0], Q.shape[1] // dim
+        _rows_of(O, rows, q_heads * dim, "O")
+        if rows == 0:
+            return
+        _check(load().svdq_attn_kv8(
+            _ptr(Q, _bf16(), "Q", rows=True), _ld(Q), rows, q_heads, heads, int(dim), cu, ln, B,
+            int(max_rows), int(max_kv), table, blocks, n_pages, *ptrs, float(scale),
+            int(bool(causal)), _ptr(O, _bf16(), "O", rows=True), _ld(O),
+            _ptr(lse, torch.float32, "lse", rows * q_heads),
+            _ptr(workspace, torch.uint8, "workspace"),
+            workspace.numel() if workspace is not None else 0, _stream(stream)))

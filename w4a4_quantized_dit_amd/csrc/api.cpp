@@ -1,6 +1,7 @@
 // C ABI: argument validation on the host (nothing is enqueued for an invalid call), dispatch to
 // the gfx950 kernels, status codes and a thread-local error message.
 #include <hip/hip_runtime.h>
+#include <math.h>
 #include <stdarg.h>
 #include <stdint.h>
 #include <stdio.h>
@@ -97,6 +98,47 @@ svdq_status check_fmt(const char* fn, int fmt) {
   if (fmt != SVDQ_NVFP4 && fmt != SVDQ_INT4_G64 && fmt != SVDQ_MXFP4 && fmt != SVDQ_MXFP8)
     return fail(SVDQ_INVALID_ARG, "%s: unknown format %d", fn, fmt);
   return SVDQ_OK;
+}
+
+svdq_status check_rows(const char* fn, const char* name, int64_t n, int64_t least) {
+  if (n < least || n > INT32_MAX)
+    return fail(SVDQ_UNSUPPORTED_SHAPE, "%s: %s=%lld must lie in [%lld, 2^31)", fn, name,
+                (long long)n, (long long)least);
+  return SVDQ_OK;
+}
+
+svdq_status check_axes(const char* fn, int64_t n_axes, const int64_t* axis_dims) {
+  if (n_axes < 1 || n_axes > 4)
+    return fail(SVDQ_UNSUPPORTED_SHAPE, "%s: n_axes=%lld must lie in [1, 4]", fn,
+                (long long)n_axes);
+  for (int64_t a = 0; a < n_axes; ++a)
+    if (axis_dims[a] < 0 || axis_dims[a] > 256 || axis_dims[a] % 2 != 0)
+      return fail(SVDQ_UNSUPPORTED_SHAPE, "%s: axis_dims[%lld]=%lld must be even, in [0, 256]", fn,
+                  (long long)a, (long long)axis_dims[a]);
+  return SVDQ_OK;
+}
+
+// The arguments every call on the paged cache shares.
+svdq_status check_cache(const char* fn, int64_t heads, int64_t dim, const int32_t* cu_rows,
+                        int64_t B, int64_t rows, int64_t max_rows, const int32_t* block_table,
+                        int64_t max_blocks, int64_t n_pages, const uint8_t* k_codes,
+                        const uint8_t* v_codes, const uint8_t* k_scales,
+                        const uint8_t* v_scales) {
+  REQUIRE_PTR(cu_rows); REQUIRE_PTR(block_table); REQUIRE_PTR(k_codes); REQUIRE_PTR(v_codes);
+  REQUIRE_PTR(k_scales); REQUIRE_PTR(v_scales);
+  REQUIRE_ALIGNED(k_codes); REQUIRE_ALIGNED(v_codes);
+  if (dim != 64 && dim != 128)
+    return fail(SVDQ_UNSUPPORTED_SHAPE, "%s: dim=%lld must be 64 or 128", fn, (long long)dim);
+  if (heads < 1 || heads > 65535)
+    return fail(SVDQ_UNSUPPORTED_SHAPE, "%s: %lld key heads, must lie in [1, 65535]", fn,
+                (long long)heads);
+  if (B < 1 || B > 65535)
+    return fail(SVDQ_UNSUPPORTED_SHAPE, "%s: B=%lld must lie in [1, 65535]", fn, (long long)B);
+  svdq_status s = check_rows(fn, "rows", rows, 0);
+  if (s == SVDQ_OK) s = check_rows(fn, "max_rows", max_rows, 0);
+  if (s == SVDQ_OK) s = check_rows(fn, "max_blocks", max_blocks, 1);
+  if (s == SVDQ_OK) s = check_rows(fn, "n_pages", n_pages, 1);
+  return s;
 }
 
 #define TRY(x)                      \
@@ -699,6 +741,179 @@ svdq_status svdq_score_modal_rel_l2_ref(const uint16_t* Y, int64_t ldy, const ui
   if (n_rows == 0) return ok();
   return hip_result(svdq::launch_score_ref(Y, ldy, Yref, ldr, M, N, rows, row_group, n_rows, sums,
                                            reinterpret_cast<hipStream_t>(stream)),
+                    fn);
+}
+
+svdq_status svdq_rmsnorm_quant_act(const uint16_t* X, int64_t M, int64_t K, int64_t ldx,
+                                   const uint16_t* residual, int64_t ldr, uint16_t* H,
+                                   int64_t ldh, const uint16_t* gamma, float eps,
+                                   const float* lambda, const uint16_t* lora_down, int64_t r,
+                                   uint8_t* codes, uint8_t* scales, float* D,
+                                   svdq_stream_t stream) {
+  const char* fn = "svdq_rmsnorm_quant_act";
+  REQUIRE_PTR(X); REQUIRE_PTR(codes); REQUIRE_PTR(scales);
+  if (residual) REQUIRE_PTR(H);
+  REQUIRE_ALIGNED(X); REQUIRE_ALIGNED(residual); REQUIRE_ALIGNED(H); REQUIRE_ALIGNED(gamma);
+  REQUIRE_ALIGNED(lambda); REQUIRE_ALIGNED(lora_down); REQUIRE_ALIGNED(codes);
+  TRY(check_rows(fn, "M", M, 1));
+  TRY(check_k(fn, K));
+  TRY(check_ld(fn, "ldx", ldx, K));
+  if (residual) {
+    TRY(check_ld(fn, "ldr", ldr, K));
+    TRY(check_ld(fn, "ldh", ldh, K));
+    if ((H == X && ldh != ldx) || (H == residual && ldh != ldr))
+      return fail(SVDQ_INVALID_ARG, "%s: H in place needs the leading dimension of its input", fn);
+  }
+  if (!(eps > 0.0f && eps < 1e30f))
+    return fail(SVDQ_INVALID_ARG, "%s: eps must be positive and finite", fn);
+  TRY(check_rank(fn, r));
+  if (r > 0) { REQUIRE_PTR(lora_down); REQUIRE_PTR(D); REQUIRE_ALIGNED(D); }
+  return hip_result(svdq::launch_norm_quant(X, M, K, ldx, residual, ldr, H, ldh, gamma, eps, lambda,
+                                            lora_down, r, codes, scales, D,
+                                            reinterpret_cast<hipStream_t>(stream)),
+                    fn);
+}
+
+svdq_status svdq_rope_axes(const uint16_t* X, int64_t M, int64_t ldx, int64_t heads, int64_t dim,
+                           const int32_t* pos, const double* freq, int64_t n_axes,
+                           const int64_t* axis_dims, int interleaved, int inverse, uint16_t* Y,
+                           int64_t ldy, svdq_stream_t stream) {
+  const char* fn = "svdq_rope_axes";
+  REQUIRE_PTR(X); REQUIRE_PTR(pos); REQUIRE_PTR(freq); REQUIRE_PTR(axis_dims); REQUIRE_PTR(Y);
+  REQUIRE_ALIGNED(X); REQUIRE_ALIGNED(Y); REQUIRE_ALIGNED(freq);
+  if (dim < 16 || dim > 256 || dim % 16 != 0)
+    return fail(SVDQ_UNSUPPORTED_SHAPE, "%s: dim=%lld must be a multiple of 16 in [16, 256]", fn,
+                (long long)dim);
+  if (heads < 1 || heads > (1 << 20))
+    return fail(SVDQ_UNSUPPORTED_SHAPE, "%s: heads=%lld must lie in [1, 2^20]", fn,
+                (long long)heads);
+  TRY(check_axes(fn, n_axes, axis_dims));
+  int64_t rot = 0;
+  int pairs[4] = {0, 0, 0, 0};
+  for (int64_t i = 0; i < n_axes; ++i) {
+    rot += axis_dims[i];
+    pairs[i] = (int)(axis_dims[i] / 2);
+  }
+  if (rot < 16 || rot > dim || rot % 16 != 0)
+    return fail(SVDQ_UNSUPPORTED_SHAPE,
+                "%s: the axes' dimensions add up to %lld, not a multiple of 16 in [16, dim=%lld]",
+                fn, (long long)rot, (long long)dim);
+  TRY(check_rows(fn, "M", M, 1));
+  TRY(check_ld(fn, "ldx", ldx, heads * dim));
+  TRY(check_ld(fn, "ldy", ldy, heads * dim));
+  if (X == Y && ldx != ldy)
+    return fail(SVDQ_INVALID_ARG, "%s: in place needs ldy == ldx", fn);
+  return hip_result(svdq::launch_rope(X, M, ldx, (int)heads, (int)dim, pos, freq, (int)n_axes,
+                                      pairs, interleaved != 0, inverse != 0, Y, ldy,
+                                      reinterpret_cast<hipStream_t>(stream)),
+                    fn);
+}
+
+svdq_status svdq_rope_frequencies(int64_t n_axes, const int64_t* axis_dims, double theta,
+                                  double* freq) {
+  const char* fn = "svdq_rope_frequencies";
+  REQUIRE_PTR(axis_dims); REQUIRE_PTR(freq);
+  TRY(check_axes(fn, n_axes, axis_dims));
+  if (!(theta > 1.0 && theta < 1e300))
+    return fail(SVDQ_INVALID_ARG, "%s: theta must be above 1 and finite", fn);
+  for (int64_t a = 0; a < n_axes; ++a)
+    for (int64_t j = 0; 2 * j < axis_dims[a]; ++j)
+      *freq++ = pow(theta, -2.0 * (double)j / (double)axis_dims[a]);
+  return ok();
+}
+
+svdq_status svdq_kv_write(const uint16_t* K, int64_t ldk, const uint16_t* V, int64_t ldv,
+                          int64_t rows, int64_t heads, int64_t dim, const int32_t* cu_rows,
+                          const int32_t* start, int64_t B, int64_t max_rows,
+                          const int32_t* block_table, int64_t max_blocks, int64_t n_pages,
+                          uint8_t* k_codes, uint8_t* v_codes, uint8_t* k_scales,
+                          uint8_t* v_scales, svdq_stream_t stream) {
+  const char* fn = "svdq_kv_write";
+  REQUIRE_PTR(K); REQUIRE_PTR(V); REQUIRE_PTR(start);
+  REQUIRE_ALIGNED(K); REQUIRE_ALIGNED(V);
+  TRY(check_cache(fn, heads, dim, cu_rows, B, rows, max_rows, block_table, max_blocks, n_pages,
+                  k_codes, v_codes, k_scales, v_scales));
+  TRY(check_ld(fn, "ldk", ldk, heads * dim));
+  TRY(check_ld(fn, "ldv", ldv, heads * dim));
+  if (rows == 0 || max_rows == 0) return ok();
+  return hip_result(svdq::launch_kv_write(K, ldk, V, ldv, rows, (int)heads, (int)dim, cu_rows,
+                                          start, B, max_rows, block_table, max_blocks, n_pages,
+                                          k_codes, v_codes, k_scales, v_scales,
+                                          reinterpret_cast<hipStream_t>(stream)),
+                    fn);
+}
+
+svdq_status svdq_kv_read(uint16_t* K, int64_t ldk, uint16_t* V, int64_t ldv, int64_t rows,
+                         int64_t heads, int64_t dim, const int32_t* cu_rows, const int32_t* start,
+                         int64_t B, int64_t max_rows, const int32_t* block_table,
+                         int64_t max_blocks, int64_t n_pages, const uint8_t* k_codes,
+                         const uint8_t* v_codes, const uint8_t* k_scales, const uint8_t* v_scales,
+                         svdq_stream_t stream) {
+  const char* fn = "svdq_kv_read";
+  REQUIRE_PTR(K); REQUIRE_PTR(V); REQUIRE_PTR(start);
+  REQUIRE_ALIGNED(K); REQUIRE_ALIGNED(V);
+  TRY(check_cache(fn, heads, dim, cu_rows, B, rows, max_rows, block_table, max_blocks, n_pages,
+                  k_codes, v_codes, k_scales, v_scales));
+  TRY(check_ld(fn, "ldk", ldk, heads * dim));
+  TRY(check_ld(fn, "ldv", ldv, heads * dim));
+  if (rows == 0 || max_rows == 0) return ok();
+  return hip_result(svdq::launch_kv_read(K, ldk, V, ldv, rows, (int)heads, (int)dim, cu_rows, start,
+                                         B, max_rows, block_table, max_blocks, n_pages, k_codes,
+                                         v_codes, k_scales, v_scales,
+                                         reinterpret_cast<hipStream_t>(stream)),
+                    fn);
+}
+
+int64_t svdq_attn_kv8_workspace_bytes(int64_t rows, int64_t q_heads, int64_t kv_heads,
+                                      int64_t dim, int64_t B, int64_t max_rows, int64_t max_kv) {
+  if (rows < 0 || kv_heads < 1 || q_heads < kv_heads || q_heads % kv_heads != 0 ||
+      q_heads > 65535 || (dim != 64 && dim != 128) || B < 1 || B > 65535 || max_rows < 0 ||
+      max_kv < 0 || rows > INT32_MAX || max_rows > INT32_MAX || max_kv > INT32_MAX)
+    return -1;
+  return svdq::attn_workspace_bytes(rows, q_heads, kv_heads, dim, B, max_rows, max_kv);
+}
+
+svdq_status svdq_attn_kv8(const uint16_t* Q, int64_t ldq, int64_t rows, int64_t q_heads,
+                          int64_t kv_heads, int64_t dim, const int32_t* cu_rows,
+                          const int32_t* kv_len, int64_t B, int64_t max_rows, int64_t max_kv,
+                          const int32_t* block_table, int64_t max_blocks, int64_t n_pages,
+                          const uint8_t* k_codes, const uint8_t* v_codes, const uint8_t* k_scales,
+                          const uint8_t* v_scales, float scale, int causal, uint16_t* O,
+                          int64_t ldo, float* lse, void* workspace, int64_t workspace_bytes,
+                          svdq_stream_t stream) {
+  const char* fn = "svdq_attn_kv8";
+  REQUIRE_PTR(Q); REQUIRE_PTR(O); REQUIRE_PTR(kv_len);
+  REQUIRE_ALIGNED(Q); REQUIRE_ALIGNED(O); REQUIRE_ALIGNED(lse);
+  TRY(check_cache(fn, kv_heads, dim, cu_rows, B, rows, max_rows, block_table, max_blocks, n_pages,
+                  k_codes, v_codes, k_scales, v_scales));
+  if (q_heads < kv_heads || q_heads % kv_heads != 0 || q_heads > 65535)
+    return fail(SVDQ_UNSUPPORTED_SHAPE,
+                "%s: q_heads=%lld must be a multiple of kv_heads=%lld, at most 65535", fn,
+                (long long)q_heads, (long long)kv_heads);
+  TRY(check_ld(fn, "ldq", ldq, q_heads * dim));
+  TRY(check_ld(fn, "ldo", ldo, q_heads * dim));
+  if (max_kv < 0 || max_kv > INT32_MAX)
+    return fail(SVDQ_INVALID_ARG, "%s: max_kv=%lld must lie in [0, 2^31)", fn, (long long)max_kv);
+  if (!(scale > 0.0f && scale < 1e30f))
+    return fail(SVDQ_INVALID_ARG, "%s: scale must be positive and finite", fn);
+  if (Q == O) return fail(SVDQ_INVALID_ARG, "%s: O must not be Q", fn);
+  if (rows == 0 || max_rows == 0) return ok();
+  const int64_t need =
+      svdq::attn_workspace_bytes(rows, q_heads, kv_heads, dim, B, max_rows, max_kv);
+  if (need > 0) {
+    REQUIRE_PTR(workspace);
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+      return fail(SVDQ_UNSUPPORTED_SHAPE, "%s: workspace must be 256-byte aligned", fn);
+    if (workspace_bytes < need)
+      return fail(SVDQ_UNSUPPORTED_SHAPE, "%s: workspace of %lld bytes, needs %lld", fn,
+                  (long long)workspace_bytes, (long long)need);
+  }
+  if (svdq::attn_blocks(q_heads, kv_heads, B, max_rows, max_kv) > INT32_MAX)
+    return fail(SVDQ_UNSUPPORTED_SHAPE, "%s: more than 2^31 blocks of rows and heads", fn);
+  return hip_result(svdq::launch_attn(Q, ldq, rows, q_heads, kv_heads, dim, cu_rows, kv_len, B,
+                                      max_rows, max_kv, block_table, max_blocks, n_pages, k_codes,
+                                      v_codes, k_scales, v_scales, scale, causal != 0, O, ldo, lse,
+                                      workspace, reinterpret_cast<hipStream_t>(stream)),
                     fn);
 }
 

@@ -127,4 +127,39 @@ hipError_t launch_lambda_search(const uint16_t* X, int64_t M, int64_t ldx, const
                                 uint16_t* best_down, uint16_t* best_up, void* workspace,
                                 hipStream_t s);
 
+
+// Residual, RMS norm, smoothing, MXFP8 codes and the low-rank down-projection of each row.
+hipError_t launch_norm_quant(const uint16_t* X, int64_t M, int64_t K, int64_t ldx,
+                             const uint16_t* residual, int64_t ldr, uint16_t* H, int64_t ldh,
+                             const uint16_t* gamma, float eps, const float* lambda,
+                             const uint16_t* down, int64_t r, uint8_t* codes, uint8_t* scales,
+                             float* D, hipStream_t s);
+
+// Rotary positions; pairs: rotary pairs of each axis (n_axes entries).
+hipError_t launch_rope(const uint16_t* X, int64_t M, int64_t ldx, int heads, int dim,
+                       const int32_t* pos, const double* freq, int n_axes, const int* pairs,
+                       int interleaved, int inverse, uint16_t* Y, int64_t ldy, hipStream_t s);
+
+// The paged 8-bit cache (layout in kv_layout.h; dim 64 or 128).
+hipError_t launch_kv_write(const uint16_t* K, int64_t ldk, const uint16_t* V, int64_t ldv,
+                           int64_t rows, int heads, int dim, const int32_t* cu,
+                           const int32_t* start, int64_t B, int64_t max_new, const int32_t* table,
+                           int64_t max_blocks, int64_t n_pages, uint8_t* kc, uint8_t* vc,
+                           uint8_t* ks, uint8_t* vs, hipStream_t s);
+hipError_t launch_kv_read(uint16_t* K, int64_t ldk, uint16_t* V, int64_t ldv, int64_t rows,
+                          int heads, int dim, const int32_t* cu, const int32_t* start, int64_t B,
+                          int64_t max_n, const int32_t* table, int64_t max_blocks,
+                          int64_t n_pages, const uint8_t* kc, const uint8_t* vc,
+                          const uint8_t* ks, const uint8_t* vs, hipStream_t s);
+int64_t attn_workspace_bytes(int64_t rows, int64_t Hq, int64_t Hkv, int64_t dim, int64_t B,
+                             int64_t max_q, int64_t max_kv);
+// Blocks of the launch; at most 2^31.
+int64_t attn_blocks(int64_t Hq, int64_t Hkv, int64_t B, int64_t max_q, int64_t max_kv);
+hipError_t launch_attn(const uint16_t* Q, int64_t ldq, int64_t rows, int64_t Hq, int64_t Hkv,
+                       int64_t dim, const int32_t* cu, const int32_t* len, int64_t B,
+                       int64_t max_q, int64_t max_kv, const int32_t* table, int64_t max_blocks,
+                       int64_t n_pages, const uint8_t* kc, const uint8_t* vc, const uint8_t* ks,
+                       const uint8_t* vs, float scale, int causal, uint16_t* O, int64_t ldo,
+                       float* lse, void* workspace, hipStream_t s);
+
 }  // namespace svdq

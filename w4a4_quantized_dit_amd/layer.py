@@ -245,3 +245,115 @@ def forward(X, pw, act_amax, lam, lora_down, out=None):
     codes, scales, g, D = quantize_activation(X2, lam, act_amax, lora_down, pw.fmt)
     Y = gemm(codes, scales, g, D, pw, X2.shape[0], out=out)
     return Y.reshape(*lead, pw.N)
+
+
+# ------------------------------------------------------------------------------------------
+# the attention half of the block
+# ------------------------------------------------------------------------------------------
+
+KV_PAGE = 64   # tokens of a cache page
+
+
+def norm_quantize_activation(X, gamma, lam, lora_down, eps=1e-6, residual=None, out_residual=None):
+    """MXFP8 activations (codes, scales, D, H) of the RMS norm of X + residual, [M, K] bf16:
+    what gemm() of an MXFP8 weight takes, and the new residual stream H (X itself without a
+    residual).  out_residual: where H goes (X or residual: in place)."""
+    torch = _torch()
+    M, K = X.shape
+    r = 0 if lora_down is None else lora_down.shape[0]
+    dev = X.device
+    codes = torch.empty(M, K, dtype=torch.uint8, device=dev)
+    scales = torch.empty(M, K // 32, dtype=torch.uint8, device=dev)
+    D = torch.empty(M, r, dtype=torch.float32, device=dev) if r else None
+    H = X
+    if residual is not None:
+        H = out_residual if out_residual is not None else torch.empty(M, K, dtype=X.dtype,
+                                                                      device=dev)
+    _lib.svdq_rmsnorm_quant_act(X, residual, H if residual is not None else None, gamma, eps, lam,
+                                lora_down, r, codes, scales, D)
+    return codes, scales, D, H
+
+
+def rope_frequencies(axis_dims, theta=10000.0, device="cuda"):
+    """Frequencies of rope(): device float64 [sum(axis_dims) / 2]."""
+    torch = _torch()
+    return torch.from_numpy(_lib.svdq_rope_frequencies(axis_dims, theta)).to(device)
+
+
+def rope(X, pos, freq, axis_dims, dim, interleaved=True, inverse=False, out=None):
+    """Rotary positions of the heads of X [M, heads·dim] bf16; pos int32 [M, axes] (time, height,
+    width of every row), freq from rope_frequencies.  out=X turns in place."""
+    torch = _torch()
+    Y = out if out is not None else torch.empty(X.shape, dtype=X.dtype, device=X.device)
+    _lib.svdq_rope_axes(X, X.shape[1] // dim, dim, pos, freq, axis_dims, interleaved, inverse, Y)
+    return Y
+
+
+@dataclass
+class KVCache:
+    k_codes: object      # uint8 [pages, heads, 64·dim], operand order (include/svdq.h)
+    v_codes: object
+    k_scales: object     # uint8 [pages, heads]: the page's exponent + 127
+    v_scales: object
+    dim: int
+
+
+def kv_cache(n_pages, heads, dim, device="cuda"):
+    """An empty paged 8-bit cache of n_pages pages of 64 tokens."""
+    torch = _torch()
+    codes = [torch.zeros(n_pages, heads, KV_PAGE * dim, dtype=torch.uint8, device=device)
+             for _ in range(2)]
+    scales = [torch.zeros(n_pages, heads, dtype=torch.uint8, device=device) for _ in range(2)]
+    return KVCache(codes[0], codes[1], scales[0], scales[1], dim)
+
+
+def kv_write(cache, K, V, block_table, cu_rows, start, max_rows):
+    """Append the packed rows K, V [rows, heads·dim] bf16: sequence b's rows cu_rows[b] ..
+    cu_rows[b + 1] become its tokens start[b] onward, quantised with one scale a page and head."""
+    _lib.svdq_kv_write(K, V, cache.dim, cu_rows, start, max_rows, block_table, cache.k_codes,
+                       cache.v_codes, cache.k_scales, cache.v_scales)
+
+
+def kv_read(cache, block_table, cu_rows, start, rows, max_rows, out=None):
+    """(K, V) [rows, heads·dim] bf16 of tokens start[b] onward of each sequence."""
+    torch = _torch()
+    if out is None:
+        shape = (rows, cache.k_codes.shape[1] * cache.dim)
+        out = [torch.empty(shape, dtype=torch.bfloat16, device=cache.k_codes.device)
+               for _ in range(2)]
+    _lib.svdq_kv_read(out[0], out[1], cache.dim, cu_rows, start, max_rows, block_table,
+                      cache.k_codes, cache.v_codes, cache.k_scales, cache.v_scales)
+    return out[0], out[1]
+
+
+def attention_workspace(rows, q_heads, kv_heads, dim, B, max_rows, max_kv, device="cuda"):
+    """A workspace for attention() of these sizes (None when none is needed)."""
+    torch = _torch()
+    nb = _lib.svdq_attn_kv8_workspace_bytes(rows, q_heads, kv_heads, dim, B, max_rows, max_kv)
+    if nb < 0:
+        raise ValueError("unsupported attention shape")
+    if nb == 0:
+        return None
+    buf = torch.empty(nb + 256, dtype=torch.uint8, device=device)
+    off = (-buf.data_ptr()) % 256
+    return buf[off:off + nb]
+
+
+def attention(Q, cache, block_table, cu_rows, kv_len, max_rows, max_kv, scale=None, causal=False,
+              out=None, workspace=None, return_lse=False):
+    """softmax(scale·Q·Kᵀ)·V of Q [rows, q_heads·dim] bf16 over the cached tokens [0, kv_len[b]) of
+    each sequence (causal: row i of n sees kv_len − n + i + 1 of them); scale defaults to
+    dim^−1/2.  Returns O, or (O, lse) with lse fp32 [rows, q_heads]."""
+    torch = _torch()
+    dim, heads = cache.dim, cache.k_codes.shape[1]
+    rows, q_heads = Q.shape[0], Q.shape[1] // dim
+    O = out if out is not None else torch.empty(rows, q_heads * dim, dtype=torch.bfloat16,
+                                                device=Q.device)
+    lse = torch.empty(rows, q_heads, dtype=torch.float32, device=Q.device) if return_lse else None
+    if workspace is None:
+        workspace = attention_workspace(rows, q_heads, heads, dim, block_table.shape[0], max_rows,
+                                        max_kv, Q.device)
+    _lib.svdq_attn_kv8(Q, dim, cu_rows, kv_len, max_rows, max_kv, block_table, cache.k_codes,
+                       cache.v_codes, cache.k_scales, cache.v_scales,
+                       dim ** -0.5 if scale is None else scale, causal, O, lse, workspace)
+    return (O, lse) if return_lse else O
