@@ -139,13 +139,35 @@ __device__ __forceinline__ float other_half(float x) {
   return __shfl_xor(x, 32);
 }
 
-// One page for the wave's 32 rows.  kf(i) / vf(i): the lane's 16 bytes of K / V fragment i.
-// lim: tokens of this page the lane's row sees (>= 64 when all); lim_kv: tokens of the page
-// that exist.
-template <int DIM, class KF, class VF>
+// Eight codes of V, widened exactly with the page's scale: one lane's part of a 16-token step.
+__device__ __forceinline__ bf16x8_t widen8(uint32_t lo, uint32_t hi, float scale) {
+  const bf16x2_t a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, false);
+  const bf16x2_t b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, true);
+  const bf16x2_t c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, false);
+  const bf16x2_t d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, true);
+  return bf16x8_t{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+// A lane's 16 bytes of a V fragment (tokens 32·tb on) without the slots past the page's n tokens,
+// which may hold any byte, NaN codes among them.
+__device__ __forceinline__ u32x4_t drop_slots(u32x4_t v, int tb, int half, int n) {
+#pragma unroll
+  for (int d = 0; d < 4; ++d) {
+    int k = n - (32 * tb + 16 * (d >> 1) + 8 * (d & 1) + 4 * half);
+    k = k < 0 ? 0 : (k > 4 ? 4 : k);
+    v[d] &= (uint32_t)((1ull << (8 * k)) - 1ull);
+  }
+  return v;
+}
+
+// One page for the wave's 32 rows.  kf(i): the lane's 16 bytes of K fragment i; vf(j, tb, g): its
+// V operand of channels 32j on and tokens 32·tb + 16·g on.  EDGE: some row does not see the whole
+// page; lim is the number of its tokens that the lane's row sees.  (Two instances rather than
+// branches inside: the many small blocks that those leave kept the matrix and vector instructions
+// of the common pages from overlapping.)
+template <int DIM, bool EDGE, class KF, class VF>
 __device__ __forceinline__ void page_step(State<DIM>& st, const QueryOp<DIM>& q, float c, int k_exp,
-                                          int v_exp, bool masked, int lim, int lim_kv, int half,
-                                          KF kf, VF vf) {
+                                          int lim, int half, KF kf, VF vf) {
   f32x16_t z[2];
 #pragma unroll
   for (int tb = 0; tb < 2; ++tb) {
@@ -162,7 +184,7 @@ __device__ __forceinline__ void page_step(State<DIM>& st, const QueryOp<DIM>& q,
                                                               q.s_lo);
     }
   }
-  if (masked) {
+  if (EDGE) {
 #pragma unroll
     for (int tb = 0; tb < 2; ++tb)
 #pragma unroll
@@ -197,29 +219,14 @@ __device__ __forceinline__ void page_step(State<DIM>& st, const QueryOp<DIM>& q,
       }
       p[2 * tb + g] = __builtin_bit_cast(bf16x8_t, w);
     }
-  const float vscale = two_to(v_exp - 127);
 #pragma unroll
   for (int j = 0; j < DIM / 32; ++j)
 #pragma unroll
-    for (int tb = 0; tb < 2; ++tb) {
-      u32x4_t v = vf(2 * j + tb);
-      if (lim_kv < kPage) {  // slots that hold no token may hold any byte
+    for (int tb = 0; tb < 2; ++tb)
 #pragma unroll
-        for (int d = 0; d < 4; ++d) {
-          const int n = lim_kv - (32 * tb + 16 * (d >> 1) + 8 * (d & 1) + 4 * half);
-          v[d] = n <= 0 ? 0u : (n >= 4 ? v[d] : v[d] & ((1u << (8 * n)) - 1u));
-        }
-      }
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        const bf16x2_t b0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[2 * g], vscale, false);
-        const bf16x2_t b1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[2 * g], vscale, true);
-        const bf16x2_t b2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[2 * g + 1], vscale, false);
-        const bf16x2_t b3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[2 * g + 1], vscale, true);
-        const bf16x8_t vo = {b0[0], b0[1], b1[0], b1[1], b2[0], b2[1], b3[0], b3[1]};
-        st.o[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vo, p[2 * tb + g], st.o[j], 0, 0, 0);
-      }
-    }
+      for (int g = 0; g < 2; ++g)
+        st.o[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf(j, tb, g), p[2 * tb + g], st.o[j], 0,
+                                                          0, 0);
 }
 
 // The lane's page number and exponent bytes of logical page `at` (k | v << 8), page -1 outside
@@ -272,16 +279,19 @@ __device__ __forceinline__ void store_row(const AttnArgs& a, const State<DIM>& s
         l > 0.0f ? 0.6931471805599453f * (st.m + __builtin_amdgcn_logf(l)) : -__builtin_inff();
 }
 
-// Many rows: four waves of 32 rows share each page through a ring of three LDS images, filled
-// by asynchronous copies two pages ahead.
+// Many rows: four waves of 32 rows share each page through LDS.  K's codes are copied there as
+// they are, asynchronously, one page ahead.  V's go through registers two pages ahead and are
+// widened to bf16 on the way, once for the four waves (each wave widening all of them for itself
+// took a third of its vector instructions).  Two images of each, one barrier a page.
 constexpr int kTileWaves = 4;
 constexpr int kTileRows = 32 * kTileWaves;
 
 template <int DIM>
 __global__ __launch_bounds__(64 * kTileWaves, 2) void k_attn_tile(AttnArgs a) {
   constexpr int kBytes = kPage * DIM;                       // one tensor's page
-  constexpr int kCopies = 2 * kBytes / 1024 / kTileWaves;   // per wave and page
-  __shared__ __attribute__((aligned(16))) uint8_t img[3][2 * kBytes];
+  constexpr int kCopies = kBytes / 1024 / kTileWaves;       // fragments per wave, K and V each
+  __shared__ __attribute__((aligned(16))) uint8_t k_img[2][kBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t v_img[2][2 * kBytes];
   const int64_t total = (int64_t)a.B * a.Hkv * a.splits * a.tiles;
   const int64_t per_xcd = (total + 7) / 8;
   const int64_t item = (int64_t)(blockIdx.x % 8) * per_xcd + blockIdx.x / 8;
@@ -313,16 +323,37 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void k_attn_tile(AttnArgs a) {
   State<DIM> st;
   state_init(st);
 
-  const int64_t head_off = (int64_t)s.h * kBytes, page_bytes = (int64_t)a.Hkv * kBytes;
-  auto issue = [&](int page, int slot) {
-    const int64_t at = (int64_t)(page < 0 ? 0 : page) * page_bytes + head_off;
+  const int64_t head_off = (int64_t)s.h * kBytes + lane * 16;
+  const int64_t page_bytes = (int64_t)a.Hkv * kBytes;
+  auto copy_k = [&](int page, int slot) {
+    const uint8_t* src = a.kc + (int64_t)(page < 0 ? 0 : page) * page_bytes + head_off;
 #pragma unroll
     for (int i = 0; i < kCopies; ++i) {
-      const int f = wave * kCopies + i;  // 1 KB piece: K's first, then V's
-      const uint8_t* src = f < kBytes / 1024 ? a.kc + at + f * 1024
-                                             : a.vc + at + (f - kBytes / 1024) * 1024;
-      __builtin_amdgcn_global_load_lds((gvoid_t*)(src + lane * 16),
-                                       (lvoid_t*)(&img[slot][f * 1024]), 16, 0, 0);
+      const int f = wave * kCopies + i;
+      __builtin_amdgcn_global_load_lds((gvoid_t*)(src + f * 1024),
+                                       (lvoid_t*)(&k_img[slot][f * 1024]), 16, 0, 0);
+    }
+  };
+  u32x4_t vr[kCopies];
+  auto load_v = [&](int page) {
+    const uint8_t* src = a.vc + (int64_t)(page < 0 ? 0 : page) * page_bytes + head_off;
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i)
+      vr[i] = *reinterpret_cast<const u32x4_t*>(src + (wave * kCopies + i) * 1024);
+  };
+  // fragment f: its two 16-token steps of 1 KB each
+  auto widen_v = [&](int64_t at, int exps, int slot) {
+    const float scale = two_to((exps >> 8) - 127);
+    const int64_t left = s.kv - at * kPage;
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i) {
+      const int f = wave * kCopies + i;
+      u32x4_t v = vr[i];
+      if (left < kPage) v = drop_slots(v, f & 1, half, (int)left);
+#pragma unroll
+      for (int g = 0; g < 2; ++g)
+        *reinterpret_cast<bf16x8_t*>(&v_img[slot][(2 * f + g) * 1024 + lane * 16]) =
+            widen8(v[2 * g], v[2 * g + 1], scale);
     }
   };
 
@@ -335,8 +366,16 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void k_attn_tile(AttnArgs a) {
     const int d = (int)(i - g0);
     return d < 64 ? __builtin_amdgcn_readlane(cur, d) : __builtin_amdgcn_readlane(nxt, d - 64);
   };
-  if (p0 < p1) issue(page_at(p0), 0);
-  if (p0 + 1 < p1) issue(page_at(p0 + 1), 1);
+  auto exps_at = [&](int64_t i) {
+    const int d = (int)(i - g0);
+    return d < 64 ? __builtin_amdgcn_readlane(cur_e, d) : __builtin_amdgcn_readlane(nxt_e, d - 64);
+  };
+  if (p0 < p1) {
+    copy_k(page_at(p0), 0);
+    load_v(page_at(p0));
+    widen_v(p0, exps_at(p0), 0);
+    if (p0 + 1 < p1) load_v(page_at(p0 + 1));
+  }
   int slot = 0;
   for (int64_t i = p0; i < p1; ++i) {
     if (i - g0 == 64) {
@@ -344,31 +383,32 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void k_attn_tile(AttnArgs a) {
       cur = nxt;
       cur_e = nxt_e;
       page_meta(a, s, g0 + 64 + lane, p1, nxt, nxt_e);
-      wait_vmcnt<0>();
     }
-    if (i + 1 < p1)
-      wait_vmcnt<kCopies>();
-    else
-      wait_vmcnt<0>();
-    // every wave's copies of this page have landed, and every wave is done with the page before
+    // page i has landed in LDS for every wave, and every wave is done with page i - 1
+    wait_vmcnt<0>();
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    if (i + 2 < p1) issue(page_at(i + 2), slot == 0 ? 2 : slot - 1);
+    if (i + 1 < p1) {
+      copy_k(page_at(i + 1), slot ^ 1);
+      widen_v(i + 1, exps_at(i + 1), slot ^ 1);
+      if (i + 2 < p1) load_v(page_at(i + 2));
+    }
     const int page = __builtin_amdgcn_readlane(cur, (int)(i - g0));
     const int64_t t0 = i * kPage;
     if (page >= 0 && t0 < lim_last) {
-      const int exps = __builtin_amdgcn_readlane(cur_e, (int)(i - g0));
-      const uint8_t* k = img[slot];
-      const bool masked = t0 + kPage > lim_first;
-      const int64_t lr = lim_row - t0, lk = s.kv - t0;
-      page_step<DIM>(
-          st, q, a.c, exps & 255, exps >> 8, masked, (int)(lr > kPage ? kPage : lr),
-          (int)(lk > kPage ? kPage : lk), half,
-          [&](int f) { return *reinterpret_cast<const u32x4_t*>(k + f * 1024 + lane * 16); },
-          [&](int f) {
-            return *reinterpret_cast<const u32x4_t*>(k + kBytes + f * 1024 + lane * 16);
-          });
+      const int k_exp = __builtin_amdgcn_readlane(cur_e, (int)(i - g0)) & 255;
+      const uint8_t *k = k_img[slot] + lane * 16, *v = v_img[slot] + lane * 16;
+      auto kf = [&](int f) { return *reinterpret_cast<const u32x4_t*>(k + f * 1024); };
+      auto vf = [&](int j, int tb, int g) {
+        return *reinterpret_cast<const bf16x8_t*>(v + ((2 * j + tb) * 2 + g) * 1024);
+      };
+      if (t0 + kPage <= lim_first) {
+        page_step<DIM, false>(st, q, a.c, k_exp, kPage, half, kf, vf);
+      } else {
+        const int64_t lr = lim_row - t0;
+        page_step<DIM, true>(st, q, a.c, k_exp, (int)(lr > kPage ? kPage : lr), half, kf, vf);
+      }
     }
-    slot = slot == 2 ? 0 : slot + 1;
+    slot ^= 1;
   }
   const float l = st.l + other_half(st.l);
   if (live) store_row<DIM>(a, st, l, s.first + tok, head, split, half);
@@ -416,11 +456,19 @@ __global__ __launch_bounds__(256, 2) void k_attn_few(AttnArgs a) {
 #pragma unroll
       for (int f = 0; f < kFrags; ++f) vr[f] = *reinterpret_cast<const u32x4_t*>(a.vc + at + f * 1024);
       const int64_t t0 = (g0 + 4 * d) * kPage;
-      const int64_t lr = lim_row - t0, lk = s.kv - t0;
-      page_step<DIM>(
-          st, q, a.c, exps & 255, exps >> 8, t0 + kPage > lim_first,
-          (int)(lr > kPage ? kPage : lr), (int)(lk > kPage ? kPage : lk), half,
-          [&](int f) { return kr[f]; }, [&](int f) { return vr[f]; });
+      const float scale = two_to((exps >> 8) - 127);
+      auto kf = [&](int f) { return kr[f]; };
+      auto vf = [&](int j, int tb, int g) {
+        return widen8(vr[2 * j + tb][2 * g], vr[2 * j + tb][2 * g + 1], scale);
+      };
+      if (t0 + kPage <= lim_first) {
+        page_step<DIM, false>(st, q, a.c, exps & 255, kPage, half, kf, vf);
+      } else {
+        const int64_t lr = lim_row - t0, lk = s.kv - t0;
+#pragma unroll
+        for (int f = 0; f < kFrags; ++f) vr[f] = drop_slots(vr[f], f & 1, half, (int)(lk > kPage ? kPage : lk));
+        page_step<DIM, true>(st, q, a.c, exps & 255, (int)(lr > kPage ? kPage : lr), half, kf, vf);
+      }
     }
   }
   // join the four waves
