@@ -897,6 +897,8 @@ svdq_status svdq_attn_kv8(const uint16_t* Q, int64_t ldq, int64_t rows, int64_t 
   if (!(scale > 0.0f && scale < 1e30f))
     return fail(SVDQ_INVALID_ARG, "%s: scale must be positive and finite", fn);
   if (Q == O) return fail(SVDQ_INVALID_ARG, "%s: O must not be Q", fn);
+  if (max_rows * (q_heads / kv_heads) > INT32_MAX - 256 || rows * (q_heads / kv_heads) > INT32_MAX - 256)
+    return fail(SVDQ_UNSUPPORTED_SHAPE, "%s: more than 2^31 rows of a key head", fn);
   if (rows == 0 || max_rows == 0) return ok();
   const int64_t need =
       svdq::attn_workspace_bytes(rows, q_heads, kv_heads, dim, B, max_rows, max_kv);

@@ -51,10 +51,11 @@ struct AttnArgs {
   float c;
 };
 
-// One sequence and key head of a block.
+// One sequence and key head of a block.  Tokens, rows and pages fit 32 bits (lengths are int32,
+// and the entry point bounds rows·G); addresses are formed in 64.
 struct Seq {
-  int64_t first;   // packed row of its first token
-  int64_t n, kv;   // query tokens, cached tokens
+  int first;   // packed row of its first token
+  int n, kv;   // query tokens, cached tokens
   int b, h;
 };
 
@@ -62,18 +63,19 @@ __device__ __forceinline__ bool sequence(const AttnArgs& a, int bh, Seq& s) {
   s.b = bh / a.Hkv;
   s.h = bh % a.Hkv;
   s.first = a.cu[s.b];
-  s.n = (int64_t)a.cu[s.b + 1] - s.first;
-  if (s.n <= 0 || s.first < 0 || s.first + s.n > a.rows) return false;
+  const int end = a.cu[s.b + 1];
+  if (s.first < 0 || end <= s.first || end > a.rows) return false;
+  s.n = end - s.first;
   s.kv = a.len[s.b];
   const int64_t room = a.max_blocks * kPage;
-  s.kv = s.kv < 0 ? 0 : (s.kv > room ? room : s.kv);
+  s.kv = s.kv < 0 ? 0 : (s.kv > room ? (int)room : s.kv);
   return true;
 }
 
 // Tokens [0, limit) are visible to query token i.
-__device__ __forceinline__ int64_t limit_of(const AttnArgs& a, const Seq& s, int64_t i) {
+__device__ __forceinline__ int limit_of(const AttnArgs& a, const Seq& s, int i) {
   if (!a.causal) return s.kv;
-  const int64_t v = s.kv - s.n + i + 1;
+  const int v = s.kv - s.n + i + 1;
   return v < 0 ? 0 : v;
 }
 
@@ -135,8 +137,11 @@ __device__ __forceinline__ void state_init(State<DIM>& st) {
   st.l = 0.0f;
 }
 
+// The value of the lane's partner in the other half (the same row).
 __device__ __forceinline__ float other_half(float x) {
-  return __shfl_xor(x, 32);
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false,
+                                                  false);
+  return __uint_as_float((threadIdx.x & 32) ? r[0] : r[1]);
 }
 
 // Eight codes of V, widened exactly with the page's scale: one lane's part of a 16-token step.
@@ -160,15 +165,10 @@ __device__ __forceinline__ u32x4_t drop_slots(u32x4_t v, int tb, int half, int n
   return v;
 }
 
-// One page for the wave's 32 rows.  kf(i): the lane's 16 bytes of K fragment i; vf(j, tb, g): its
-// V operand of channels 32j on and tokens 32·tb + 16·g on.  EDGE: some row does not see the whole
-// page; lim is the number of its tokens that the lane's row sees.  (Two instances rather than
-// branches inside: the many small blocks that those leave kept the matrix and vector instructions
-// of the common pages from overlapping.)
-template <int DIM, bool EDGE, class KF, class VF>
-__device__ __forceinline__ void page_step(State<DIM>& st, const QueryOp<DIM>& q, float c, int k_exp,
-                                          int lim, int half, KF kf, VF vf) {
-  f32x16_t z[2];
+// Scores Sᵀ of a page: token blocks of 32, lane column = row, registers = tokens
+// 8(i/4) + 4·half + i%4.  kf(i): the lane's 16 bytes of K fragment i.
+template <int DIM, class KF>
+__device__ __forceinline__ void scores(f32x16_t (&z)[2], const QueryOp<DIM>& q, int k_exp, KF kf) {
 #pragma unroll
   for (int tb = 0; tb < 2; ++tb) {
 #pragma unroll
@@ -184,17 +184,41 @@ __device__ __forceinline__ void page_step(State<DIM>& st, const QueryOp<DIM>& q,
                                                               q.s_lo);
     }
   }
-  if (EDGE) {
+}
+
+// Scores of the tokens that the lane's row does not see (lim and later) become −inf.
+__device__ __forceinline__ void hide(f32x16_t (&z)[2], int lim, int half) {
+  lim -= 4 * half;  // the registers' tokens are then constants
 #pragma unroll
-    for (int tb = 0; tb < 2; ++tb)
+  for (int tb = 0; tb < 2; ++tb)
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (32 * tb + 8 * (i >> 2) + 4 * half + (i & 3) >= lim) z[tb][i] = -__builtin_inff();
+    for (int i = 0; i < 16; ++i)
+      if (32 * tb + 8 * (i >> 2) + (i & 3) >= lim) z[tb][i] = -__builtin_inff();
+}
+
+// The larger of the two halves' values.
+__device__ __forceinline__ float across(float m) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(m), __float_as_uint(m), false,
+                                                  false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
+// The page's largest score of the lane's row, in log2 units.
+__device__ __forceinline__ float largest(const f32x16_t (&z)[2], float c) {
+  float t[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    t[k] = fmaxf(z[k >> 1][8 * (k & 1)], z[k >> 1][8 * (k & 1) + 1]);
+#pragma unroll
+    for (int i = 2; i < 8; i += 2)
+      t[k] = fmaxf(fmaxf(t[k], z[k >> 1][8 * (k & 1) + i]), z[k >> 1][8 * (k & 1) + i + 1]);
   }
-  float top = fmaxf(z[0][0], z[1][0]);
-#pragma unroll
-  for (int i = 1; i < 16; ++i) top = fmaxf(fmaxf(top, z[0][i]), z[1][i]);
-  top = fmaxf(top, other_half(top)) * c;
+  return across(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]))) * c;
+}
+
+// Raises the running maximum to the page's where some row needs it.
+template <int DIM>
+__device__ __forceinline__ void raise(State<DIM>& st, float top) {
   if (__builtin_amdgcn_ballot_w64(top > st.m + kRaise) != 0) {
     const float m = fmaxf(st.m, top), f = __builtin_amdgcn_exp2f(st.m - m);
 #pragma unroll
@@ -204,43 +228,37 @@ __device__ __forceinline__ void page_step(State<DIM>& st, const QueryOp<DIM>& q,
     st.l *= f;
     st.m = m;
   }
-  bf16x8_t p[4];
-#pragma unroll
-  for (int tb = 0; tb < 2; ++tb)
-#pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      u32x4_t w;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(z[tb][8 * g + 2 * j], c, -st.m));
-        const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(z[tb][8 * g + 2 * j + 1], c, -st.m));
-        st.l += x + y;
-        w[j] = pack_bf16x2(x, y);
-      }
-      p[2 * tb + g] = __builtin_bit_cast(bf16x8_t, w);
-    }
-#pragma unroll
-  for (int j = 0; j < DIM / 32; ++j)
-#pragma unroll
-    for (int tb = 0; tb < 2; ++tb)
-#pragma unroll
-      for (int g = 0; g < 2; ++g)
-        st.o[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf(j, tb, g), p[2 * tb + g], st.o[j], 0,
-                                                          0, 0);
 }
 
-// The lane's page number and exponent bytes of logical page `at` (k | v << 8), page -1 outside
-// the table's range or the cache.
-__device__ __forceinline__ void page_meta(const AttnArgs& a, const Seq& s, int64_t at, int64_t end,
+// Weights of 16 tokens (step g of token block tb) as an operand of the product with V.
+template <int DIM>
+__device__ __forceinline__ bf16x8_t weights(State<DIM>& st, const f32x16_t (&z)[2], int tb, int g,
+                                            float c) {
+  u32x4_t w;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(z[tb][8 * g + 2 * j], c, -st.m));
+    const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(z[tb][8 * g + 2 * j + 1], c, -st.m));
+    st.l += x + y;
+    w[j] = pack_bf16x2(x, y);
+  }
+  return __builtin_bit_cast(bf16x8_t, w);
+}
+
+constexpr int kPresent = 1 << 16;
+
+// The lane's page number and exponent bytes (k | v << 8 | kPresent) of logical page `at`; page 0
+// and no flag outside [0, end) or the cache.
+__device__ __forceinline__ void page_meta(const AttnArgs& a, const Seq& s, int at, int end,
                                           int& page, int& exps) {
-  page = -1;
+  page = 0;
   exps = 0;
   if (at < end) {
     const int p = a.table[(int64_t)s.b * a.max_blocks + at];
     if (p >= 0 && p < a.n_pages) {
       page = p;
       const int64_t i = (int64_t)p * a.Hkv + s.h;
-      exps = (int)a.ks[i] | (int)a.vs[i] << 8;
+      exps = (int)a.ks[i] | (int)a.vs[i] << 8 | kPresent;
     }
   }
 }
@@ -290,7 +308,9 @@ template <int DIM>
 __global__ __launch_bounds__(64 * kTileWaves, 2) void k_attn_tile(AttnArgs a) {
   constexpr int kBytes = kPage * DIM;                       // one tensor's page
   constexpr int kCopies = kBytes / 1024 / kTileWaves;       // fragments per wave, K and V each
-  __shared__ __attribute__((aligned(16))) uint8_t k_img[2][kBytes];
+  // (arrays of their own: the compiler then sees that the copy into one K image does not touch
+  // the reads of the other, and does not wait for it in front of them)
+  __shared__ __attribute__((aligned(16))) uint8_t k_img0[kBytes], k_img1[kBytes];
   __shared__ __attribute__((aligned(16))) uint8_t v_img[2][2 * kBytes];
   const int64_t total = (int64_t)a.B * a.Hkv * a.splits * a.tiles;
   const int64_t per_xcd = (total + 7) / 8;
@@ -301,114 +321,197 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void k_attn_tile(AttnArgs a) {
   const int split = (int)((item / a.tiles) % a.splits);
   Seq s;
   if (!sequence(a, (int)(item / a.tiles / a.splits), s)) return;
-  const int64_t R = s.n * a.G, r0 = (int64_t)tile * kTileRows;
+  const int R = s.n * a.G, r0 = tile * kTileRows;
   if (r0 >= R) return;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, half = lane >> 5;
-  const int64_t w0 = r0 + 32 * wave, row = w0 + (lane & 31);
+  const int w0 = r0 + 32 * wave, row = w0 + (lane & 31);
   const bool live = row < R;
-  const int64_t tok = live ? row / a.G : 0;
-  const int head = s.h * a.G + (int)(live ? row % a.G : 0);
+  const int tok = live ? row / a.G : 0;
+  const int head = s.h * a.G + (live ? row % a.G : 0);
 
-  // pages this block, and tokens the wave's first and last rows and the lane's row see
-  const int64_t last = (r0 + kTileRows < R ? r0 + kTileRows : R) - 1;
-  const int64_t pages = (limit_of(a, s, last / a.G) + kPage - 1) / kPage;
-  const int64_t p0 = pages * split / a.splits, p1 = pages * (split + 1) / a.splits;
-  const int64_t lim_row = live ? limit_of(a, s, tok) : 0;
-  const int64_t lim_first = w0 < R ? limit_of(a, s, w0 / a.G) : 0;
-  const int64_t w_last = (w0 + 32 < R ? w0 + 32 : R) - 1;
-  const int64_t lim_last = w0 < R ? limit_of(a, s, w_last / a.G) : 0;
+  // pages of this block, and tokens that the wave's first row and the lane's row see
+  const int last = (r0 + kTileRows < R ? r0 + kTileRows : R) - 1;
+  const int pages = (int)(((int64_t)limit_of(a, s, last / a.G) + kPage - 1) / kPage);
+  const int p0 = __builtin_amdgcn_readfirstlane((int)((int64_t)pages * split / a.splits));
+  const int p1 = __builtin_amdgcn_readfirstlane((int)((int64_t)pages * (split + 1) / a.splits));
+  const int lim_row = live ? limit_of(a, s, tok) : 0;
+  const int lim_first = __builtin_amdgcn_readfirstlane(w0 < R ? limit_of(a, s, w0 / a.G) : 0);
 
   QueryOp<DIM> q;
-  query_operand<DIM>(a.Q + (s.first + tok) * a.ldq + (int64_t)head * DIM, live, half, q);
+  query_operand<DIM>(a.Q + (int64_t)(s.first + tok) * a.ldq + (int64_t)head * DIM, live, half, q);
   State<DIM> st;
   state_init(st);
 
   const int64_t head_off = (int64_t)s.h * kBytes + lane * 16;
   const int64_t page_bytes = (int64_t)a.Hkv * kBytes;
+  const uint8_t* k_src = a.kc + head_off + wave * kCopies * 1024;
+  const uint8_t* v_src = a.vc + head_off + wave * kCopies * 1024;
   auto copy_k = [&](int page, int slot) {
-    const uint8_t* src = a.kc + (int64_t)(page < 0 ? 0 : page) * page_bytes + head_off;
 #pragma unroll
-    for (int i = 0; i < kCopies; ++i) {
-      const int f = wave * kCopies + i;
-      __builtin_amdgcn_global_load_lds((gvoid_t*)(src + f * 1024),
-                                       (lvoid_t*)(&k_img[slot][f * 1024]), 16, 0, 0);
-    }
+    for (int i = 0; i < kCopies; ++i)
+      __builtin_amdgcn_global_load_lds((gvoid_t*)(k_src + page * page_bytes + i * 1024),
+                                       (lvoid_t*)(&(slot ? k_img1 : k_img0)[(wave * kCopies + i) * 1024]),
+                                       16, 0, 0);
   };
   u32x4_t vr[kCopies];
   auto load_v = [&](int page) {
-    const uint8_t* src = a.vc + (int64_t)(page < 0 ? 0 : page) * page_bytes + head_off;
 #pragma unroll
     for (int i = 0; i < kCopies; ++i)
-      vr[i] = *reinterpret_cast<const u32x4_t*>(src + (wave * kCopies + i) * 1024);
+      vr[i] = *reinterpret_cast<const u32x4_t*>(v_src + page * page_bytes + i * 1024);
+  };
+  // the sequence's last page may hold fewer tokens than slots
+  const int part = __builtin_amdgcn_readfirstlane(s.kv % kPage);
+  const int part_at = __builtin_amdgcn_readfirstlane(part ? s.kv / kPage : -1);
+  auto trim_v = [&] {
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i) vr[i] = drop_slots(vr[i], (wave * kCopies + i) & 1, half, part);
   };
   // fragment f: its two 16-token steps of 1 KB each
-  auto widen_v = [&](int64_t at, int exps, int slot) {
-    const float scale = two_to((exps >> 8) - 127);
-    const int64_t left = s.kv - at * kPage;
+  auto widen_v = [&](int exps, int slot) {
+    const float scale = two_to(((exps >> 8) & 255) - 127);
 #pragma unroll
-    for (int i = 0; i < kCopies; ++i) {
-      const int f = wave * kCopies + i;
-      u32x4_t v = vr[i];
-      if (left < kPage) v = drop_slots(v, f & 1, half, (int)left);
+    for (int i = 0; i < kCopies; ++i)
 #pragma unroll
       for (int g = 0; g < 2; ++g)
-        *reinterpret_cast<bf16x8_t*>(&v_img[slot][(2 * f + g) * 1024 + lane * 16]) =
-            widen8(v[2 * g], v[2 * g + 1], scale);
+        *reinterpret_cast<bf16x8_t*>(
+            &v_img[slot][(2 * (wave * kCopies + i) + g) * 1024 + lane * 16]) =
+            widen8(vr[i][2 * g], vr[i][2 * g + 1], scale);
+  };
+  auto page_scores = [&](int exps, int slot, f32x16_t (&z)[2]) {
+    const uint8_t* k = (slot ? k_img1 : k_img0) + lane * 16;
+    scores<DIM>(z, q, exps & 255,
+                [&](int f) { return *reinterpret_cast<const u32x4_t*>(k + f * 1024); });
+  };
+  auto mask = [&](int i, int exps, f32x16_t (&z)[2], float& top) {
+    const int t0 = i * kPage;
+    if (!(exps & kPresent) || t0 + kPage > lim_first) {
+      const int lr = (exps & kPresent) ? lim_row - t0 : 0;
+      hide(z, lr > kPage ? kPage : (lr < 0 ? 0 : lr), half);
+      top = largest(z, a.c);
     }
   };
 
-  // lane i: page and exponents of logical page g0 + i (cur) and g0 + 64 + i (nxt)
-  int64_t g0 = p0;
-  int cur, cur_e, nxt, nxt_e;
-  page_meta(a, s, g0 + lane, p1, cur, cur_e);
-  page_meta(a, s, g0 + 64 + lane, p1, nxt, nxt_e);
-  auto page_at = [&](int64_t i) {
-    const int d = (int)(i - g0);
-    return d < 64 ? __builtin_amdgcn_readlane(cur, d) : __builtin_amdgcn_readlane(nxt, d - 64);
-  };
-  auto exps_at = [&](int64_t i) {
-    const int d = (int)(i - g0);
-    return d < 64 ? __builtin_amdgcn_readlane(cur_e, d) : __builtin_amdgcn_readlane(nxt_e, d - 64);
-  };
   if (p0 < p1) {
+    // lane l: page number and exponents of logical page g0 + l
+    int g0 = p0, meta, meta_e;
+    page_meta(a, s, g0 + lane, p1, meta, meta_e);
+    auto lane_of = [&](int i) { return (i < p1 ? i : p1 - 1) - g0; };
+    auto page_at = [&](int i) { return __builtin_amdgcn_readlane(meta, lane_of(i)); };
+    auto exps_at = [&](int i) { return __builtin_amdgcn_readlane(meta_e, lane_of(i)); };
+
+    f32x16_t za[2], zb[2];
     copy_k(page_at(p0), 0);
     load_v(page_at(p0));
-    widen_v(p0, exps_at(p0), 0);
-    if (p0 + 1 < p1) load_v(page_at(p0 + 1));
-  }
-  int slot = 0;
-  for (int64_t i = p0; i < p1; ++i) {
-    if (i - g0 == 64) {
-      g0 += 64;
-      cur = nxt;
-      cur_e = nxt_e;
-      page_meta(a, s, g0 + 64 + lane, p1, nxt, nxt_e);
-    }
-    // page i has landed in LDS for every wave, and every wave is done with page i - 1
+    if (p0 == part_at) trim_v();
+    int e0 = exps_at(p0);
+    widen_v(e0, 0);
+    copy_k(page_at(p0 + 1), 1);
+    load_v(page_at(p0 + 1));
     wait_vmcnt<0>();
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    if (i + 1 < p1) {
-      copy_k(page_at(i + 1), slot ^ 1);
-      widen_v(i + 1, exps_at(i + 1), slot ^ 1);
-      if (i + 2 < p1) load_v(page_at(i + 2));
-    }
-    const int page = __builtin_amdgcn_readlane(cur, (int)(i - g0));
-    const int64_t t0 = i * kPage;
-    if (page >= 0 && t0 < lim_last) {
-      const int k_exp = __builtin_amdgcn_readlane(cur_e, (int)(i - g0)) & 255;
-      const uint8_t *k = k_img[slot] + lane * 16, *v = v_img[slot] + lane * 16;
-      auto kf = [&](int f) { return *reinterpret_cast<const u32x4_t*>(k + f * 1024); };
-      auto vf = [&](int j, int tb, int g) {
-        return *reinterpret_cast<const bf16x8_t*>(v + ((2 * j + tb) * 2 + g) * 1024);
-      };
-      if (t0 + kPage <= lim_first) {
-        page_step<DIM, false>(st, q, a.c, k_exp, kPage, half, kf, vf);
-      } else {
-        const int64_t lr = lim_row - t0;
-        page_step<DIM, true>(st, q, a.c, k_exp, (int)(lr > kPage ? kPage : lr), half, kf, vf);
+    page_scores(e0, 0, za);
+    float top = largest(za, a.c);
+    mask(p0, e0, za, top);
+    raise(st, top);
+
+    // Page i, whose scores are in z (the maximum raised): its exponentials run while the matrix
+    // units form the next page's scores, and the next page's V is widened and its maximum
+    // taken while they form this page's product.  Pages behind the last repeat it; what is
+    // computed of them is not used.
+    auto step = [&](int i, int slot, f32x16_t (&z)[2], f32x16_t (&zn)[2]) {
+      // K of page i + 1 and V of page i are in LDS for every wave, and every wave is done with
+      // what takes their places (V loads of page i + 1 may still be in flight)
+      wait_vmcnt<kCopies>();
+      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      if (i - g0 >= 61) {
+        g0 = i;
+        page_meta(a, s, g0 + lane, p1, meta, meta_e);
       }
+      if (i + 1 == part_at) trim_v();
+      // From here to the masks one block without branches, its order fixed: a wave issues in
+      // order, so what is to run under a matrix instruction has to stand right behind it.
+      const int ahead = page_at(i + 2), e1 = exps_at(i + 1);
+      copy_k(ahead, slot);
+      const uint8_t* kp = (slot ? k_img0 : k_img1) + lane * 16;
+      const uint8_t* vp = v_img[slot] + lane * 16;
+      const int k_exp = e1 & 255;
+      u32x4_t kr[2][DIM / 32], w[4];
+      bf16x8_t vb[4];
+      auto k_read = [&](int tb) {
+#pragma unroll
+        for (int f = 0; f < DIM / 32; ++f)
+          kr[tb][f] = *reinterpret_cast<const u32x4_t*>(kp + (tb * (DIM / 32) + f) * 1024);
+      };
+      // V operand n: channels 32 (n % (DIM/32)) on, token step n / (DIM/32)
+      auto v_read = [&](int n) {
+        const int j = n % (DIM / 32), t = n / (DIM / 32);
+        vb[n % 4] = *reinterpret_cast<const bf16x8_t*>(
+            vp + ((2 * j + (t >> 1)) * 2 + (t & 1)) * 1024);
+      };
+      // weights of two tokens: pair n of the lane's sixteen
+      auto pair = [&](int n) {
+        const int tb = n >> 3, e = 2 * (n & 7);
+        const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(z[tb][e], a.c, -st.m));
+        const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(z[tb][e + 1], a.c, -st.m));
+        st.l += x + y;
+        w[n >> 2][n & 3] = pack_bf16x2(x, y);
+        asm volatile("" : "+v"(st.l));  // the sum is taken here, not behind the block
+      };
+      constexpr int kQk = 4 * (DIM / 64), kPv = 4 * (DIM / 32);
+      k_read(0);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int n = 0; n < kQk; ++n) {
+        const int tb = n / (kQk / 2), sc = n % (kQk / 2) / 2;
+        const u32x4_t a0 = kr[tb][2 * sc], a1 = kr[tb][2 * sc + 1];
+        const i32x8_t k = {(int)a0[0], (int)a0[1], (int)a0[2], (int)a0[3],
+                           (int)a1[0], (int)a1[1], (int)a1[2], (int)a1[3]};
+        if (n % (kQk / 2) == 0) zn[tb] = f32x16_t{};
+        zn[tb] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+            k, n % 2 ? q.lo[sc] : q.hi[sc], zn[tb], 0, 0, 0, k_exp, 0, n % 2 ? q.s_lo : q.s_hi);
+        if (n == 0) k_read(1);
+        if (n == kQk - 1) {
+#pragma unroll
+          for (int f = 0; f < 4; ++f) v_read(f);
+        }
+#pragma unroll
+        for (int f = 0; f < 16 / kQk; ++f) pair(n * (16 / kQk) + f);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      // the next page's V has arrived (the copies of K behind it may be in flight)
+      wait_vmcnt<kCopies>();
+      float t4[4];
+      const float scale = two_to(((e1 >> 8) & 255) - 127);
+#pragma unroll
+      for (int n = 0; n < kPv; ++n) {
+        const int j = n % (DIM / 32), t = n / (DIM / 32);
+        st.o[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+            vb[n % 4], __builtin_bit_cast(bf16x8_t, w[t]), st.o[j], 0, 0, 0);
+        if (n + 4 < kPv) v_read(n + 4);
+        if (n % 2 == 0 && n / 2 < 2 * kCopies) {  // one 16-token step of the next page's V
+          const int f = n / 4, g = n / 2 % 2;
+          *reinterpret_cast<bf16x8_t*>(
+              &v_img[slot ^ 1][(2 * (wave * kCopies + f) + g) * 1024 + lane * 16]) =
+              widen8(vr[f][2 * g], vr[f][2 * g + 1], scale);
+        }
+        if (n == kPv / 2) load_v(ahead);
+        if (n >= kPv / 2) {  // the next page's largest scores
+#pragma unroll
+          for (int k = (n - kPv / 2) * 32 / kPv; k < (n - kPv / 2 + 1) * 32 / kPv; ++k) {
+            const float x = zn[k >> 3][2 * (k & 7)], y = zn[k >> 3][2 * (k & 7) + 1];
+            t4[k & 3] = k < 4 ? fmaxf(x, y) : fmaxf(fmaxf(t4[k & 3], x), y);
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      float top = across(fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]))) * a.c;
+      mask(i + 1, e1, zn, top);
+      raise(st, top);
+    };
+    for (int i = p0; i < p1; i += 2) {
+      step(i, 0, za, zb);
+      if (i + 1 < p1) step(i + 1, 1, zb, za);
     }
-    slot ^= 1;
   }
   const float l = st.l + other_half(st.l);
   if (live) store_row<DIM>(a, st, l, s.first + tok, head, split, half);
@@ -426,49 +529,56 @@ __global__ __launch_bounds__(256, 2) void k_attn_few(AttnArgs a) {
   const int split = (int)(item % a.splits);
   Seq s;
   if (!sequence(a, (int)(item / a.splits), s)) return;
-  int64_t R = s.n * a.G;
-  R = R < 32 ? R : 32;
+  const int R = s.n * a.G < 32 ? s.n * a.G : 32;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, half = lane >> 5, n = lane & 31;
   const bool live = n < R;
-  const int64_t tok = live ? n / a.G : 0;
+  const int tok = live ? n / a.G : 0;
   const int head = s.h * a.G + (live ? n % a.G : 0);
-  const int64_t pages = (limit_of(a, s, (R - 1) / a.G) + kPage - 1) / kPage;
-  const int64_t p0 = pages * split / a.splits, p1 = pages * (split + 1) / a.splits;
-  const int64_t lim_row = live ? limit_of(a, s, tok) : 0;
-  const int64_t lim_first = limit_of(a, s, 0);
+  const int pages = (int)(((int64_t)limit_of(a, s, (R - 1) / a.G) + kPage - 1) / kPage);
+  const int p0 = (int)((int64_t)pages * split / a.splits);
+  const int p1 = (int)((int64_t)pages * (split + 1) / a.splits);
+  const int lim_row = live ? limit_of(a, s, tok) : 0;
+  const int lim_first = limit_of(a, s, 0);
 
   QueryOp<DIM> q;
-  query_operand<DIM>(a.Q + (s.first + tok) * a.ldq + (int64_t)head * DIM, live, half, q);
+  query_operand<DIM>(a.Q + (int64_t)(s.first + tok) * a.ldq + (int64_t)head * DIM, live, half, q);
   State<DIM> st;
   state_init(st);
-  const int64_t head_off = (int64_t)s.h * kBytes, page_bytes = (int64_t)a.Hkv * kBytes;
-  for (int64_t g0 = p0 + wave; g0 < p1; g0 += 256) {
+  const int64_t head_off = (int64_t)s.h * kBytes + lane * 16, page_bytes = (int64_t)a.Hkv * kBytes;
+  for (int g0 = p0 + wave; g0 < p1; g0 += 256) {
     int meta, meta_e;
     page_meta(a, s, g0 + 4 * lane, p1, meta, meta_e);
     for (int d = 0; d < 64 && g0 + 4 * d < p1; ++d) {
-      const int page = __builtin_amdgcn_readlane(meta, d);
-      if (page < 0) continue;
       const int exps = __builtin_amdgcn_readlane(meta_e, d);
-      const int64_t at = (int64_t)page * page_bytes + head_off + lane * 16;
+      if (!(exps & kPresent)) continue;
+      const int64_t at = __builtin_amdgcn_readlane(meta, d) * page_bytes + head_off;
       u32x4_t kr[kFrags], vr[kFrags];
 #pragma unroll
       for (int f = 0; f < kFrags; ++f) kr[f] = *reinterpret_cast<const u32x4_t*>(a.kc + at + f * 1024);
 #pragma unroll
       for (int f = 0; f < kFrags; ++f) vr[f] = *reinterpret_cast<const u32x4_t*>(a.vc + at + f * 1024);
-      const int64_t t0 = (g0 + 4 * d) * kPage;
-      const float scale = two_to((exps >> 8) - 127);
-      auto kf = [&](int f) { return kr[f]; };
-      auto vf = [&](int j, int tb, int g) {
-        return widen8(vr[2 * j + tb][2 * g], vr[2 * j + tb][2 * g + 1], scale);
-      };
-      if (t0 + kPage <= lim_first) {
-        page_step<DIM, false>(st, q, a.c, exps & 255, kPage, half, kf, vf);
-      } else {
-        const int64_t lr = lim_row - t0, lk = s.kv - t0;
+      const int t0 = (g0 + 4 * d) * kPage;
+      const float scale = two_to(((exps >> 8) & 255) - 127);
+      f32x16_t z[2];
+      scores<DIM>(z, q, exps & 255, [&](int f) { return kr[f]; });
+      if (t0 + kPage > lim_first) {
+        const int lr = lim_row - t0, lk = s.kv - t0;
+        hide(z, lr > kPage ? kPage : lr, half);
 #pragma unroll
-        for (int f = 0; f < kFrags; ++f) vr[f] = drop_slots(vr[f], f & 1, half, (int)(lk > kPage ? kPage : lk));
-        page_step<DIM, true>(st, q, a.c, exps & 255, (int)(lr > kPage ? kPage : lr), half, kf, vf);
+        for (int f = 0; f < kFrags; ++f)
+          vr[f] = drop_slots(vr[f], f & 1, half, lk > kPage ? kPage : lk);
       }
+      raise(st, largest(z, a.c));
+#pragma unroll
+      for (int tb = 0; tb < 2; ++tb)
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          const bf16x8_t p = weights(st, z, tb, g, a.c);
+#pragma unroll
+          for (int j = 0; j < DIM / 32; ++j)
+            st.o[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                widen8(vr[2 * j + tb][2 * g], vr[2 * j + tb][2 * g + 1], scale), p, st.o[j], 0, 0, 0);
+        }
     }
   }
   // join the four waves
@@ -486,7 +596,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_few(AttnArgs a) {
     for (int i = 0; i < 16; ++i)
       s_o[wave][32 * j + 8 * (i >> 2) + 4 * half + (i & 3)][n] = st.o[j][i] * f;
   __syncthreads();
-  for (int o = threadIdx.x; o < (int)R * DIM; o += 256) {
+  for (int o = threadIdx.x; o < R * DIM; o += 256) {
     const int rr = o / DIM, d = o % DIM;
     float sum = 0.0f, l = 0.0f;
     const float mm = fmaxf(fmaxf(s_m[0][rr], s_m[1][rr]), fmaxf(s_m[2][rr], s_m[3][rr]));
