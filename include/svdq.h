@@ -469,7 +469,8 @@ svdq_status svdq_score_modal_rel_l2_ref(const uint16_t* Y, int64_t ldy, const ui
  *   inv = fl32(1 / sqrt(mean_k h² + eps))                (sum, mean and root in fp64)
  *   x̂   = fl32(fl32(fl32(h·inv)·gamma)·fl32(1/λ))        (gamma NULL: 1; lambda NULL: λ = 1)
  *   codes, scales: MXFP8 of x̂ (see svdq_format);  D = bf16(x̂)·lora_downᵀ, fp32 [M, r]
- * X, residual and H [M, K] bf16 with leading dimensions ldx, ldr, ldh; gamma [K] bf16; eps > 0.
+ * X, residual and H [M, K] bf16 with leading dimensions ldx, ldr, ldh, K at most 32768; gamma [K]
+ * bf16; eps > 0.
  * H receives h and is required with a residual (ignored without one); it may be X or residual
  * itself (in place), but must not overlap them otherwise.  codes [M, K], scales [M, K/32].  D may
  * be NULL iff r == 0.  Codes and scales bit-exact: the fp64 sum leaves inv independent of the

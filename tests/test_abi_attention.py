@@ -39,6 +39,7 @@ def test_norm_refusals(lib):
         assert call(**{k: MIS}) == SHAPE and "aligned" in _err(lib), k
     assert call(M=0) == SHAPE and call(M=1 << 31) == SHAPE
     assert call(K=128) == SHAPE and call(K=0) == SHAPE
+    assert call(K=33024, ldx=33024, ldr=33024, ldh=33024) == SHAPE
     for k in ("ldx", "ldr", "ldh"):
         assert call(**{k: 255}) == SHAPE and call(**{k: 260}) == SHAPE, k
     for eps in (0.0, -1.0, float("inf"), float("nan")):

@@ -55,21 +55,23 @@ def _check(L, c, K, eps=1e-6, in_place=None):
         assert D is None
 
 
-@pytest.mark.parametrize("M", [1, 2, 15, 17, 65])
+@pytest.mark.parametrize("M", [1, 2, 15, 17, 65, 600, 4200])
 @pytest.mark.parametrize("r", [0, 8, 128])
 def test_rows_and_ranks(L, M, r):
     _check(L, _case(M, 512, r, True, True, True, seed=M), 512)
 
 
-@pytest.mark.parametrize("K", [256, 768, 2048, 2304, 5120, 5376, 6400, 8448, 16640])
+@pytest.mark.parametrize("K", [256, 768, 2048, 2304, 5120, 5376, 6400, 8448, 16640, 32768])
 @pytest.mark.parametrize("r", [0, 32])
 def test_row_lengths(L, K, r):
     _check(L, _case(19, K, r, True, True, True, seed=K), K)
 
 
 @pytest.mark.parametrize("r", [16, 24, 40, 64, 72, 96, 112, 120])
-def test_every_rank_tile(L, r):
-    _check(L, _case(33, 1280, r, True, True, True, seed=r), 1280)
+@pytest.mark.parametrize("M", [33, 1500, 20500])
+def test_every_rank_tile(L, r, M):
+    K = 1280 if M == 33 else 256
+    _check(L, _case(M, K, r, True, True, True, seed=r), K)
 
 
 @pytest.mark.parametrize("residual", [False, True])

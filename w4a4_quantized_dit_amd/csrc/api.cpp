@@ -757,6 +757,9 @@ svdq_status svdq_rmsnorm_quant_act(const uint16_t* X, int64_t M, int64_t K, int6
   REQUIRE_ALIGNED(lambda); REQUIRE_ALIGNED(lora_down); REQUIRE_ALIGNED(codes);
   TRY(check_rows(fn, "M", M, 1));
   TRY(check_k(fn, K));
+  if (K > svdq::kNormMaxK)
+    return fail(SVDQ_UNSUPPORTED_SHAPE, "%s: K=%lld exceeds %lld", fn, (long long)K,
+                (long long)svdq::kNormMaxK);
   TRY(check_ld(fn, "ldx", ldx, K));
   if (residual) {
     TRY(check_ld(fn, "ldr", ldr, K));

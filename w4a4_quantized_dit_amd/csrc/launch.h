@@ -128,6 +128,8 @@ hipError_t launch_lambda_search(const uint16_t* X, int64_t M, int64_t ldx, const
                                 hipStream_t s);
 
 
+// Channels of a row that the norm kernel holds.
+constexpr int64_t kNormMaxK = 32768;
 // Residual, RMS norm, smoothing, MXFP8 codes and the low-rank down-projection of each row.
 hipError_t launch_norm_quant(const uint16_t* X, int64_t M, int64_t K, int64_t ldx,
                              const uint16_t* residual, int64_t ldr, uint16_t* H, int64_t ldh,

@@ -10,14 +10,18 @@
 // is, so inv does not depend on the summation order and the codes, which sit next to rounding
 // borders, are the same for every work split.
 //
-// Memory-bound: 7 bytes per element (x, res in; h, code out).  Each element is read once, held
-// in registers between the sum and the quantisation.
+// Memory-bound: 7 bytes per element (x, res in; h, code out).  Each element is read once and held
+// in registers between the sum and the quantisation (16384 x 5120: 123 us, 4.8 TB/s, what a
+// large copy reaches).  D is a kernel of its own over h.
 #include "device.h"
 #include "launch.h"
 
 namespace svdq {
 
 namespace {
+
+typedef __attribute__((address_space(1))) void gvoid_t;
+typedef __attribute__((address_space(3))) void lvoid_t;
 
 struct NormArgs {
   const uint16_t* X;
@@ -99,15 +103,15 @@ __device__ __forceinline__ uint2 codes8(const float (&x)[8], int e) {
   return uint2{e4m3_pack4(y[0], y[1], y[2], y[3]), e4m3_pack4(y[4], y[5], y[6], y[7])};
 }
 
-// One row per TPR threads, r == 0.  Thread t of the row owns the 16-byte pieces t, t + TPR, ...;
-// four neighbouring threads hold one block of 32.
+// One row per block of TPR threads: thread t owns the 16-byte pieces t, t + TPR, ... of the row;
+// four neighbouring threads hold one MX block.  With a low-rank branch the row's inv is left in
+// the first element of every 4 of its D row for the product kernels below, whose blocks read
+// it before they write these elements of D.
 template <int TPR, int NV>
-__global__ __launch_bounds__(256) void k_norm_row(NormArgs a) {
-  constexpr int kRows = 256 / TPR;
-  __shared__ double s_part[4];
-  const int t = threadIdx.x % TPR;
-  const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / TPR;
-  const bool live = row < a.M;
+__global__ __launch_bounds__(TPR) void k_norm_row(NormArgs a) {
+  __shared__ double s_part[TPR / 64];
+  const int t = threadIdx.x;
+  const int64_t row = blockIdx.x;
   const int nv = (int)(a.K / 8);
   u32x4_t h[NV];
   double s = 0.0;
@@ -115,7 +119,7 @@ __global__ __launch_bounds__(256) void k_norm_row(NormArgs a) {
   for (int i = 0; i < NV; ++i) {
     const int v = t + TPR * i;
     h[i] = u32x4_t{0u, 0u, 0u, 0u};
-    if (live && v < nv) {
+    if (v < nv) {
       h[i] = load16(a.X + row * a.ldx + 8 * v);
       if (a.res) {
         h[i] = add8(h[i], load16(a.res + row * a.ldr + 8 * v));
@@ -126,16 +130,17 @@ __global__ __launch_bounds__(256) void k_norm_row(NormArgs a) {
   }
 #pragma unroll
   for (int d = 1; d < 64; d *= 2) s += __shfl_xor(s, d);
-  if (TPR > 64) {
-    if ((threadIdx.x & 63) == 0) s_part[threadIdx.x >> 6] = s;
-    __syncthreads();
-    s = s_part[0] + s_part[1] + s_part[2] + s_part[3];
-  }
+  if ((threadIdx.x & 63) == 0) s_part[threadIdx.x >> 6] = s;
+  __syncthreads();
+  s = 0.0;
+#pragma unroll
+  for (int w = 0; w < TPR / 64; ++w) s += s_part[w];
   const float inv = (float)(1.0 / sqrt(s / (double)a.K + a.eps));
+  if (4 * t < a.r) a.D[row * a.r + 4 * t] = inv;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int v = t + TPR * i;
-    const bool on = live && v < nv;  // whole blocks: nv is a multiple of 32
+    const bool on = v < nv;  // whole blocks: nv is a multiple of 32
     float x[8];
     if (on) xhat8(a, h[i], 8 * v, inv, x);
     float m = on ? amax8(x) : 0.0f;
@@ -149,138 +154,236 @@ __global__ __launch_bounds__(256) void k_norm_row(NormArgs a) {
   }
 }
 
-// Sixteen rows per block of eight waves, any K, with the down-projection on MFMA 16x16x32: lane
-// (row = lane % 16, q = lane / 16) holds 8 channels of a 32-channel step, which is the A operand
-// of the step, so the quantised registers feed the product directly; the four lanes of a row
-// hold one MX block.  Wave w takes the 64-channel chunks w, w + 8, ...; the partial D of the
-// waves are added in wave order through LDS.
-constexpr int kLrWaves = 8;
+// D = bf16(x̂)·L1 on MFMA 16x16x32, from h and the inv left in D.  Fusing it into the row kernel
+// was tried first: a block then holds sixteen rows of h in registers while it reads all of L1
+// from L2, one block a CU, 701 us at 31688 x 5120, rank 128; reading h once more costs 2 bytes
+// an element, most of them from the cache below HBM (the blocks go backwards, the rows written
+// last come first), and lets 64 rows share each piece of L1.
+struct DownArgs {
+  const uint16_t* h;
+  int64_t ldh;
+};
 
-template <int NT, int NCH>
-__global__ __launch_bounds__(64 * kLrWaves) void k_norm_lr(NormArgs a) {
-  constexpr int NTc = NT > 0 ? NT : 1;
-  __shared__ double s_sum[kLrWaves][16];
-  __shared__ float s_d[NT > 0 ? kLrWaves * 16 * NT * 16 : 1];
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int rl = lane & 15, q = lane >> 4;
-  const int64_t row = (int64_t)blockIdx.x * 16 + rl;
-  const bool live = row < a.M;
-  const int64_t lrow = live ? row : a.M - 1;
-  const int nch = (int)(a.K / 64);
-  const uint16_t* xr = a.X + lrow * a.ldx;
-  const uint16_t* rr = a.res ? a.res + lrow * a.ldr : nullptr;
-  uint16_t* hr = a.res ? a.H + lrow * a.ldh : nullptr;
-  u32x4_t keep[2 * NCH];
-  double s = 0.0;
+__device__ __forceinline__ void xhat8_lds(u32x4_t h, float inv, const float* g, const float* l,
+                                          float (&x)[8]) {
 #pragma unroll
-  for (int i = 0; i < NCH; ++i) {
-    const int c = wave + kLrWaves * i;
-    if (c < nch) {
+  for (int c = 0; c < 4; ++c) {
+    x[2 * c] = bf16_lo(h[c]) * inv;
+    x[2 * c + 1] = bf16_hi(h[c]) * inv;
+  }
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int64_t k = 64 * c + 32 * u + 8 * q;
-        u32x4_t h = load16(xr + k);
-        if (rr) h = add8(h, load16(rr + k));
-        keep[2 * i + u] = h;
-        s += sq8(h);
+  for (int j = 0; j < 8; ++j) x[j] = (x[j] * g[j]) * l[j];
+}
+
+// Many rows: eight waves of 16 rows.  Each 64-channel chunk of h (128 rows) and of L1 goes
+// straight into one of three LDS images, two chunks ahead, in whole 128-byte lines: what bounds
+// such a kernel is the requests a CU can make, about one per four clocks, and h read by the
+// lanes that need it is twice as many, L1 for 64 rows instead of 128 again (117 us instead of
+// 101 at 31688 x 5120, rank 128; one chunk ahead instead of two or three 137).  The 16-byte
+// pieces of a row's 128 bytes lie at piece ^ (row % 8), so that the sixteen rows of a fragment
+// read are on different banks.  γ and 1/λ follow through registers.  Every step issues the same
+// loads (past the end the last chunk's again), so that one count waits for the oldest.  Rows past
+// M and ranks past r repeat the last one; what comes of them is not stored.
+constexpr int kDownRows = 128, kChunk = 64, kImages = 3;
+
+template <int NT>
+__global__ __launch_bounds__(512) void k_norm_down(NormArgs a, DownArgs d) {
+  constexpr int kL = NT * 16 * kChunk * 2, kH = kDownRows * kChunk * 2;  // bytes of an image
+  constexpr int kCopies = (2 * NT + 7) / 8;                               // of L1, per wave
+  constexpr int kLoads = kCopies + 4;
+  __shared__ __attribute__((aligned(16))) uint8_t s_0[kL + kH], s_1[kL + kH], s_2[kL + kH];
+  __shared__ __attribute__((aligned(16))) float s_g[8][kChunk], s_i[8][kChunk];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, rl = lane & 15, q = lane >> 4;
+  const int64_t first = (int64_t)(gridDim.x - 1 - blockIdx.x) * kDownRows;
+  const int64_t row0 = first + 16 * wave;
+  const int64_t row = row0 + rl < a.M ? row0 + rl : a.M - 1;
+  const int nch = (int)(a.K / kChunk);
+  const float inv = a.D[row * a.r];
+  // without γ or λ something else of K elements is read in their place, and not used
+  const uint16_t* gp = (a.gamma ? a.gamma : d.h) + lane;
+  const float* lp = (a.lambda ? a.lambda : reinterpret_cast<const float*>(a.down)) + lane;
+  // copy f of an image: rows 8f .. 8f + 7, eight lanes each
+  const int piece = 8 * ((lane ^ (lane >> 3)) & 7);
+  const uint16_t *src_l[kCopies], *src_h[2];
+  int f_l[kCopies];
+#pragma unroll
+  for (int i = 0; i < kCopies; ++i) {
+    f_l[i] = wave + 8 * i < 2 * NT ? wave + 8 * i : wave % (2 * NT);  // some twice, the same bytes
+    const int n = 8 * f_l[i] + lane / 8;
+    src_l[i] = a.down + (n < a.r ? n : a.r - 1) * a.K + piece;
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int64_t m = first + 16 * wave + 8 * i + lane / 8;
+    src_h[i] = d.h + (m < a.M ? m : a.M - 1) * d.ldh + piece;
+  }
+  uint16_t g[kImages];
+  float l[kImages];
+  auto load = [&](int c, int slot, uint8_t* img) {
+    const int64_t k = (int64_t)(c < nch ? c : nch - 1) * kChunk;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      __builtin_amdgcn_global_load_lds((gvoid_t*)(src_h[i] + k),
+                                       (lvoid_t*)(img + kL + (2 * wave + i) * 1024), 16, 0, 0);
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i)
+      __builtin_amdgcn_global_load_lds((gvoid_t*)(src_l[i] + k), (lvoid_t*)(img + f_l[i] * 1024),
+                                       16, 0, 0);
+    g[slot] = gp[k];
+    l[slot] = lp[k];
+  };
+  f32x4_t acc[NT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) acc[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  const int sw = rl & 7;
+  auto step = [&](int c, int slot, const uint8_t* img, uint8_t* free_img) {
+    wait_vmcnt<kLoads>();  // chunk c is here; c + 1 may be on its way
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);  // no use of the chunk moves up in front of its wait
+    // the wave's own copy of the chunk's factors: channel = lane
+    s_g[wave][lane] = a.gamma ? bf16_to_f32(g[slot]) : 1.0f;
+    s_i[wave][lane] = a.lambda ? 1.0f / l[slot] : 1.0f;
+    load(c + 2, (slot + 2) % kImages, free_img);
+    u32x4_t bv[2][NT], hv[2];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const int at = ((4 * s + q) ^ sw) * 16;
+      hv[s] = *reinterpret_cast<const u32x4_t*>(img + kL + (16 * wave + rl) * 128 + at);
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+        bv[s][j] = *reinterpret_cast<const u32x4_t*>(img + (16 * j + rl) * 128 + at);
+    }
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      float x[8], gg[8], ll[8];
+#pragma unroll
+      for (int j = 0; j < 8; j += 4) {
+        *reinterpret_cast<f32x4_t*>(gg + j) =
+            *reinterpret_cast<const f32x4_t*>(&s_g[wave][32 * s + 8 * q + j]);
+        *reinterpret_cast<f32x4_t*>(ll + j) =
+            *reinterpret_cast<const f32x4_t*>(&s_i[wave][32 * s + 8 * q + j]);
       }
-    }
-  }
-  // the chunks past the registers: their h is read again below
-  for (int c = wave + kLrWaves * NCH; c < nch; c += kLrWaves) {
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int64_t k = 64 * c + 32 * u + 8 * q;
-      u32x4_t h = load16(xr + k);
-      if (rr) h = add8(h, load16(rr + k));
-      s += sq8(h);
-    }
-  }
-  s += __shfl_xor(s, 16);
-  s += __shfl_xor(s, 32);
-  if (q == 0) s_sum[wave][rl] = s;
-  __syncthreads();
-  s = 0.0;
-#pragma unroll
-  for (int w = 0; w < kLrWaves; ++w) s += s_sum[w][rl];
-  const float inv = (float)(1.0 / sqrt(s / (double)a.K + a.eps));
-
-  f32x4_t acc[NTc];
-#pragma unroll
-  for (int j = 0; j < NTc; ++j) acc[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  auto step = [&](u32x4_t h, int64_t k) {
-    if (hr && live) *reinterpret_cast<u32x4_t*>(hr + k) = h;
-    float x[8];
-    xhat8(a, h, k, inv, x);
-    float m = amax8(x);
-    m = fmaxf(m, __shfl_xor(m, 16));
-    m = fmaxf(m, __shfl_xor(m, 32));
-    const int e = mx_exponent(m, 8);
-    if (live) {
-      *reinterpret_cast<uint2*>(a.codes + row * a.K + k) = codes8(x, e);
-      if (q == 0) a.scales[row * (a.K / 32) + k / 32] = (uint8_t)(e + 127);
-    }
-    if (NT > 0) {
+      xhat8_lds(hv[s], inv, gg, ll, x);
       u32x4_t av;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) av[c] = pack_bf16x2(x[2 * c], x[2 * c + 1]);
+      for (int j = 0; j < 4; ++j) av[j] = c < nch ? pack_bf16x2(x[2 * j], x[2 * j + 1]) : 0u;
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        const int n = 16 * j + rl;
-        u32x4_t bv = u32x4_t{0u, 0u, 0u, 0u};
-        if (n < a.r) bv = load16(a.down + n * a.K + k);
+      for (int j = 0; j < NT; ++j)
         acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, av),
-                                                         __builtin_bit_cast(bf16x8_t, bv), acc[j],
-                                                         0, 0, 0);
-      }
+                                                         __builtin_bit_cast(bf16x8_t, bv[s][j]),
+                                                         acc[j], 0, 0, 0);
     }
   };
-#pragma unroll
-  for (int i = 0; i < NCH; ++i) {
-    const int c = wave + kLrWaves * i;
-    if (c < nch) {
-      step(keep[2 * i], 64 * c + 8 * q);
-      step(keep[2 * i + 1], 64 * c + 32 + 8 * q);
-    }
+  load(0, 0, s_0);
+  load(1, 1, s_1);
+  // (steps past the end add zeros: a branch around them would make the compiler drain the loads
+  // where the paths meet)
+  for (int c = 0; c < nch; c += 3) {
+    step(c, 0, s_0, s_2);
+    step(c + 1, 1, s_1, s_0);
+    step(c + 2, 2, s_2, s_1);
   }
-  for (int c = wave + kLrWaves * NCH; c < nch; c += kLrWaves) {
+  wait_vmcnt<0>();  // no copy is left in flight when the block ends
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int64_t k = 64 * c + 32 * u + 8 * q;
-      u32x4_t h = load16(xr + k);
-      if (rr) h = add8(h, load16(rr + k));
-      step(h, k);
-    }
-  }
-  if (NT > 0) {
+  for (int j = 0; j < NT; ++j) {
+    const int n = 16 * j + rl;
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        s_d[(wave * 16 + 4 * q + i) * (NT * 16) + 16 * j + rl] = acc[j][i];
-    __syncthreads();
-    for (int o = threadIdx.x; o < 16 * a.r; o += 64 * kLrWaves) {
-      const int m = o / a.r, n = o % a.r;
-      const int64_t rw = (int64_t)blockIdx.x * 16 + m;
-      if (rw < a.M) {
-        float d = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kLrWaves; ++w) d += s_d[(w * 16 + m) * (NT * 16) + n];
-        a.D[rw * a.r + n] = d;
-      }
+    for (int i = 0; i < 4; ++i) {
+      const int64_t m = row0 + 4 * q + i;
+      if (m < a.M && n < a.r) a.D[m * a.r + n] = acc[j][i];
     }
   }
 }
 
+// Few rows: a block for each 16 rows and RT ranks, sixteen waves that take alternate 64-channel
+// chunks with the loads of four chunks under way at once, the partial sums added in wave order
+// (one block for all ranks, eight waves and a chunk at a time took 24 us for one row of 5120 at
+// rank 32 instead of 13).  A CU fetches L1 in half lines here, about one in four clocks, so
+// where 16 ranks a block leave CUs idle a block takes 4 of them (the other columns of its matrix
+// instructions repeat the last one and are not stored).
+constexpr int kFewWaves = 16, kFewBatch = 4;
+
+template <int RT>
+__global__ __launch_bounds__(64 * kFewWaves) void k_norm_down_few(NormArgs a, DownArgs d) {
+  __shared__ float s_d[kFewWaves][16][16];
+  __shared__ __attribute__((aligned(16))) float s_g[kFewWaves][kChunk], s_i[kFewWaves][kChunk];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, rl = lane & 15, q = lane >> 4;
+  const int64_t row = (int64_t)blockIdx.x * 16 + rl, lrow = row < a.M ? row : a.M - 1;
+  const int n0 = RT * blockIdx.y, nr = a.r - n0 < RT ? a.r - n0 : RT;
+  const float inv = a.D[lrow * a.r + n0];
+  const uint16_t* hr = d.h + lrow * d.ldh + 8 * q;
+  const uint16_t* dr = a.down + (n0 + (rl < nr ? rl : nr - 1)) * a.K + 8 * q;
+  const int nch = (int)(a.K / kChunk);
+  f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+  for (int c0 = wave; c0 < nch; c0 += kFewWaves * kFewBatch) {
+    u32x4_t h[kFewBatch][2], l1[kFewBatch][2];
+    float g[kFewBatch], l[kFewBatch];
+#pragma unroll
+    for (int i = 0; i < kFewBatch; ++i) {
+      const int c = c0 + kFewWaves * i;
+      if (c < nch) {
+        const int64_t k = (int64_t)c * kChunk;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          h[i][s] = load16(hr + k + 32 * s);
+          l1[i][s] = load16(dr + k + 32 * s);
+        }
+        g[i] = a.gamma ? bf16_to_f32(a.gamma[k + lane]) : 1.0f;
+        l[i] = a.lambda ? a.lambda[k + lane] : 1.0f;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kFewBatch; ++i) {
+      if (c0 + kFewWaves * i < nch) {
+        s_g[wave][lane] = g[i];  // the wave's own: LDS accesses of a wave keep their order
+        s_i[wave][lane] = 1.0f / l[i];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          float x[8], gg[8], ll[8];
+#pragma unroll
+          for (int j = 0; j < 8; j += 4) {
+            *reinterpret_cast<f32x4_t*>(gg + j) =
+                *reinterpret_cast<const f32x4_t*>(&s_g[wave][32 * s + 8 * q + j]);
+            *reinterpret_cast<f32x4_t*>(ll + j) =
+                *reinterpret_cast<const f32x4_t*>(&s_i[wave][32 * s + 8 * q + j]);
+          }
+          xhat8_lds(h[i][s], inv, gg, ll, x);
+          u32x4_t av;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) av[j] = pack_bf16x2(x[2 * j], x[2 * j + 1]);
+          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, av),
+                                                        __builtin_bit_cast(bf16x8_t, l1[i][s]), acc,
+                                                        0, 0, 0);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) s_d[wave][4 * q + i][rl] = acc[i];
+  __syncthreads();
+  const int m = threadIdx.x >> 4, n = threadIdx.x & 15;
+  const int64_t rw = (int64_t)blockIdx.x * 16 + m;
+  if (m < 16 && n < nr && rw < a.M) {
+    float v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kFewWaves; ++w) v += s_d[w][m][n];
+    a.D[rw * a.r + n0 + n] = v;
+  }
+}
+
+// Up to 1280 blocks of 16 rows and 16 ranks the kernel for few rows is the faster one (K = 5120,
+// whole call, few against many: rank 128, M 2048 63 and 93 us, M 4096 121 and 102; rank 32,
+// M 4096 51 and 74, M 8192 91 and 90, M 16384 205 and 164).
 template <int NT>
-hipError_t launch_lr(const NormArgs& a, hipStream_t s) {
-  const unsigned grid = (unsigned)((a.M + 15) / 16);
-  const int64_t per_wave = (a.K / 64 + kLrWaves - 1) / kLrWaves;
-  if (per_wave <= 4)
-    k_norm_lr<NT, 4><<<grid, 64 * kLrWaves, 0, s>>>(a);
+void launch_down(const NormArgs& a, hipStream_t s) {
+  const DownArgs d = a.res ? DownArgs{a.H, a.ldh} : DownArgs{a.X, a.ldx};
+  const int64_t rows = (a.M + 15) / 16;
+  if (rows * NT < 256)
+    k_norm_down_few<4><<<dim3((unsigned)rows, (unsigned)a.r / 4), 64 * kFewWaves, 0, s>>>(a, d);
+  else if (rows * NT <= 1280)
+    k_norm_down_few<16><<<dim3((unsigned)rows, NT), 64 * kFewWaves, 0, s>>>(a, d);
   else
-    k_norm_lr<NT, 10><<<grid, 64 * kLrWaves, 0, s>>>(a);
-  return hipGetLastError();
+    k_norm_down<NT><<<(unsigned)((a.M + kDownRows - 1) / kDownRows), 512, 0, s>>>(a, d);
 }
 
 }  // namespace
@@ -292,29 +395,28 @@ hipError_t launch_norm_quant(const uint16_t* X, int64_t M, int64_t K, int64_t ld
                              float* D, hipStream_t s) {
   const NormArgs a{X, residual, H, gamma, lambda, down, codes, scales, D, M, K, ldx, ldr, ldh,
                    (double)eps, (int)r};
-  if (r == 0) {
-    if (K <= 8192) {
-      const unsigned grid = (unsigned)M;
-      if (K <= 2048)
-        k_norm_row<256, 1><<<grid, 256, 0, s>>>(a);
-      else if (K <= 6144)
-        k_norm_row<256, 3><<<grid, 256, 0, s>>>(a);
-      else
-        k_norm_row<256, 4><<<grid, 256, 0, s>>>(a);
-      return hipGetLastError();
-    }
-    return launch_lr<0>(a, s);
-  }
+  const unsigned grid = (unsigned)M;
+  if (K <= 2048)
+    k_norm_row<256, 1><<<grid, 256, 0, s>>>(a);
+  else if (K <= 6144)
+    k_norm_row<256, 3><<<grid, 256, 0, s>>>(a);
+  else if (K <= 8192)
+    k_norm_row<256, 4><<<grid, 256, 0, s>>>(a);
+  else
+    k_norm_row<1024, 4><<<grid, 1024, 0, s>>>(a);
+  if (hipError_t e = hipGetLastError()) return e;
   switch ((r + 15) / 16) {
-    case 1: return launch_lr<1>(a, s);
-    case 2: return launch_lr<2>(a, s);
-    case 3: return launch_lr<3>(a, s);
-    case 4: return launch_lr<4>(a, s);
-    case 5: return launch_lr<5>(a, s);
-    case 6: return launch_lr<6>(a, s);
-    case 7: return launch_lr<7>(a, s);
-    default: return launch_lr<8>(a, s);
+    case 0: break;
+    case 1: launch_down<1>(a, s); break;
+    case 2: launch_down<2>(a, s); break;
+    case 3: launch_down<3>(a, s); break;
+    case 4: launch_down<4>(a, s); break;
+    case 5: launch_down<5>(a, s); break;
+    case 6: launch_down<6>(a, s); break;
+    case 7: launch_down<7>(a, s); break;
+    default: launch_down<8>(a, s); break;
   }
+  return hipGetLastError();
 }
 
 }  // namespace svdq
