@@ -5,7 +5,6 @@ memory owned by the caller) plus sizes; it checks dtypes / devices / shapes, pas
 and the current torch stream, and raises SvdqError on a non-zero status.  No step of the layer
 runs in Python: when the library is missing, loading fails loudly.
 """
-import contextlib
 import ctypes
 import os
 import re
@@ -171,9 +170,12 @@ def _ld(t):
 
 
 def _stream(stream=None):
+    if stream is not None:
+        return stream.cuda_stream
+    # the current device's current stream, without building a Stream object around its handle
+    # (0.3 us instead of 2.7, a sixth of a small call)
     torch = _torch()
-    s = torch.cuda.current_stream() if stream is None else stream
-    return s.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _bf16():
@@ -519,27 +521,68 @@ def svdq_score_modal_rel_l2(Y, X, W, rows, row_group, sums, stream=None):
 # the attention half: norm, rotary positions, the 8-bit cache and attention over it
 # ------------------------------------------------------------------------------------------
 
-def _on_device(*tensors):
-    """A guard for the device of the tensors (which must all be on one), so that a call on
-    tensors of another device than the current one runs there, on that device's stream."""
-    torch = _torch()
-    dev = None
-    for t in tensors:
-        if t is not None:
-            if dev is None:
-                dev = t.device
-            elif t.device != dev:
-                raise ValueError(f"tensors on {dev} and {t.device}: one device is needed")
-    if dev is None or dev.type != "cuda" or dev.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(dev)
+class _Args:
+    """Checked pointers of one call's tensors, which must all be on one device; as a context, the
+    call runs on that device and its current stream, also when another device is current.
+    (Everything about a tensor is checked in one place and once: a small call's time is its
+    marshalling.)"""
+    __slots__ = ("dev", "back")
 
+    def __init__(self):
+        self.dev = -1
 
-def _rows_of(t, rows, cols, name):
-    """A matrix of at least `rows` rows and exactly `cols` columns."""
-    if t is not None and (t.dim() != 2 or t.shape[0] < rows or t.shape[1] != cols):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [{rows}, {cols}]")
-    return t
+    def _at(self, t, name):
+        dev = t.get_device()
+        if dev != self.dev:
+            if dev < 0:
+                raise ValueError(f"{name} must be a device tensor")
+            if self.dev >= 0:
+                raise ValueError(f"{name} is on device {dev}, the others on {self.dev}")
+            self.dev = dev
+        return t.data_ptr()
+
+    def mat(self, t, rows, cols, dtypes, name):
+        """(pointer, leading dimension) of a matrix of at least `rows` rows and exactly `cols`
+        columns with contiguous rows; (None, cols) for None."""
+        if t is None:
+            return None, cols
+        try:
+            shape, stride = t.shape, t.stride()
+            if t.dtype not in dtypes:
+                raise TypeError(f"{name} has dtype {t.dtype}, expected {dtypes[0]}")
+        except AttributeError:
+            raise TypeError(f"{name} must be a torch.Tensor") from None
+        if len(shape) != 2 or shape[0] < rows or shape[1] != cols:
+            raise ValueError(f"{name} has shape {tuple(shape)}, expected [{rows}, {cols}]")
+        if cols > 1 and stride[1] != 1 and shape[0] > 0:
+            raise ValueError(f"{name} must be a 2-D matrix with contiguous rows")
+        return self._at(t, name), (stride[0] if shape[0] > 1 else max(stride[0], cols))
+
+    def vec(self, t, n, dtype, name):
+        """Pointer of a contiguous tensor of at least n elements; None for None."""
+        if t is None:
+            return None
+        try:
+            if t.dtype is not dtype and t.dtype != dtype:
+                raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+        except AttributeError:
+            raise TypeError(f"{name} must be a torch.Tensor") from None
+        if t.numel() < n:
+            raise ValueError(f"{name} has {t.numel()} elements, needs {n}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        return self._at(t, name)
+
+    def __enter__(self):
+        cuda = _torch().cuda
+        self.back = None
+        if self.dev >= 0 and self.dev != cuda.current_device():
+            self.back = cuda.device(self.dev)
+            self.back.__enter__()
+
+    def __exit__(self, *exc):
+        if self.back is not None:
+            self.back.__exit__(*exc)
 
 
 def svdq_rmsnorm_quant_act(X, residual, H, gamma, eps, lam, lora_down, r, codes, scales, D,
@@ -550,21 +593,34 @@ def svdq_rmsnorm_quant_act(X, residual, H, gamma, eps, lam, lora_down, r, codes,
     if X.dim() != 2:
         raise ValueError("X must be a 2-D matrix with contiguous rows")
     M, K = X.shape
-    f32, bf = torch.float32, _bf16()
-    if r:
-        _rows_of(lora_down, r, K, "lora_down")
-    with _on_device(X, residual, H, gamma, lam, lora_down if r else None, codes, scales,
-                    D if r else None):
-        _check(load().svdq_rmsnorm_quant_act(
-            _ptr(X, bf, "X", rows=True), M, K, _ld(X),
-            _ptr(_rows_of(residual, M, K, "residual"), bf, "residual", rows=True),
-            _ld(residual) if residual is not None else K,
-            _ptr(_rows_of(H, M, K, "H"), bf, "H", rows=True), _ld(H) if H is not None else K,
-            _ptr(gamma, bf, "gamma", K), float(eps), _ptr(lam, f32, "lambda", K),
-            _ptr(lora_down if r else None, bf, "lora_down", r * K), int(r),
-            _ptr(codes, torch.uint8, "codes", M * K),
-            _ptr(scales, torch.uint8, "scales", M * K // 32),
-            _ptr(D if r else None, f32, "D", M * r), _stream(stream)))
+    bf, f32, u8 = _bf16(), torch.float32, torch.uint8
+    a = _Args()
+    x, ldx = a.mat(X, M, K, bf, "X")
+    res, ldr = a.mat(residual, M, K, bf, "residual")
+    h, ldh = a.mat(H, M, K, bf, "H")
+    args = (x, M, K, ldx, res, ldr, h, ldh, _gamma(a, gamma, K, bf), float(eps),
+            a.vec(lam, K, f32, "lambda"), _down(a, lora_down, r, K, bf), int(r),
+            a.vec(codes, M * K, u8, "codes"), a.vec(scales, M * K // 32, u8, "scales"),
+            a.vec(D, M * r, f32, "D") if r else None)
+    with a:
+        _check(load().svdq_rmsnorm_quant_act(*args, _stream(stream)))
+
+
+def _gamma(a, t, K, bf):
+    """Pointer of the norm's weight [K] bf16."""
+    if t is None:
+        return None
+    return a.vec(t, K, t.dtype if getattr(t, "dtype", None) in bf else bf[0], "gamma")
+
+
+def _down(a, t, r, K, bf):
+    """Pointer of the packed down factor [r, K] bf16."""
+    if not r:
+        return None
+    p, ld = a.mat(t, r, K, bf, "lora_down")
+    if p is not None and ld != K and r > 1:
+        raise ValueError("lora_down must be contiguous")
+    return p
 
 
 def svdq_rope_frequencies(axis_dims, theta):
@@ -582,58 +638,58 @@ def svdq_rope_axes(X, heads, dim, pos, freq, axis_dims, interleaved, inverse, Y,
     """Rotary positions of `heads` heads of each row of X into Y (X itself: in place); pos int32
     [M, n_axes], freq fp64 [sum(axis_dims)/2]."""
     torch = _torch()
-    M = X.shape[0]
-    n = len(axis_dims)
-    arr = (ctypes.c_int64 * max(1, n))(*[int(d) for d in axis_dims])
-    _rows_of(X, M, heads * dim, "X")
-    _rows_of(Y, M, heads * dim, "Y")
-    with _on_device(X, pos, freq, Y):
-        _check(load().svdq_rope_axes(
-            _ptr(X, _bf16(), "X", rows=True), M, _ld(X), int(heads), int(dim),
-            _ptr(_rows_of(pos, M, n, "pos"), torch.int32, "pos"),
-            _ptr(freq, torch.float64, "freq", sum(int(d) for d in axis_dims) // 2), n,
-            ctypes.cast(arr, _c_p), int(bool(interleaved)), int(bool(inverse)),
-            _ptr(Y, _bf16(), "Y", rows=True), _ld(Y), _stream(stream)))
+    M, n, bf = X.shape[0], len(axis_dims), _bf16()
+    arr = (ctypes.c_int64 * max(1, n))(*axis_dims)
+    a = _Args()
+    x, ldx = a.mat(X, M, heads * dim, bf, "X")
+    y, ldy = a.mat(Y, M, heads * dim, bf, "Y")
+    p, ldp = a.mat(pos, M, n, (torch.int32,), "pos")
+    if ldp != n and M > 1:
+        raise ValueError("pos must be contiguous")
+    args = (x, M, ldx, int(heads), int(dim), p, a.vec(freq, sum(axis_dims) // 2, torch.float64, "freq"),
+            n, arr, int(bool(interleaved)), int(bool(inverse)), y, ldy)
+    with a:
+        _check(load().svdq_rope_axes(*args, _stream(stream)))
 
 
-def _cache_args(k_codes, v_codes, k_scales, v_scales, dim, block_table, cu_rows, per_seq, what):
-    """Checked pointers and sizes of the cache operands: (codes and scales pointers), heads,
+def _cache_args(a, k_codes, v_codes, k_scales, v_scales, dim, block_table, cu_rows, per_seq, what):
+    """Checked pointers and sizes of the cache operands: (pointers of codes and scales), heads,
     n_pages, B, max_blocks and the pointers of block_table, cu_rows and per_seq."""
     torch = _torch()
     u8, i32 = torch.uint8, torch.int32
-    if k_codes.dim() != 3 or k_codes.shape[2] != 64 * dim:
-        raise ValueError(f"k_codes has shape {tuple(k_codes.shape)}, expected "
-                         f"[pages, heads, {64 * dim}]")
-    n_pages, heads = k_codes.shape[:2]
-    if v_codes.shape != k_codes.shape:
+    shape = k_codes.shape
+    if len(shape) != 3 or shape[2] != 64 * dim:
+        raise ValueError(f"k_codes has shape {tuple(shape)}, expected [pages, heads, {64 * dim}]")
+    n_pages, heads, _ = shape
+    if v_codes.shape != shape:
         raise ValueError("v_codes must have the shape of k_codes")
-    for t, name in ((k_scales, "k_scales"), (v_scales, "v_scales")):
-        if tuple(t.shape) != (n_pages, heads):
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [{n_pages}, {heads}]")
+    if k_scales.shape != shape[:2] or v_scales.shape != shape[:2]:
+        raise ValueError(f"k_scales and v_scales must be [{n_pages}, {heads}]")
     if block_table.dim() != 2:
         raise ValueError("block_table must be [B, max_blocks]")
     B, blocks = block_table.shape
-    ptrs = [_ptr(k_codes, u8, "k_codes"), _ptr(v_codes, u8, "v_codes"),
-            _ptr(k_scales, u8, "k_scales"), _ptr(v_scales, u8, "v_scales")]
-    return (ptrs, heads, n_pages, B, blocks, _ptr(block_table, i32, "block_table"),
-            _ptr(cu_rows, i32, "cu_rows", B + 1), _ptr(per_seq, i32, what, B))
+    ptrs = (a.vec(k_codes, 0, u8, "k_codes"), a.vec(v_codes, 0, u8, "v_codes"),
+            a.vec(k_scales, 0, u8, "k_scales"), a.vec(v_scales, 0, u8, "v_scales"))
+    return (ptrs, heads, n_pages, B, blocks, a.vec(block_table, 0, i32, "block_table"),
+            a.vec(cu_rows, B + 1, i32, "cu_rows"), a.vec(per_seq, B, i32, what))
 
 
 def _kv_call(name, K, V, dim, cu_rows, start, max_rows, block_table, k_codes, v_codes, k_scales,
              v_scales, stream):
-    with _on_device(K, V, cu_rows, start, block_table, k_codes, v_codes, k_scales, v_scales):
-        ptrs, heads, n_pages, B, blocks, table, cu, st = _cache_args(
-            k_codes, v_codes, k_scales, v_scales, dim, block_table, cu_rows, start, "start")
-        rows = K.shape[0]
-        _rows_of(K, rows, heads * dim, "K")
-        if V.shape != K.shape:
-            raise ValueError("V must have the shape of K")
-        if rows == 0:   # an empty tensor has no address
-            return
-        _check(getattr(load(), name)(
-            _ptr(K, _bf16(), "K", rows=True), _ld(K), _ptr(V, _bf16(), "V", rows=True), _ld(V),
-            rows, heads, int(dim), cu, st, B, int(max_rows), table, blocks, n_pages, *ptrs,
-            _stream(stream)))
+    a, bf = _Args(), _bf16()
+    ptrs, heads, n_pages, B, blocks, table, cu, st = _cache_args(
+        a, k_codes, v_codes, k_scales, v_scales, dim, block_table, cu_rows, start, "start")
+    rows = K.shape[0]
+    k, ldk = a.mat(K, rows, heads * dim, bf, "K")
+    if V.shape != K.shape:
+        raise ValueError("V must have the shape of K")
+    v, ldv = a.mat(V, rows, heads * dim, bf, "V")
+    if rows == 0:   # an empty tensor has no address
+        return
+    with a:
+        _check(getattr(load(), name)(k, ldk, v, ldv, rows, heads, int(dim), cu, st, B,
+                                     int(max_rows), table, blocks, n_pages, *ptrs,
+                                     _stream(stream)))
 
 
 def svdq_kv_write(K, V, dim, cu_rows, start, max_rows, block_table, k_codes, v_codes, k_scales,
@@ -660,20 +716,21 @@ def svdq_attn_kv8(Q, dim, cu_rows, kv_len, max_rows, max_kv, block_table, k_code
     """Attention of Q [rows, q_heads·dim] bf16 over the paged 8-bit cache into O and lse (fp32
     [rows, q_heads] or None); workspace uint8 (svdq_attn_kv8_workspace_bytes) or None."""
     torch = _torch()
-    with _on_device(Q, cu_rows, kv_len, block_table, k_codes, v_codes, k_scales, v_scales, O, lse,
-                    workspace):
-        ptrs, heads, n_pages, B, blocks, table, cu, ln = _cache_args(
-            k_codes, v_codes, k_scales, v_scales, dim, block_table, cu_rows, kv_len, "kv_len")
-        if Q.dim() != 2 or Q.shape[1] % dim != 0:
-            raise ValueError(f"Q has shape {tuple(Q.shape)}, expected [rows, heads·{dim}]")
-        rows, q_heads = Q.shape[0], Q.shape[1] // dim
-        _rows_of(O, rows, q_heads * dim, "O")
-        if rows == 0:
-            return
-        _check(load().svdq_attn_kv8(
-            _ptr(Q, _bf16(), "Q", rows=True), _ld(Q), rows, q_heads, heads, int(dim), cu, ln, B,
-            int(max_rows), int(max_kv), table, blocks, n_pages, *ptrs, float(scale),
-            int(bool(causal)), _ptr(O, _bf16(), "O", rows=True), _ld(O),
-            _ptr(lse, torch.float32, "lse", rows * q_heads),
-            _ptr(workspace, torch.uint8, "workspace"),
-            workspace.numel() if workspace is not None else 0, _stream(stream)))
+    a, bf = _Args(), _bf16()
+    ptrs, heads, n_pages, B, blocks, table, cu, ln = _cache_args(
+        a, k_codes, v_codes, k_scales, v_scales, dim, block_table, cu_rows, kv_len, "kv_len")
+    if Q.dim() != 2 or Q.shape[1] % dim != 0:
+        raise ValueError(f"Q has shape {tuple(Q.shape)}, expected [rows, heads·{dim}]")
+    rows, width = Q.shape
+    q_heads = width // dim
+    q, ldq = a.mat(Q, rows, width, bf, "Q")
+    o, ldo = a.mat(O, rows, width, bf, "O")
+    lse_p = a.vec(lse, rows * q_heads, torch.float32, "lse")
+    ws = a.vec(workspace, 0, torch.uint8, "workspace")
+    if rows == 0:
+        return
+    with a:
+        _check(load().svdq_attn_kv8(q, ldq, rows, q_heads, heads, int(dim), cu, ln, B,
+                                    int(max_rows), int(max_kv), table, blocks, n_pages, *ptrs,
+                                    float(scale), int(bool(causal)), o, ldo, lse_p, ws,
+                                    workspace.numel() if ws is not None else 0, _stream(stream)))
