@@ -913,7 +913,7 @@ svdq_status svdq_attn_kv8(const uint16_t* Q, int64_t ldq, int64_t rows, int64_t 
       return fail(SVDQ_UNSUPPORTED_SHAPE, "%s: workspace of %lld bytes, needs %lld", fn,
                   (long long)workspace_bytes, (long long)need);
   }
-  if (svdq::attn_blocks(q_heads, kv_heads, B, max_rows, max_kv) > INT32_MAX)
+  if (svdq::attn_blocks(rows, q_heads, kv_heads, dim, B, max_rows, max_kv) > INT32_MAX)
     return fail(SVDQ_UNSUPPORTED_SHAPE, "%s: more than 2^31 blocks of rows and heads", fn);
   return hip_result(svdq::launch_attn(Q, ldq, rows, q_heads, kv_heads, dim, cu_rows, kv_len, B,
                                       max_rows, max_kv, block_table, max_blocks, n_pages, k_codes,

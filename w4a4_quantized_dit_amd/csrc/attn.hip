@@ -660,19 +660,39 @@ struct Plan {
   int64_t tiles, splits;
 };
 
-// Few rows per key head go to the kernel that splits pages over its waves.  The page range is
-// split further until about three blocks per CU run (768 of 256 CUs), but never below eight
-// pages a block, where the join costs more than the parallelism brings.
-Plan plan(int64_t G, int64_t Hkv, int64_t B, int64_t max_q, int64_t max_kv) {
+// Few rows per key head go to the kernel that splits pages over its waves; its page range is split
+// further until about three blocks per CU run (768 of 256 CUs), but never below eight pages a
+// block, where the join costs more than the parallelism brings.  The tile kernel runs two blocks
+// a CU, in rounds of that many: of up to 16 splits the one of the least
+//   rounds · (pages a block + 4 for its ends) + the join's traffic, in pages
+// is taken (1008 rows x 31688 tokens x 40 heads are 320 blocks, five eighths of a round, which
+// took 748 us; three splits, two nearly full rounds of a third, SPLIT_US).
+Plan plan(int64_t G, int64_t Hkv, int64_t dim, int64_t rows, int64_t B, int64_t max_q,
+          int64_t max_kv) {
   Plan p;
   p.few = max_q * G <= 32;
   p.tiles = p.few ? 1 : (max_q * G + kTileRows - 1) / kTileRows;
-  const int64_t items = B * Hkv * p.tiles;
+  const int64_t items = B * Hkv * p.tiles > 0 ? B * Hkv * p.tiles : 1;
   const int64_t pages = (max_kv + kPage - 1) / kPage;
-  const int64_t want = (p.few ? 768 : 512) / (items < 1 ? 1 : items);
   const int64_t most = pages / 8;
-  p.splits = want < most ? want : most;
-  if (p.splits < 1) p.splits = 1;
+  p.splits = 1;
+  if (p.few) {
+    const int64_t want = 768 / items;
+    p.splits = want < most ? want : most;
+    if (p.splits < 1) p.splits = 1;
+    return p;
+  }
+  const int64_t slots = 512;
+  double best = 0.0;
+  for (int64_t s = 1; s <= 16 && (s == 1 || s <= most); ++s) {
+    // a block takes about 1.2 us a page; the join writes and reads its fp32 rows at 5 TB/s
+    const double join = s == 1 ? 0.0 : 4.0 + (double)(s * rows * G * Hkv * (dim + 2)) * 8.0 / 6.0e6;
+    const double cost = (double)((items * s + slots - 1) / slots) * ((double)((pages + s - 1) / s) + 4.0) + join;
+    if (s == 1 || cost < best) {
+      best = cost;
+      p.splits = s;
+    }
+  }
   return p;
 }
 
@@ -680,12 +700,13 @@ Plan plan(int64_t G, int64_t Hkv, int64_t B, int64_t max_q, int64_t max_kv) {
 
 int64_t attn_workspace_bytes(int64_t rows, int64_t Hq, int64_t Hkv, int64_t dim, int64_t B,
                              int64_t max_q, int64_t max_kv) {
-  const Plan p = plan(Hq / Hkv, Hkv, B, max_q, max_kv);
+  const Plan p = plan(Hq / Hkv, Hkv, dim, rows, B, max_q, max_kv);
   return p.splits > 1 ? p.splits * rows * Hq * (dim + 2) * 4 : 0;
 }
 
-int64_t attn_blocks(int64_t Hq, int64_t Hkv, int64_t B, int64_t max_q, int64_t max_kv) {
-  const Plan p = plan(Hq / Hkv, Hkv, B, max_q, max_kv);
+int64_t attn_blocks(int64_t rows, int64_t Hq, int64_t Hkv, int64_t dim, int64_t B, int64_t max_q,
+                    int64_t max_kv) {
+  const Plan p = plan(Hq / Hkv, Hkv, dim, rows, B, max_q, max_kv);
   return B * Hkv * p.tiles * p.splits + 8;
 }
 
@@ -695,7 +716,7 @@ hipError_t launch_attn(const uint16_t* Q, int64_t ldq, int64_t rows, int64_t Hq,
                        int64_t n_pages, const uint8_t* kc, const uint8_t* vc, const uint8_t* ks,
                        const uint8_t* vs, float scale, int causal, uint16_t* O, int64_t ldo,
                        float* lse, void* workspace, hipStream_t s) {
-  const Plan p = plan(Hq / Hkv, Hkv, B, max_q, max_kv);
+  const Plan p = plan(Hq / Hkv, Hkv, dim, rows, B, max_q, max_kv);
   AttnArgs a{Q, O, lse, (float*)workspace, cu, len, table, kc, vc, ks, vs, ldq, ldo, rows,
              max_blocks, n_pages, (int)B, (int)Hq, (int)Hkv, (int)(Hq / Hkv), (int)p.tiles,
              (int)p.splits, causal, (float)((double)scale * 1.4426950408889634)};

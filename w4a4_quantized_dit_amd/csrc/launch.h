@@ -156,7 +156,8 @@ hipError_t launch_kv_read(uint16_t* K, int64_t ldk, uint16_t* V, int64_t ldv, in
 int64_t attn_workspace_bytes(int64_t rows, int64_t Hq, int64_t Hkv, int64_t dim, int64_t B,
                              int64_t max_q, int64_t max_kv);
 // Blocks of the launch; at most 2^31.
-int64_t attn_blocks(int64_t Hq, int64_t Hkv, int64_t B, int64_t max_q, int64_t max_kv);
+int64_t attn_blocks(int64_t rows, int64_t Hq, int64_t Hkv, int64_t dim, int64_t B, int64_t max_q,
+                    int64_t max_kv);
 hipError_t launch_attn(const uint16_t* Q, int64_t ldq, int64_t rows, int64_t Hq, int64_t Hkv,
                        int64_t dim, const int32_t* cu, const int32_t* len, int64_t B,
                        int64_t max_q, int64_t max_kv, const int32_t* table, int64_t max_blocks,
