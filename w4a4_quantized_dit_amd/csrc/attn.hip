@@ -85,22 +85,31 @@ struct QueryOp {
   int s_hi, s_lo;  // E8M0 scale operands
 };
 
-// Lane (n, half) of the row's operand: channels 64s + 32·half + 0..31 of step s.
+// A lane's part of its row's query: channels 64s + 32·half + 0..31 of step s.
 template <int DIM>
-__device__ __forceinline__ void query_operand(const uint16_t* q, bool live, int half,
-                                              QueryOp<DIM>& op) {
+struct QueryRow {
   u32x4_t w[DIM / 64][4];
+};
+
+template <int DIM>
+__device__ __forceinline__ void query_load(const uint16_t* q, int half, QueryRow<DIM>& r) {
+#pragma unroll
+  for (int s = 0; s < DIM / 64; ++s)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r.w[s][j] = reinterpret_cast<const u32x4_t*>(q + 64 * s + 32 * half)[j];
+}
+
+template <int DIM>
+__device__ __forceinline__ void query_operand(const QueryRow<DIM>& r, QueryOp<DIM>& op) {
+  const auto& w = r.w;
   float m = 0.0f;
 #pragma unroll
   for (int s = 0; s < DIM / 64; ++s)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      w[s][j] = u32x4_t{0u, 0u, 0u, 0u};
-      if (live) w[s][j] = reinterpret_cast<const u32x4_t*>(q + 64 * s + 32 * half)[j];
+    for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int c = 0; c < 4; ++c)
         m = fmaxf(m, fmaxf(fabsf(bf16_lo(w[s][j][c])), fabsf(bf16_hi(w[s][j][c]))));
-    }
   m = fmaxf(m, __shfl_xor(m, 32));
   const int e = page_exponent(m);
   const float up = two_to(-e);
@@ -247,20 +256,21 @@ __device__ __forceinline__ bf16x8_t weights(State<DIM>& st, const f32x16_t (&z)[
 
 constexpr int kPresent = 1 << 16;
 
-// The lane's page number and exponent bytes (k | v << 8 | kPresent) of logical page `at`; page 0
-// and no flag outside [0, end) or the cache.
-__device__ __forceinline__ void page_meta(const AttnArgs& a, const Seq& s, int at, int end,
-                                          int& page, int& exps) {
-  page = 0;
-  exps = 0;
-  if (at < end) {
-    const int p = a.table[(int64_t)s.b * a.max_blocks + at];
-    if (p >= 0 && p < a.n_pages) {
-      page = p;
-      const int64_t i = (int64_t)p * a.Hkv + s.h;
-      exps = (int)a.ks[i] | (int)a.vs[i] << 8 | kPresent;
-    }
-  }
+// The lane's logical page `at` (of pages [0, end), end >= 1; later ones repeat the last): its
+// number in the cache, −1 outside it.
+__device__ __forceinline__ int page_id(const AttnArgs& a, const Seq& s, int at, int end) {
+  const int p = a.table[(int64_t)s.b * a.max_blocks + (at < end ? at : end - 1)];
+  return p >= 0 && p < a.n_pages ? p : -1;
+}
+
+// Exponent bytes (k | v << 8 | kPresent) of a page, no flag outside the cache; the number of a
+// missing page becomes 0, which can be read.
+__device__ __forceinline__ int page_exps(const AttnArgs& a, const Seq& s, int& page) {
+  const bool there = page >= 0;
+  page = there ? page : 0;
+  const int64_t i = (int64_t)page * a.Hkv + s.h;
+  const int e = (int)a.ks[i] | (int)a.vs[i] << 8;
+  return there ? e | kPresent : 0;
 }
 
 // Output of one row: bf16 and lse, or the unnormalised sums of a split.
@@ -337,8 +347,10 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void k_attn_tile(AttnArgs a) {
   const int lim_row = live ? limit_of(a, s, tok) : 0;
   const int lim_first = __builtin_amdgcn_readfirstlane(w0 < R ? limit_of(a, s, w0 / a.G) : 0);
 
+  // (rows past the last read token 0's; nothing of them is stored)
   QueryOp<DIM> q;
-  query_operand<DIM>(a.Q + (int64_t)(s.first + tok) * a.ldq + (int64_t)head * DIM, live, half, q);
+  QueryRow<DIM> qrow;
+  query_load<DIM>(a.Q + (int64_t)(s.first + tok) * a.ldq + (int64_t)head * DIM, half, qrow);
   State<DIM> st;
   state_init(st);
 
@@ -392,20 +404,25 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void k_attn_tile(AttnArgs a) {
   };
 
   if (p0 < p1) {
-    // lane l: page number and exponents of logical page g0 + l
-    int g0 = p0, meta, meta_e;
-    page_meta(a, s, g0 + lane, p1, meta, meta_e);
+    // lane l: page number and exponents of logical page g0 + l.  The copies need the numbers
+    // only, the exponents come and the query is split while they are on their way.
+    int g0 = p0, meta = page_id(a, s, g0 + lane, p1), meta_e;
     auto lane_of = [&](int i) { return (i < p1 ? i : p1 - 1) - g0; };
     auto page_at = [&](int i) { return __builtin_amdgcn_readlane(meta, lane_of(i)); };
     auto exps_at = [&](int i) { return __builtin_amdgcn_readlane(meta_e, lane_of(i)); };
 
     f32x16_t za[2], zb[2];
-    copy_k(page_at(p0), 0);
-    load_v(page_at(p0));
+    {
+      const int first = page_at(p0), second = page_at(p0 + 1);
+      copy_k(first < 0 ? 0 : first, 0);
+      load_v(first < 0 ? 0 : first);
+      copy_k(second < 0 ? 0 : second, 1);
+      meta_e = page_exps(a, s, meta);
+    }
+    query_operand(qrow, q);
     if (p0 == part_at) trim_v();
-    int e0 = exps_at(p0);
+    const int e0 = exps_at(p0);
     widen_v(e0, 0);
-    copy_k(page_at(p0 + 1), 1);
     load_v(page_at(p0 + 1));
     wait_vmcnt<0>();
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
@@ -425,7 +442,8 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void k_attn_tile(AttnArgs a) {
       asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
       if (i - g0 >= 61) {
         g0 = i;
-        page_meta(a, s, g0 + lane, p1, meta, meta_e);
+        meta = page_id(a, s, g0 + lane, p1);
+        meta_e = page_exps(a, s, meta);
       }
       if (i + 1 == part_at) trim_v();
       // From here to the masks one block without branches, its order fixed: a wave issues in
@@ -541,16 +559,18 @@ __global__ __launch_bounds__(256, 2) void k_attn_few(AttnArgs a) {
   const int lim_first = limit_of(a, s, 0);
 
   QueryOp<DIM> q;
-  query_operand<DIM>(a.Q + (int64_t)(s.first + tok) * a.ldq + (int64_t)head * DIM, live, half, q);
+  QueryRow<DIM> qrow;
+  query_load<DIM>(a.Q + (int64_t)(s.first + tok) * a.ldq + (int64_t)head * DIM, half, qrow);
   State<DIM> st;
   state_init(st);
   const int64_t head_off = (int64_t)s.h * kBytes + lane * 16, page_bytes = (int64_t)a.Hkv * kBytes;
+  query_operand(qrow, q);
   for (int g0 = p0 + wave; g0 < p1; g0 += 256) {
-    int meta, meta_e;
-    page_meta(a, s, g0 + 4 * lane, p1, meta, meta_e);
+    // lane l: logical page g0 + 4 l
+    int meta = page_id(a, s, g0 + 4 * lane, p1);
+    const int meta_e = page_exps(a, s, meta);
     for (int d = 0; d < 64 && g0 + 4 * d < p1; ++d) {
       const int exps = __builtin_amdgcn_readlane(meta_e, d);
-      if (!(exps & kPresent)) continue;
       const int64_t at = __builtin_amdgcn_readlane(meta, d) * page_bytes + head_off;
       u32x4_t kr[kFrags], vr[kFrags];
 #pragma unroll
@@ -561,9 +581,9 @@ __global__ __launch_bounds__(256, 2) void k_attn_few(AttnArgs a) {
       const float scale = two_to(((exps >> 8) & 255) - 127);
       f32x16_t z[2];
       scores<DIM>(z, q, exps & 255, [&](int f) { return kr[f]; });
-      if (t0 + kPage > lim_first) {
-        const int lr = lim_row - t0, lk = s.kv - t0;
-        hide(z, lr > kPage ? kPage : lr, half);
+      if (!(exps & kPresent) || t0 + kPage > lim_first) {
+        const int lr = (exps & kPresent) ? lim_row - t0 : 0, lk = s.kv - t0;
+        hide(z, lr > kPage ? kPage : (lr < 0 ? 0 : lr), half);
 #pragma unroll
         for (int f = 0; f < kFrags; ++f)
           vr[f] = drop_slots(vr[f], f & 1, half, lk > kPage ? kPage : lk);
