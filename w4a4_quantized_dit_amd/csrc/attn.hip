@@ -569,18 +569,23 @@ __global__ __launch_bounds__(256, 2) void k_attn_few(AttnArgs a) {
     // lane l: logical page g0 + 4 l
     int meta = page_id(a, s, g0 + 4 * lane, p1);
     const int meta_e = page_exps(a, s, meta);
-    for (int d = 0; d < 64 && g0 + 4 * d < p1; ++d) {
+    u32x4_t kr[kFrags], vr[kFrags];
+    auto load = [&](u32x4_t (&r)[kFrags], const uint8_t* codes, int page) {
+#pragma unroll
+      for (int f = 0; f < kFrags; ++f)
+        r[f] = *reinterpret_cast<const u32x4_t*>(codes + page * page_bytes + head_off + f * 1024);
+    };
+    const int count = (p1 - g0 + 3) / 4 < 64 ? (p1 - g0 + 3) / 4 : 64;
+    load(kr, a.kc, __builtin_amdgcn_readfirstlane(meta));
+    load(vr, a.vc, __builtin_amdgcn_readfirstlane(meta));
+    for (int d = 0; d < count; ++d) {
       const int exps = __builtin_amdgcn_readlane(meta_e, d);
-      const int64_t at = __builtin_amdgcn_readlane(meta, d) * page_bytes + head_off;
-      u32x4_t kr[kFrags], vr[kFrags];
-#pragma unroll
-      for (int f = 0; f < kFrags; ++f) kr[f] = *reinterpret_cast<const u32x4_t*>(a.kc + at + f * 1024);
-#pragma unroll
-      for (int f = 0; f < kFrags; ++f) vr[f] = *reinterpret_cast<const u32x4_t*>(a.vc + at + f * 1024);
+      const int next = __builtin_amdgcn_readlane(meta, d + 1 < count ? d + 1 : d);
       const int t0 = (g0 + 4 * d) * kPage;
       const float scale = two_to(((exps >> 8) & 255) - 127);
       f32x16_t z[2];
       scores<DIM>(z, q, exps & 255, [&](int f) { return kr[f]; });
+      load(kr, a.kc, next);
       if (!(exps & kPresent) || t0 + kPage > lim_first) {
         const int lr = (exps & kPresent) ? lim_row - t0 : 0, lk = s.kv - t0;
         hide(z, lr > kPage ? kPage : (lr < 0 ? 0 : lr), half);
@@ -599,6 +604,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_few(AttnArgs a) {
             st.o[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
                 widen8(vr[2 * j + tb][2 * g], vr[2 * j + tb][2 * g + 1], scale), p, st.o[j], 0, 0, 0);
         }
+      load(vr, a.vc, next);
     }
   }
   // join the four waves
