@@ -18,8 +18,9 @@
 // sum.  The accumulator of Sᵀ holds, per lane, one row's weights in exactly the token order of
 // the stored V, so P needs no exchange between lanes.
 //
-// The maximum is only raised when a tile exceeds it by more than 2^8: the weights stay below 2^8
-// (exact in range for bf16 and fp32) and most tiles skip the rescaling of O.
+// The maximum is only raised when a page exceeds it by more than 2^8 (few rows) or its weights add
+// up to more than 2^12 (many rows): bf16 and fp32 hold the larger weights as well, and most pages
+// skip the rescaling of O, and with many rows the maximum itself.
 #include "device.h"
 #include "kv_layout.h"
 #include "launch.h"
@@ -33,6 +34,7 @@ typedef __attribute__((address_space(3))) void lvoid_t;
 
 constexpr float kNoMax = -1.0e30f;  // running maximum before the first visible token
 constexpr float kRaise = 8.0f;
+constexpr float kMostSum = 4096.0f;
 
 struct AttnArgs {
   const uint16_t* Q;
@@ -225,18 +227,21 @@ __device__ __forceinline__ float largest(const f32x16_t (&z)[2], float c) {
   return across(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]))) * c;
 }
 
-// Raises the running maximum to the page's where some row needs it.
+// Raises the running maximum to the page's: always, or where some row needs it.
+template <int DIM>
+__device__ __forceinline__ void raise_to(State<DIM>& st, float top) {
+  const float m = fmaxf(st.m, top), f = __builtin_amdgcn_exp2f(st.m - m);
+#pragma unroll
+  for (int j = 0; j < DIM / 32; ++j)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) st.o[j][i] *= f;
+  st.l *= f;
+  st.m = m;
+}
+
 template <int DIM>
 __device__ __forceinline__ void raise(State<DIM>& st, float top) {
-  if (__builtin_amdgcn_ballot_w64(top > st.m + kRaise) != 0) {
-    const float m = fmaxf(st.m, top), f = __builtin_amdgcn_exp2f(st.m - m);
-#pragma unroll
-    for (int j = 0; j < DIM / 32; ++j)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) st.o[j][i] *= f;
-    st.l *= f;
-    st.m = m;
-  }
+  if (__builtin_amdgcn_ballot_w64(top > st.m + kRaise) != 0) raise_to(st, top);
 }
 
 // Weights of 16 tokens (step g of token block tb) as an operand of the product with V.
@@ -394,12 +399,11 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void k_attn_tile(AttnArgs a) {
     scores<DIM>(z, q, exps & 255,
                 [&](int f) { return *reinterpret_cast<const u32x4_t*>(k + f * 1024); });
   };
-  auto mask = [&](int i, int exps, f32x16_t (&z)[2], float& top) {
+  auto mask = [&](int i, int exps, f32x16_t (&z)[2]) {
     const int t0 = i * kPage;
     if (!(exps & kPresent) || t0 + kPage > lim_first) {
       const int lr = (exps & kPresent) ? lim_row - t0 : 0;
       hide(z, lr > kPage ? kPage : (lr < 0 ? 0 : lr), half);
-      top = largest(z, a.c);
     }
   };
 
@@ -427,14 +431,12 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void k_attn_tile(AttnArgs a) {
     wait_vmcnt<0>();
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
     page_scores(e0, 0, za);
-    float top = largest(za, a.c);
-    mask(p0, e0, za, top);
-    raise(st, top);
+    mask(p0, e0, za);
+    raise(st, largest(za, a.c));
 
-    // Page i, whose scores are in z (the maximum raised): its exponentials run while the matrix
-    // units form the next page's scores, and the next page's V is widened and its maximum
-    // taken while they form this page's product.  Pages behind the last repeat it; what is
-    // computed of them is not used.
+    // Page i, whose scores are in z: its exponentials run while the matrix units form the next
+    // page's scores, and the next page's V is widened while they form this page's product.
+    // Pages behind the last repeat it; what is computed of them is not used.
     auto step = [&](int i, int slot, f32x16_t (&z)[2], f32x16_t (&zn)[2]) {
       // K of page i + 1 and V of page i are in LDS for every wave, and every wave is done with
       // what takes their places (V loads of page i + 1 may still be in flight)
@@ -455,6 +457,7 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void k_attn_tile(AttnArgs a) {
       const int k_exp = e1 & 255;
       u32x4_t kr[2][DIM / 32], w[4];
       bf16x8_t vb[4];
+      float sum = 0.0f;
       auto k_read = [&](int tb) {
 #pragma unroll
         for (int f = 0; f < DIM / 32; ++f)
@@ -471,9 +474,10 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void k_attn_tile(AttnArgs a) {
         const int tb = n >> 3, e = 2 * (n & 7);
         const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(z[tb][e], a.c, -st.m));
         const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(z[tb][e + 1], a.c, -st.m));
-        st.l += x + y;
-        w[n >> 2][n & 3] = pack_bf16x2(x, y);
-        asm volatile("" : "+v"(st.l));  // the sum is taken here, not behind the block
+        sum += x + y;
+        uint32_t both = pack_bf16x2(x, y);
+        asm volatile("" : "+v"(sum), "+v"(both));  // formed here, not behind the block
+        w[n >> 2][n & 3] = both;
       };
       constexpr int kQk = 4 * (DIM / 64), kPv = 4 * (DIM / 32);
       k_read(0);
@@ -492,13 +496,26 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void k_attn_tile(AttnArgs a) {
 #pragma unroll
           for (int f = 0; f < 4; ++f) v_read(f);
         }
+        // (fewer behind the first ones: the last scores are ready when the last weights are)
+        constexpr int kEach = 16 / kQk;
 #pragma unroll
-        for (int f = 0; f < 16 / kQk; ++f) pair(n * (16 / kQk) + f);
+        for (int f = n * kEach - (n > 0) - (n > 1); f < (n + 1) * kEach - (n < kQk - 1) - (n > 0 && n < kQk - 1); ++f)
+          pair(f);
         __builtin_amdgcn_sched_barrier(0);
       }
+      asm volatile("" : "+v"(zn[0]), "+v"(zn[1]));  // formed here, not behind the branch
+      // The page's maximum is not taken: the sum of its weights tells when they have grown too
+      // large for the running maximum (a first page's are small, and 32 of at most 1 after a
+      // raise).  Then, seldom, the maximum is raised and the weights are formed again.
+      if (__builtin_amdgcn_ballot_w64(!(sum <= kMostSum)) != 0) {
+        raise_to(st, largest(z, a.c));
+        sum = 0.0f;
+#pragma unroll
+        for (int n = 0; n < 16; ++n) pair(n);
+      }
+      st.l += sum;
       // the next page's V has arrived (the copies of K behind it may be in flight)
       wait_vmcnt<kCopies>();
-      float t4[4];
       const float scale = two_to(((e1 >> 8) & 255) - 127);
 #pragma unroll
       for (int n = 0; n < kPv; ++n) {
@@ -513,18 +530,9 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void k_attn_tile(AttnArgs a) {
               widen8(vr[f][2 * g], vr[f][2 * g + 1], scale);
         }
         if (n == kPv / 2) load_v(ahead);
-        if (n >= kPv / 2) {  // the next page's largest scores
-#pragma unroll
-          for (int k = (n - kPv / 2) * 32 / kPv; k < (n - kPv / 2 + 1) * 32 / kPv; ++k) {
-            const float x = zn[k >> 3][2 * (k & 7)], y = zn[k >> 3][2 * (k & 7) + 1];
-            t4[k & 3] = k < 4 ? fmaxf(x, y) : fmaxf(fmaxf(t4[k & 3], x), y);
-          }
-        }
         __builtin_amdgcn_sched_barrier(0);
       }
-      float top = across(fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]))) * a.c;
-      mask(i + 1, e1, zn, top);
-      raise(st, top);
+      mask(i + 1, e1, zn);
     };
     for (int i = p0; i < p1; i += 2) {
       step(i, 0, za, zb);
@@ -692,7 +700,7 @@ struct Plan {
 // a CU, in rounds of that many: of up to 16 splits the one of the least
 //   rounds · (pages a block + 4 for its ends) + the join's traffic, in pages
 // is taken (1008 rows x 31688 tokens x 40 heads are 320 blocks, five eighths of a round, which
-// took 748 us; three splits, two nearly full rounds of a third, SPLIT_US).
+// took 748 us; three splits, two nearly full rounds of a third, 598).
 Plan plan(int64_t G, int64_t Hkv, int64_t dim, int64_t rows, int64_t B, int64_t max_q,
           int64_t max_kv) {
   Plan p;

@@ -184,15 +184,15 @@ __device__ __forceinline__ void xhat8_lds(u32x4_t h, float inv, const float* g, 
 // read are on different banks.  γ and 1/λ follow through registers.  Every step issues the same
 // loads (past the end the last chunk's again), so that one count waits for the oldest.  Rows past
 // M and ranks past r repeat the last one; what comes of them is not stored.
-constexpr int kDownRows = 128, kChunk = 64, kImages = 3;
+constexpr int kDownWaves = 8, kDownRows = 16 * kDownWaves, kChunk = 64, kImages = 3;
 
 template <int NT>
-__global__ __launch_bounds__(512) void k_norm_down(NormArgs a, DownArgs d) {
+__global__ __launch_bounds__(64 * kDownWaves, 2) void k_norm_down(NormArgs a, DownArgs d) {
   constexpr int kL = NT * 16 * kChunk * 2, kH = kDownRows * kChunk * 2;  // bytes of an image
-  constexpr int kCopies = (2 * NT + 7) / 8;                               // of L1, per wave
+  constexpr int kCopies = (2 * NT + kDownWaves - 1) / kDownWaves;                               // of L1, per wave
   constexpr int kLoads = kCopies + 4;
   __shared__ __attribute__((aligned(16))) uint8_t s_0[kL + kH], s_1[kL + kH], s_2[kL + kH];
-  __shared__ __attribute__((aligned(16))) float s_g[8][kChunk], s_i[8][kChunk];
+  __shared__ __attribute__((aligned(16))) float s_g[kDownWaves][kChunk], s_i[kDownWaves][kChunk];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, rl = lane & 15, q = lane >> 4;
   const int64_t first = (int64_t)(gridDim.x - 1 - blockIdx.x) * kDownRows;
   const int64_t row0 = first + 16 * wave;
@@ -208,7 +208,7 @@ __global__ __launch_bounds__(512) void k_norm_down(NormArgs a, DownArgs d) {
   int f_l[kCopies];
 #pragma unroll
   for (int i = 0; i < kCopies; ++i) {
-    f_l[i] = wave + 8 * i < 2 * NT ? wave + 8 * i : wave % (2 * NT);  // some twice, the same bytes
+    f_l[i] = wave + kDownWaves * i < 2 * NT ? wave + kDownWaves * i : wave % (2 * NT);  // some twice, the same bytes
     const int n = 8 * f_l[i] + lane / 8;
     src_l[i] = a.down + (n < a.r ? n : a.r - 1) * a.K + piece;
   }
@@ -383,7 +383,7 @@ void launch_down(const NormArgs& a, hipStream_t s) {
   else if (rows * NT <= 1280)
     k_norm_down_few<16><<<dim3((unsigned)rows, NT), 64 * kFewWaves, 0, s>>>(a, d);
   else
-    k_norm_down<NT><<<(unsigned)((a.M + kDownRows - 1) / kDownRows), 512, 0, s>>>(a, d);
+    k_norm_down<NT><<<(unsigned)((a.M + kDownRows - 1) / kDownRows), 64 * kDownWaves, 0, s>>>(a, d);
 }
 
 }  // namespace
