@@ -473,7 +473,7 @@ svdq_status svdq_score_modal_rel_l2_ref(const uint16_t* Y, int64_t ldy, const ui
  * bf16; eps > 0.
  * H receives h and is required with a residual (ignored without one); it may be X or residual
  * itself (in place), but must not overlap them otherwise.  codes [M, K], scales [M, K/32].  D may
- * be NULL iff r == 0.  Codes and scales bit-exact: the fp64 sum leaves inv independent of the
+ * be NULL iff r == 0.  M at most 2^28.  Codes and scales bit-exact: the fp64 sum leaves inv independent of the
  * order of summation except where a sum of squares spanning more than 2^24 in magnitude lies
  * next to a rounding border.
  */
@@ -497,7 +497,7 @@ svdq_status svdq_rmsnorm_quant_act(const uint16_t* X, int64_t M, int64_t K, int6
  * int32 [M, n_axes], any values; freq: device fp64 [rot/2], radians per position
  * (svdq_rope_frequencies).  θ is formed and reduced to a turn in fp64.  dim a multiple of 16 in
  * [16, 256]; axis_dims (host int64[n_axes]) even and >= 0, their sum a multiple of 16 in
- * [16, dim]; n_axes in [1, 4].  inverse != 0 is also the gradient of the forward turn.
+ * [16, dim]; n_axes in [1, 4]; M at most 2^28.  inverse != 0 is also the gradient of the forward turn.
  */
 svdq_status svdq_rope_axes(const uint16_t* X, int64_t M, int64_t ldx, int64_t heads, int64_t dim,
                            const int32_t* pos, const double* freq, int64_t n_axes,
@@ -527,7 +527,8 @@ svdq_status svdq_rope_frequencies(int64_t n_axes, const int64_t* axis_dims, doub
  * device int32 [B]).  max_rows: host bound of the rows of one sequence (rows past it are not
  * handled).  Tokens whose block_table entry is missing (past max_blocks) or outside
  * [0, n_pages) are skipped, as are sequences whose cu_rows leave [0, rows].  dim 64 or 128;
- * heads and B at most 65535.  rows == 0 or max_rows == 0: nothing to do.
+ * heads and B at most 65535, rows, max_rows, max_blocks and n_pages at most 2^28.  rows == 0 or
+ * max_rows == 0: nothing to do.
  *
  * svdq_kv_write appends rows of K and V (bf16 [rows, heads·dim], leading dimensions ldk, ldv).
  * Per page and head, for K and V each: a = max|new values of the page|; e = the smallest exponent
@@ -567,7 +568,7 @@ svdq_status svdq_kv_read(uint16_t* K, int64_t ldk, uint16_t* V, int64_t ldv, int
  * Rows of no sequence are left as they were.  lse: fp32 [rows, q_heads], may be NULL.
  * scale > 0 and finite.  max_rows, max_kv: host bounds of one sequence's rows and of kv_len (they
  * size the grid and the split; rows past max_rows are not computed, kv_len itself is not
- * limited by max_kv).  workspace: at least svdq_attn_kv8_workspace_bytes(...) bytes (0 when the
+ * limited by max_kv); max_rows·q_heads at most 2^28.  workspace: at least svdq_attn_kv8_workspace_bytes(...) bytes (0 when the
  * page range is not split; −1: unsupported), 256-byte aligned, the caller's, not shared with a
  * call that may run at the same time.  dim 64 or 128.  fp32 statistics and accumulation, the
  * weights rounded once to bf16; no atomics, results repeat bit for bit.

@@ -37,7 +37,7 @@ def test_norm_refusals(lib):
         assert call(**{k: None}) == NULLP, k
     for k in ("X", "res", "H", "g", "lam", "down", "c", "D"):
         assert call(**{k: MIS}) == SHAPE and "aligned" in _err(lib), k
-    assert call(M=0) == SHAPE and call(M=1 << 31) == SHAPE
+    assert call(M=0) == SHAPE and call(M=(1 << 28) + 1) == SHAPE
     assert call(K=128) == SHAPE and call(K=0) == SHAPE
     assert call(K=33024, ldx=33024, ldr=33024, ldh=33024) == SHAPE
     for k in ("ldx", "ldr", "ldh"):
@@ -123,6 +123,7 @@ def test_attention_refusals(lib):
     for s in (0.0, -1.0, float("nan"), float("inf")):
         assert call(scale=s) == INVALID
     assert call(rows=0) == OK and call(mr=0) == OK
+    assert call(rows=(1 << 28) + 1) == SHAPE and call(rows=1 << 28, mr=1 << 28) == SHAPE
     # a long cache is split: the workspace is checked
     need = lib.svdq_attn_kv8_workspace_bytes(4, 4, 2, 128, 1, 4, 20000)
     assert need > 0 and need % (4 * 4 * 130 * 4) == 0

@@ -218,6 +218,27 @@ def test_missing_pages_are_masked(L, q):
               lse.cpu().numpy().astype(np.float64), qf, 6.0, 0.125, kv)
 
 
+@pytest.mark.parametrize("q,kv,bound", [(3, 100, 1), (20, 5000, 7), (300, 300, 130), (150, 5000, 129)])
+def test_rows_past_the_bound_are_left(L, q, kv, bound):
+    """max_rows below a sequence's rows: the rows past it stay as they were, with a split too, and
+    the others see what they see without the bound (causal by the true number of rows)."""
+    torch = torch_mod()
+    rng = np.random.default_rng(9)
+    c, table = make_cache(rng, [kv, kv], 1, 64)
+    kvc, t = device_cache(L, c), i32(table)
+    Q = dev_bf16(bf16_rne(rng.standard_normal((2 * q, 2 * 64)).astype(np.float32)))
+    cu, ln = i32([0, q, 2 * q]), i32([kv, kv])
+    whole = L.attention(Q, kvc, t, cu, ln, q, kv, causal=True)
+    out = torch.full_like(whole, 7.0)
+    L.attention(Q, kvc, t, cu, ln, bound, kv, causal=True, out=out)
+    torch.cuda.synchronize()
+    for b in range(2):
+        got, want = out[b * q:(b + 1) * q].float(), whole[b * q:(b + 1) * q].float()
+        assert torch.all(got[bound:] == 7.0)
+        # another split of the pages may round each result the other way
+        assert torch.all((got[:bound] - want[:bound]).abs() <= 2.0 ** -6 * want[:bound].abs() + 1e-2)
+
+
 @pytest.mark.parametrize("q,kv", [(1, 3000), (150, 3000), (300, 300)])
 def test_repeats_bit_for_bit(L, q, kv):
     torch = torch_mod()

@@ -127,3 +127,22 @@ def test_feeds_the_mxfp8_product(L):
     Y = L.gemm(codes, scales, None, D, pw, M)
     torch.cuda.synchronize()
     check_y(host_bits(Y), y)
+
+
+@pytest.mark.parametrize("r", [0, 8])
+def test_more_rows_than_blocks(L, r):
+    """2^21 + 5 rows: two launches of the row kernel."""
+    torch = torch_mod()
+    M, K, n = (1 << 21) + 5, 256, 96
+    g = torch.Generator(device="cuda").manual_seed(4)
+    X = torch.randn(M, K, generator=g, device="cuda", dtype=torch.bfloat16)
+    c = _case(1, K, r, False, True, True, seed=9)
+    codes, scales, D, _ = L.norm_quantize_activation(X, dev_bf16(c["gamma"]), dev(c["lam"]),
+                                                     dev_bf16(c["down"]) if r else None)
+    torch.cuda.synchronize()
+    for rows in (slice(0, n), slice(M - n, M)):
+        want = OA.rmsnorm_quant(host_bits(X[rows]), None, c["gamma"], 1e-6, c["lam"], c["down"])
+        assert np.array_equal(codes[rows].cpu().numpy(), want["codes"])
+        assert np.array_equal(scales[rows].cpu().numpy(), want["scales"])
+        if r:
+            check_d(D[rows].cpu().numpy(), want["D"])

@@ -103,3 +103,22 @@ def test_inverse_is_the_gradient(L):
             e[i, 0, j] = 0.5
             diff = f(x + e) - f(x - e)          # linear: exact up to float64 rounding
             assert abs(got[i, j] - diff) <= 2.0 ** -8 * abs(diff) + 2.0 ** -20 * 8
+
+
+def test_more_rows_than_blocks(L):
+    """2^21 + 5 rows: the blocks take a second row each."""
+    torch = torch_mod()
+    from w4a4_quantized_dit_amd import _lib
+    M, n = (1 << 21) + 5, 64
+    freq = _lib.svdq_rope_frequencies([16], 1000.0)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    X = torch.randn(M, 16, generator=g, device="cuda").to(torch.bfloat16)
+    pos = torch.randint(-1000, 1000, (M, 1), generator=g, device="cuda", dtype=torch.int32)
+    Y = L.rope(X, pos, dev(freq), [16], 16)
+    torch.cuda.synchronize()
+    for rows in (slice(0, n), slice(M - n, M)):
+        x = X[rows].float().cpu().numpy().reshape(n, 1, 16).astype(np.float64)
+        want = OA.rope(x, pos[rows].cpu().numpy(), freq, [16], True, False)
+        got = Y[rows].float().cpu().numpy().reshape(n, 1, 16)
+        mag = np.repeat(np.abs(x[..., 0::2]) + np.abs(x[..., 1::2]), 2, axis=-1)
+        assert np.all(np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -20 * mag)

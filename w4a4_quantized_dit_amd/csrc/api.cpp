@@ -100,9 +100,10 @@ svdq_status check_fmt(const char* fn, int fmt) {
   return SVDQ_OK;
 }
 
+// Counts of rows, tokens or pages: a launch has fewer than 2^32 threads in a dimension.
 svdq_status check_rows(const char* fn, const char* name, int64_t n, int64_t least) {
-  if (n < least || n > INT32_MAX)
-    return fail(SVDQ_UNSUPPORTED_SHAPE, "%s: %s=%lld must lie in [%lld, 2^31)", fn, name,
+  if (n < least || n > (1 << 28))
+    return fail(SVDQ_UNSUPPORTED_SHAPE, "%s: %s=%lld must lie in [%lld, 2^28]", fn, name,
                 (long long)n, (long long)least);
   return SVDQ_OK;
 }
@@ -871,7 +872,7 @@ int64_t svdq_attn_kv8_workspace_bytes(int64_t rows, int64_t q_heads, int64_t kv_
                                       int64_t dim, int64_t B, int64_t max_rows, int64_t max_kv) {
   if (rows < 0 || kv_heads < 1 || q_heads < kv_heads || q_heads % kv_heads != 0 ||
       q_heads > 65535 || (dim != 64 && dim != 128) || B < 1 || B > 65535 || max_rows < 0 ||
-      max_kv < 0 || rows > INT32_MAX || max_rows > INT32_MAX || max_kv > INT32_MAX)
+      max_kv < 0 || rows > (1 << 28) || max_rows > (1 << 28) || max_kv > INT32_MAX)
     return -1;
   return svdq::attn_workspace_bytes(rows, q_heads, kv_heads, dim, B, max_rows, max_kv);
 }
@@ -900,8 +901,8 @@ svdq_status svdq_attn_kv8(const uint16_t* Q, int64_t ldq, int64_t rows, int64_t 
   if (!(scale > 0.0f && scale < 1e30f))
     return fail(SVDQ_INVALID_ARG, "%s: scale must be positive and finite", fn);
   if (Q == O) return fail(SVDQ_INVALID_ARG, "%s: O must not be Q", fn);
-  if (max_rows * (q_heads / kv_heads) > INT32_MAX - 256 || rows * (q_heads / kv_heads) > INT32_MAX - 256)
-    return fail(SVDQ_UNSUPPORTED_SHAPE, "%s: more than 2^31 rows of a key head", fn);
+  if (max_rows * q_heads > (1 << 28) || rows * (q_heads / kv_heads) > (1 << 30))
+    return fail(SVDQ_UNSUPPORTED_SHAPE, "%s: more than 2^28 rows and heads in a sequence", fn);
   if (rows == 0 || max_rows == 0) return ok();
   const int64_t need =
       svdq::attn_workspace_bytes(rows, q_heads, kv_heads, dim, B, max_rows, max_kv);
@@ -913,8 +914,8 @@ svdq_status svdq_attn_kv8(const uint16_t* Q, int64_t ldq, int64_t rows, int64_t 
       return fail(SVDQ_UNSUPPORTED_SHAPE, "%s: workspace of %lld bytes, needs %lld", fn,
                   (long long)workspace_bytes, (long long)need);
   }
-  if (svdq::attn_blocks(rows, q_heads, kv_heads, dim, B, max_rows, max_kv) > INT32_MAX)
-    return fail(SVDQ_UNSUPPORTED_SHAPE, "%s: more than 2^31 blocks of rows and heads", fn);
+  if (svdq::attn_blocks(rows, q_heads, kv_heads, dim, B, max_rows, max_kv) >= (1 << 24))
+    return fail(SVDQ_UNSUPPORTED_SHAPE, "%s: more than 2^24 blocks of rows and heads", fn);
   return hip_result(svdq::launch_attn(Q, ldq, rows, q_heads, kv_heads, dim, cu_rows, kv_len, B,
                                       max_rows, max_kv, block_table, max_blocks, n_pages, k_codes,
                                       v_codes, k_scales, v_scales, scale, causal != 0, O, ldo, lse,

@@ -49,7 +49,7 @@ struct AttnArgs {
   const uint8_t* ks;
   const uint8_t* vs;
   int64_t ldq, ldo, rows, max_blocks, n_pages;
-  int B, Hq, Hkv, G, tiles, splits, causal;
+  int B, Hq, Hkv, G, tiles, splits, causal, max_q;
   float c;
 };
 
@@ -58,6 +58,7 @@ struct AttnArgs {
 struct Seq {
   int first;   // packed row of its first token
   int n, kv;   // query tokens, cached tokens
+  int q;       // query tokens that are computed: at most the caller's bound
   int b, h;
 };
 
@@ -68,6 +69,7 @@ __device__ __forceinline__ bool sequence(const AttnArgs& a, int bh, Seq& s) {
   const int end = a.cu[s.b + 1];
   if (s.first < 0 || end <= s.first || end > a.rows) return false;
   s.n = end - s.first;
+  s.q = s.n < a.max_q ? s.n : a.max_q;
   s.kv = a.len[s.b];
   const int64_t room = a.max_blocks * kPage;
   s.kv = s.kv < 0 ? 0 : (s.kv > room ? (int)room : s.kv);
@@ -336,7 +338,7 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void k_attn_tile(AttnArgs a) {
   const int split = (int)((item / a.tiles) % a.splits);
   Seq s;
   if (!sequence(a, (int)(item / a.tiles / a.splits), s)) return;
-  const int R = s.n * a.G, r0 = tile * kTileRows;
+  const int R = s.q * a.G, r0 = tile * kTileRows;
   if (r0 >= R) return;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, half = lane >> 5;
   const int w0 = r0 + 32 * wave, row = w0 + (lane & 31);
@@ -555,7 +557,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_few(AttnArgs a) {
   const int split = (int)(item % a.splits);
   Seq s;
   if (!sequence(a, (int)(item / a.splits), s)) return;
-  const int R = s.n * a.G < 32 ? s.n * a.G : 32;
+  const int R = s.q * a.G;  // at most 32
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, half = lane >> 5, n = lane & 31;
   const bool live = n < R;
   const int tok = live ? n / a.G : 0;
@@ -658,14 +660,16 @@ __global__ __launch_bounds__(256, 2) void k_attn_few(AttnArgs a) {
   }
 }
 
-// The splits of every row joined, one wave per row.  Rows past the last sequence stay as they
-// are.
+// The splits of every row joined, one wave per row of sequence blockIdx.y.
 template <int DIM>
 __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
-  const int64_t at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int lane = threadIdx.x & 63;
-  const int64_t token = at / a.Hq;
-  if (token >= a.rows || token >= a.cu[a.B]) return;
+  const int b = blockIdx.y, lane = threadIdx.x & 63;
+  const int first = a.cu[b], end = a.cu[b + 1];
+  if (first < 0 || end <= first || end > a.rows) return;
+  const int n = end - first < a.max_q ? end - first : a.max_q;
+  const int64_t local = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (local >= (int64_t)n * a.Hq) return;
+  const int64_t at = (int64_t)first * a.Hq + local, token = at / a.Hq;
   const int head = (int)(at % a.Hq);
   const int64_t each = a.rows * a.Hq;
   const float* ml = a.part + a.splits * each * DIM + at * 2;
@@ -753,7 +757,7 @@ hipError_t launch_attn(const uint16_t* Q, int64_t ldq, int64_t rows, int64_t Hq,
   const Plan p = plan(Hq / Hkv, Hkv, dim, rows, B, max_q, max_kv);
   AttnArgs a{Q, O, lse, (float*)workspace, cu, len, table, kc, vc, ks, vs, ldq, ldo, rows,
              max_blocks, n_pages, (int)B, (int)Hq, (int)Hkv, (int)(Hq / Hkv), (int)p.tiles,
-             (int)p.splits, causal, (float)((double)scale * 1.4426950408889634)};
+             (int)p.splits, causal, (int)max_q, (float)((double)scale * 1.4426950408889634)};
   const int64_t items = B * Hkv * p.tiles * p.splits;
   const unsigned grid = (unsigned)(p.few ? items : (items + 7) / 8 * 8);
   if (p.few) {
@@ -769,7 +773,7 @@ hipError_t launch_attn(const uint16_t* Q, int64_t ldq, int64_t rows, int64_t Hq,
   }
   if (hipError_t e = hipGetLastError()) return e;
   if (p.splits > 1) {
-    const unsigned joins = (unsigned)((rows * Hq + 3) / 4);
+    const dim3 joins((unsigned)((max_q * Hq + 3) / 4), (unsigned)B);
     if (dim == 64)
       k_attn_join<64><<<joins, 256, 0, s>>>(a);
     else

@@ -108,11 +108,11 @@ __device__ __forceinline__ uint2 codes8(const float (&x)[8], int e) {
 // the first element of every 4 of its D row for the product kernels below, whose blocks read
 // it before they write these elements of D.
 template <int TPR, int NV>
-__global__ __launch_bounds__(TPR) void k_norm_row(NormArgs a) {
+__global__ __launch_bounds__(TPR) void k_norm_row(NormArgs a, int64_t first) {
   __shared__ double s_part[TPR / 64];
   const int t = threadIdx.x;
-  const int64_t row = blockIdx.x;
   const int nv = (int)(a.K / 8);
+  const int64_t row = first + blockIdx.x;
   u32x4_t h[NV];
   double s = 0.0;
 #pragma unroll
@@ -395,15 +395,18 @@ hipError_t launch_norm_quant(const uint16_t* X, int64_t M, int64_t K, int64_t ld
                              float* D, hipStream_t s) {
   const NormArgs a{X, residual, H, gamma, lambda, down, codes, scales, D, M, K, ldx, ldr, ldh,
                    (double)eps, (int)r};
-  const unsigned grid = (unsigned)M;
-  if (K <= 2048)
-    k_norm_row<256, 1><<<grid, 256, 0, s>>>(a);
-  else if (K <= 6144)
-    k_norm_row<256, 3><<<grid, 256, 0, s>>>(a);
-  else if (K <= 8192)
-    k_norm_row<256, 4><<<grid, 256, 0, s>>>(a);
-  else
-    k_norm_row<1024, 4><<<grid, 1024, 0, s>>>(a);
+  // a launch has fewer than 2^32 threads
+  for (int64_t first = 0; first < M; first += 1 << 21) {
+    const unsigned grid = (unsigned)(M - first < (1 << 21) ? M - first : (1 << 21));
+    if (K <= 2048)
+      k_norm_row<256, 1><<<grid, 256, 0, s>>>(a, first);
+    else if (K <= 6144)
+      k_norm_row<256, 3><<<grid, 256, 0, s>>>(a, first);
+    else if (K <= 8192)
+      k_norm_row<256, 4><<<grid, 256, 0, s>>>(a, first);
+    else
+      k_norm_row<1024, 4><<<grid, 1024, 0, s>>>(a, first);
+  }
   if (hipError_t e = hipGetLastError()) return e;
   switch ((r + 15) / 16) {
     case 0: break;
