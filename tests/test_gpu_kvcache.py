@@ -179,3 +179,23 @@ def test_refusals_of_the_binding(L):
     with pytest.raises(ValueError):
         L.kv_write(L.KVCache(kv.k_codes, kv.v_codes, kv.k_scales[:1], kv.v_scales, 64), X, X, *good)
     torch.cuda.synchronize()
+
+
+def test_large_read_back(L):
+    """Outputs past 256 MB are stored past the caches: the same values."""
+    torch = torch_mod()
+    n, H, dim = 4300, 128, 128
+    g = torch.Generator(device="cuda").manual_seed(5)
+    X = [torch.randn(n, H * dim, generator=g, device="cuda", dtype=torch.bfloat16) for _ in range(2)]
+    pages = (n + 63) // 64
+    kv = L.kv_cache(pages, H, dim)
+    table = torch.randperm(pages, generator=g, device="cuda").int()[None]
+    L.kv_write(kv, X[0], X[1], table, i32([0, n]), i32([0]), n)
+    whole = L.kv_read(kv, table, i32([0, n]), i32([0]), n, n)
+    parts = [L.kv_read(kv, table, i32([0, 1075]), i32([a]), 1075, 1075) for a in range(0, n, 1075)]
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert torch.equal(whole[i], torch.cat([p[i] for p in parts]))
+        err = (whole[i].float() - X[i].float()).abs()
+        # half a step of E4M3, or of its smallest step under the page's scale
+        assert torch.all(err <= 2.0 ** -4 * X[i].float().abs() + 2.0 ** -10 * 8 / 448)

@@ -62,7 +62,7 @@ def test_axes_and_layouts(L, dim, axes, inter, inverse):
     _run(L, 13, 5, dim, axes, inter, inverse)
 
 
-@pytest.mark.parametrize("M,heads", [(1, 1), (1, 80), (3, 2), (700, 17), (5000, 3), (2, 200)])
+@pytest.mark.parametrize("M,heads", [(1, 1), (1, 80), (3, 2), (700, 17), (5000, 3), (2, 200), (21000, 50)])
 @pytest.mark.parametrize("inter", [True, False])
 def test_row_and_head_counts(L, M, heads, inter):
     _run(L, M, heads, 128, [44, 42, 42], inter, False, seed=M)

@@ -583,7 +583,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_few(AttnArgs a) {
     auto load = [&](u32x4_t (&r)[kFrags], const uint8_t* codes, int page) {
 #pragma unroll
       for (int f = 0; f < kFrags; ++f)
-        r[f] = *reinterpret_cast<const u32x4_t*>(codes + page * page_bytes + head_off + f * 1024);
+        r[f] = load_nt(codes + page * page_bytes + head_off + f * 1024);
     };
     const int count = (p1 - g0 + 3) / 4 < 64 ? (p1 - g0 + 3) / 4 : 64;
     load(kr, a.kc, __builtin_amdgcn_readfirstlane(meta));

@@ -36,6 +36,25 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t raw_rsrc(const void* base, uin
 // Cache-policy operand of a streaming (nontemporal) buffer load.
 constexpr int kNt = 2;
 
+// 16 bytes that are not read again (nontemporal load).
+__device__ __forceinline__ u32x4_t load_nt(const void* p) {
+  return __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(p));
+}
+
+// 16 bytes stored, past the caches where NT.
+template <bool NT>
+__device__ __forceinline__ void store16(void* p, u32x4_t v) {
+  if (NT)
+    __builtin_nontemporal_store(v, reinterpret_cast<u32x4_t*>(p));
+  else
+    *reinterpret_cast<u32x4_t*>(p) = v;
+}
+// Outputs larger than the cache in front of HBM (256 MB) that this call does not read again are
+// stored past the caches: 649 MB of rotated heads 239 -> 224 us, 336 MB of keys and values read
+// back 91 -> 56 us; smaller ones are kept for their reader (34 MB read back: 13 us, past the
+// caches 15).
+constexpr int64_t kPastCaches = (int64_t)256 << 20;
+
 // s_waitcnt vmcnt(n) (other counters untouched), gfx9 encoding
 template <int N>
 __device__ __forceinline__ void wait_vmcnt() {

@@ -119,8 +119,8 @@ __global__ __launch_bounds__(256) void k_kv_write(KvArgs a) {
     for (int i = 0; i < 4; ++i) {
       x[kv][i] = u32x4_t{0u, 0u, 0u, 0u};
       if (t + i >= w.lo && t + i < w.hi)
-        x[kv][i] = *reinterpret_cast<const u32x4_t*>(
-            (kv ? a.V : a.K) + (w.row0 + t + i - w.lo) * (kv ? a.ldv : a.ldk) + (int64_t)h * DIM + d);
+        x[kv][i] = load_nt((kv ? a.V : a.K) + (w.row0 + t + i - w.lo) * (kv ? a.ldv : a.ldk) +
+                           (int64_t)h * DIM + d);
     }
   if (entry < 0 || entry >= a.n_pages) return;
   const int64_t at = entry * a.heads + h;
@@ -202,7 +202,7 @@ __global__ __launch_bounds__(256) void k_kv_write(KvArgs a) {
   if (tid < 2) scale[tid][0] = (uint8_t)(e[tid] + 127);
 }
 
-template <int DIM>
+template <int DIM, bool NT>
 __global__ __launch_bounds__(256) void k_kv_read(KvArgs a) {
   constexpr int kThreads = kUnits<DIM>, kBytes = kPage * DIM;
   __shared__ __attribute__((aligned(16))) uint8_t img[2][kBytes];
@@ -243,8 +243,8 @@ __global__ __launch_bounds__(256) void k_kv_read(KvArgs a) {
       ko[j] = pack_bf16x2(value(c, 2 * (j & 1)) * s[0], value(c, 2 * (j & 1) + 1) * s[0]);
       vo[j] = pack_bf16x2(value(v[2 * j], i) * s[1], value(v[2 * j + 1], i) * s[1]);
     }
-    *reinterpret_cast<u32x4_t*>(a.Ko + row * a.ldk + col) = ko;
-    *reinterpret_cast<u32x4_t*>(a.Vo + row * a.ldv + col) = vo;
+    store16<NT>(a.Ko + row * a.ldk + col, ko);
+    store16<NT>(a.Vo + row * a.ldv + col, vo);
   }
 }
 
@@ -275,10 +275,13 @@ hipError_t launch_kv_read(uint16_t* K, int64_t ldk, uint16_t* V, int64_t ldv, in
                  const_cast<uint8_t*>(kc), const_cast<uint8_t*>(vc), const_cast<uint8_t*>(ks),
                  const_cast<uint8_t*>(vs), heads};
   const dim3 grid((unsigned)((max_n + kPage - 2) / kPage + 1), (unsigned)heads, (unsigned)B);
+  const bool nt = rows * heads * dim * 4 > kPastCaches;
   if (dim == 64)
-    k_kv_read<64><<<grid, kUnits<64>, 0, s>>>(a);
+    nt ? k_kv_read<64, true><<<grid, kUnits<64>, 0, s>>>(a)
+       : k_kv_read<64, false><<<grid, kUnits<64>, 0, s>>>(a);
   else
-    k_kv_read<128><<<grid, kUnits<128>, 0, s>>>(a);
+    nt ? k_kv_read<128, true><<<grid, kUnits<128>, 0, s>>>(a)
+       : k_kv_read<128, false><<<grid, kUnits<128>, 0, s>>>(a);
   return hipGetLastError();
 }
 

@@ -120,9 +120,9 @@ __global__ __launch_bounds__(TPR) void k_norm_row(NormArgs a, int64_t first) {
     const int v = t + TPR * i;
     h[i] = u32x4_t{0u, 0u, 0u, 0u};
     if (v < nv) {
-      h[i] = load16(a.X + row * a.ldx + 8 * v);
+      h[i] = load_nt(a.X + row * a.ldx + 8 * v);
       if (a.res) {
-        h[i] = add8(h[i], load16(a.res + row * a.ldr + 8 * v));
+        h[i] = add8(h[i], load_nt(a.res + row * a.ldr + 8 * v));
         *reinterpret_cast<u32x4_t*>(a.H + row * a.ldh + 8 * v) = h[i];
       }
       s += sq8(h[i]);
