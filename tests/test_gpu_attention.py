@@ -218,6 +218,33 @@ def test_missing_pages_are_masked(L, q):
               lse.cpu().numpy().astype(np.float64), qf, 6.0, 0.125, kv)
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("q,kv", [(1, 400), (70, 400), (3, 5000), (150, 5000)])
+@pytest.mark.parametrize("causal", [False, True])
+def test_missing_pages_beside_a_garbage_page(L, q, kv, dim, causal):
+    """Page 0, which no sequence owns, holds NaN codes: nothing of it shows where pages are missing."""
+    torch = torch_mod()
+    rng = np.random.default_rng(17)
+    c, table = make_cache(rng, [kv], 1, dim)
+    for name in ("kc", "vc", "ks", "vs"):     # page 0 <-> the one that holds nothing
+        free = next(p for p in range(len(c[name])) if p not in table) if 0 in table else 0
+        c[name][[0, free]] = c[name][[free, 0]]
+    table = np.where(table == 0, free, table)
+    assert np.all(c["vc"][0] == 0xFF)
+    for miss in ([0], [1, 3], [table.shape[1] - 1], list(range(table.shape[1]))):
+        t = table.copy()
+        t[0, miss] = -1
+        bits = bf16_rne(rng.standard_normal((q, dim)).astype(np.float32))
+        O, lse = L.attention(dev_bf16(bits), device_cache(L, c), i32(t), i32([0, q]), i32([kv]), q,
+                             kv, causal=causal, return_lse=True)
+        torch.cuda.synchronize()
+        assert torch.isfinite(O.float()).all()
+        qf = bf16_bits_to_f32(bits).reshape(q, 1, dim)
+        want = OA.attention(qf, c, t, np.array([0, q]), [kv], float(np.float32(dim ** -0.5)), causal)
+        check(want, O.float().cpu().numpy().reshape(q, 1, dim).astype(np.float64),
+              lse.cpu().numpy().astype(np.float64), qf, 6.0, dim ** -0.5, kv)
+
+
 @pytest.mark.parametrize("q,kv,bound", [(3, 100, 1), (20, 5000, 7), (300, 300, 130), (150, 5000, 129)])
 def test_rows_past_the_bound_are_left(L, q, kv, bound):
     """max_rows below a sequence's rows: the rows past it stay as they were, with a split too, and

@@ -167,7 +167,7 @@ __device__ __forceinline__ bf16x8_t widen8(uint32_t lo, uint32_t hi, float scale
 }
 
 // A lane's 16 bytes of a V fragment (tokens 32·tb on) without the slots past the page's n tokens,
-// which may hold any byte, NaN codes among them.
+// which may hold any byte, NaN codes among them: a weight of 0 would not hide those.
 __device__ __forceinline__ u32x4_t drop_slots(u32x4_t v, int tb, int half, int n) {
 #pragma unroll
   for (int d = 0; d < 4; ++d) {
@@ -378,12 +378,14 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void k_attn_tile(AttnArgs a) {
     for (int i = 0; i < kCopies; ++i)
       vr[i] = *reinterpret_cast<const u32x4_t*>(v_src + page * page_bytes + i * 1024);
   };
-  // the sequence's last page may hold fewer tokens than slots
-  const int part = __builtin_amdgcn_readfirstlane(s.kv % kPage);
-  const int part_at = __builtin_amdgcn_readfirstlane(part ? s.kv / kPage : -1);
-  auto trim_v = [&] {
+  // the sequence's last page may hold fewer tokens than slots, and a page outside the cache (page 0
+  // is read in its place) holds none
+  const int whole = s.kv / kPage;
+  auto trim_v = [&](int i, int exps) {
+    if (i < whole && (exps & kPresent)) return;
+    const int n = i == whole && (exps & kPresent) ? s.kv % kPage : 0;
 #pragma unroll
-    for (int i = 0; i < kCopies; ++i) vr[i] = drop_slots(vr[i], (wave * kCopies + i) & 1, half, part);
+    for (int f = 0; f < kCopies; ++f) vr[f] = drop_slots(vr[f], (wave * kCopies + f) & 1, half, n);
   };
   // fragment f: its two 16-token steps of 1 KB each
   auto widen_v = [&](int exps, int slot) {
@@ -402,10 +404,10 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void k_attn_tile(AttnArgs a) {
                 [&](int f) { return *reinterpret_cast<const u32x4_t*>(k + f * 1024); });
   };
   auto mask = [&](int i, int exps, f32x16_t (&z)[2]) {
-    const int t0 = i * kPage;
-    if (!(exps & kPresent) || t0 + kPage > lim_first) {
-      const int lr = (exps & kPresent) ? lim_row - t0 : 0;
-      hide(z, lr > kPage ? kPage : (lr < 0 ? 0 : lr), half);
+    if (!(exps & kPresent) || i >= lim_first / kPage) {
+      const uint32_t t0 = (uint32_t)i * kPage, lim = (uint32_t)lim_row;
+      const uint32_t lr = (exps & kPresent) && lim > t0 ? lim - t0 : 0u;
+      hide(z, lr > kPage ? kPage : (int)lr, half);
     }
   };
 
@@ -426,8 +428,8 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void k_attn_tile(AttnArgs a) {
       meta_e = page_exps(a, s, meta);
     }
     query_operand(qrow, q);
-    if (p0 == part_at) trim_v();
     const int e0 = exps_at(p0);
+    trim_v(p0, e0);
     widen_v(e0, 0);
     load_v(page_at(p0 + 1));
     wait_vmcnt<0>();
@@ -449,10 +451,11 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void k_attn_tile(AttnArgs a) {
         meta = page_id(a, s, g0 + lane, p1);
         meta_e = page_exps(a, s, meta);
       }
-      if (i + 1 == part_at) trim_v();
+      const int e1 = exps_at(i + 1);
+      trim_v(i + 1, e1);
       // From here to the masks one block without branches, its order fixed: a wave issues in
       // order, so what is to run under a matrix instruction has to stand right behind it.
-      const int ahead = page_at(i + 2), e1 = exps_at(i + 1);
+      const int ahead = page_at(i + 2);
       copy_k(ahead, slot);
       const uint8_t* kp = (slot ? k_img0 : k_img1) + lane * 16;
       const uint8_t* vp = v_img[slot] + lane * 16;
@@ -596,8 +599,8 @@ __global__ __launch_bounds__(256, 2) void k_attn_few(AttnArgs a) {
       f32x16_t z[2];
       scores<DIM>(z, q, exps & 255, [&](int f) { return kr[f]; });
       load(kr, a.kc, next);
-      if (!(exps & kPresent) || t0 + kPage > lim_first) {
-        const int lr = (exps & kPresent) ? lim_row - t0 : 0, lk = s.kv - t0;
+      if (!(exps & kPresent) || t0 > lim_first - kPage) {
+        const int lr = (exps & kPresent) ? lim_row - t0 : 0, lk = (exps & kPresent) ? s.kv - t0 : 0;
         hide(z, lr > kPage ? kPage : (lr < 0 ? 0 : lr), half);
 #pragma unroll
         for (int f = 0; f < kFrags; ++f)
