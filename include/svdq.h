@@ -531,12 +531,13 @@ svdq_status svdq_rope_frequencies(int64_t n_axes, const int64_t* axis_dims, doub
  * max_rows == 0: nothing to do.
  *
  * svdq_kv_write appends rows of K and V (bf16 [rows, heads·dim], leading dimensions ldk, ldv).
- * Per page and head, for K and V each: a = max|new values of the page|; e = the smallest exponent
- * with a <= 448·2^e, within [−110, 119] (−110 for a == 0); if the page already holds tokens
+ * Per page and head, for K and V each: a = max|finite new values of the page|; e = the smallest
+ * exponent with a <= 448·2^e, within [−110, 119] (−110 for a == 0); if the page already holds tokens
  * before start[b], e is at least the stored exponent, and where it grows the earlier codes are
  * rounded again, E4M3(code·2^(e_old − e)).  code = E4M3(x·2^−e), nearest even, saturating;
- * scale byte = e + 127.  The page's later slots keep their bytes.  Bit-exact.  Two sequences
- * must not write the same page in one call.
+ * scale byte = e + 127.  An infinity or NaN becomes the NaN code 0xFF and leaves the page's other
+ * tokens as they would be without it.  The page's later slots keep their bytes.  Bit-exact.  No
+ * page may be written twice in one call, by one sequence or by two.
  *
  * svdq_kv_read writes the values of tokens start[b] .. of each sequence to K and V (bf16, exact).
  * Rows of skipped tokens are left as they were.
@@ -565,6 +566,10 @@ svdq_status svdq_kv_read(uint16_t* K, int64_t ldk, uint16_t* V, int64_t ldv, int
  * each sequence (limited to 64·max_blocks).  Row i of a sequence of n rows sees tokens
  * [0, kv_len), with causal != 0 [0, kv_len − n + i + 1): the last row sees every token.  A row
  * that sees none gets O = 0 and lse = −inf.  Tokens in pages outside [0, n_pages) are masked.
+ * Codes of tokens that a row does not see have no part in its result, NaN codes included; a NaN
+ * in a key that it sees, or an infinity or NaN in its query, makes the row and its lse NaN, one in
+ * a value that it sees that channel.  Scores up to 2^27 in magnitude (fp32 holds no difference
+ * between larger ones).
  * Rows of no sequence are left as they were.  lse: fp32 [rows, q_heads], may be NULL.
  * scale > 0 and finite.  max_rows, max_kv: host bounds of one sequence's rows and of kv_len (they
  * size the grid and the split; rows past max_rows are not computed, kv_len itself is not

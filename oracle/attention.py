@@ -10,7 +10,7 @@ is defined by the formulas here:
   cache  pages of 64 tokens; per page and head (K and V apart) value = code·2^(byte - 127), the
          exponent the smallest e with max|x| <= 448·2^e in [-110, 119] (-110 for an all-zero
          page); on a page with earlier tokens not below the stored one, the earlier codes rounded
-         again where it grows
+         again where it grows; infinities and NaN have no part in it and become code 0xFF
   attn   softmax over the visible tokens in float64; a row that sees none: 0, lse -inf
 """
 import numpy as np
@@ -83,6 +83,17 @@ def page_exponent(a):
     return e
 
 
+def _encode(x):
+    """E4M3 codes, 0xFF for NaN."""
+    c = e4m3_encode_signed(np.where(np.isnan(x), 0, x).astype(F32))
+    return np.where(np.isnan(x), np.uint8(0xFF), c)
+
+
+def _decode(codes):
+    nan = (codes & 0x7F) == 0x7F
+    return np.where(nan, np.nan, e4m3_decode(np.where(nan, np.uint8(0), codes)))
+
+
 def new_cache(n_pages, heads, dim, fill=0):
     """kc, vc [pages, heads, 64·dim], ks, vs [pages, heads], every byte `fill`."""
     return dict(kc=np.full((n_pages, heads, PAGE * dim), fill, np.uint8),
@@ -92,11 +103,13 @@ def new_cache(n_pages, heads, dim, fill=0):
 
 
 def kv_write(cache, K_bits, V_bits, table, cu, start):
-    """Appends in place; pages outside the table or the cache are skipped."""
+    """Appends in place; pages outside the table or the cache are skipped.  Infinities and NaN have
+    no part in the scale and become the code 0xFF."""
     dim, (n_pages, heads) = cache["dim"], cache["ks"].shape
     for is_v, bits, codes, scales in ((0, K_bits, cache["kc"], cache["ks"]),
                                       (1, V_bits, cache["vc"], cache["vs"])):
         x = bf16_bits_to_f32(bits).reshape(-1, heads, dim)
+        x = np.where(np.isfinite(x), x, F32(np.nan))
         place = _place(dim, is_v)
         for b in range(len(cu) - 1):
             n, s = cu[b + 1] - cu[b], start[b]
@@ -107,16 +120,16 @@ def kv_write(cache, K_bits, V_bits, table, cu, start):
                 lo, hi = max(0, s - PAGE * p), min(PAGE, s + n - PAGE * p)
                 rows = x[cu[b] + PAGE * p + lo - s:cu[b] + PAGE * p + hi - s]
                 for h in range(heads):
-                    e = page_exponent(np.abs(rows[:, h]).max())
+                    e = page_exponent(np.nan_to_num(np.abs(rows[:, h]), nan=0.0).max())
                     if lo > 0:
                         e0 = int(np.clip(int(scales[page, h]) - 127, E_MIN, E_MAX))
                         e = max(e, e0)
                         if e > e0:
                             at = place[:lo]
-                            old = e4m3_decode(codes[page, h, at]) * 2.0 ** (e0 - e)
-                            codes[page, h, at] = e4m3_encode_signed(old.astype(F32))
+                            old = _decode(codes[page, h, at]) * 2.0 ** (e0 - e)
+                            codes[page, h, at] = _encode(old)
                     scaled = (rows[:, h].astype(np.float64) * 2.0 ** -e).astype(F32)
-                    codes[page, h, place[lo:hi]] = e4m3_encode_signed(scaled)
+                    codes[page, h, place[lo:hi]] = _encode(scaled)
                     scales[page, h] = e + 127
 
 
@@ -130,7 +143,7 @@ def kv_values(cache, table_row, n, head, is_v):
         if p >= len(table_row) or not 0 <= table_row[p] < n_pages:
             continue
         m = min(PAGE, n - PAGE * p)
-        v = e4m3_decode(codes[table_row[p], head, place[:m]])
+        v = _decode(codes[table_row[p], head, place[:m]])
         out[PAGE * p:PAGE * p + m] = v * 2.0 ** (int(scales[table_row[p], head]) - 127)
         ok[PAGE * p:PAGE * p + m] = True
     return out, ok
@@ -138,7 +151,8 @@ def kv_values(cache, table_row, n, head, is_v):
 
 def attention(Q, cache, table, cu, kv_len, scale, causal):
     """Q float [rows, q_heads, dim]: dict(O, lse float64, absO = Σ p|v|, absz = scale·max_t
-    Σ_d |q_d k_td| of every row, the magnitudes that rounding errors are relative to)."""
+    Σ_d |q_d k_td| of every row, the magnitudes that rounding errors are relative to).  What a row
+    does not see has no part in it, NaN included; a query with an infinity or NaN is NaN."""
     rows, Hq, dim = Q.shape
     H = cache["ks"].shape[1]
     G = Hq // H
@@ -156,16 +170,20 @@ def attention(Q, cache, table, cu, kv_len, scale, causal):
             for g in range(G):
                 j = h * G + g
                 q = Q[cu[b]:cu[b + 1], j].astype(np.float64)
+                q = np.where(np.isfinite(q).all(axis=1, keepdims=True), q, np.nan)
                 z = np.where(vis, scale * (q @ k.T), -np.inf)
                 m = z.max(axis=1, keepdims=True)
-                m = np.where(np.isinf(m), 0.0, m)
+                m = np.where(np.isneginf(m), 0.0, m)
                 p = np.exp(z - m)
                 l = p.sum(axis=1, keepdims=True)
-                some = l[:, 0] > 0
-                p = p / np.where(l > 0, l, 1.0)
-                O[cu[b]:cu[b + 1], j] = p @ v
-                absO[cu[b]:cu[b + 1], j] = p @ np.abs(v)
-                absz[cu[b]:cu[b + 1], j] = scale * (np.abs(q) @ np.abs(k).T).max(axis=1)
+                some = l[:, 0] != 0
+                p = p / np.where(l != 0, l, 1.0)
+                seen_nan = np.where(vis.astype(np.float64) @ np.isnan(v) > 0, np.nan, 0.0)
+                v0 = np.nan_to_num(v, nan=0.0)
+                O[cu[b]:cu[b + 1], j] = p @ v0 + seen_nan
+                absO[cu[b]:cu[b + 1], j] = p @ np.abs(v0)
+                absz[cu[b]:cu[b + 1], j] = scale * np.nan_to_num(
+                    np.abs(q) @ np.nan_to_num(np.abs(k)).T).max(axis=1)
                 with np.errstate(divide="ignore"):
                     lse[cu[b]:cu[b + 1], j] = np.where(some, m[:, 0] + np.log(l[:, 0]), -np.inf)
     return dict(O=O, lse=lse, absO=absO, absz=absz)

@@ -245,6 +245,83 @@ def test_missing_pages_beside_a_garbage_page(L, q, kv, dim, causal):
               lse.cpu().numpy().astype(np.float64), qf, 6.0, dim ** -0.5, kv)
 
 
+def check_with_nan(want, O, lse, q, kmax, scale, tokens, what=""):
+    """NaN exactly where the oracle has it, the rest as in `check`."""
+    assert np.array_equal(np.isnan(O), np.isnan(want["O"])), what
+    assert np.array_equal(np.isnan(lse), np.isnan(want["lse"])), what
+    clean = {k: np.nan_to_num(v, nan=0.0, neginf=-np.inf) for k, v in want.items()}
+    check(clean, np.nan_to_num(O), np.nan_to_num(lse, neginf=-np.inf), q, kmax, scale, tokens, what)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("G", [1, 2])
+@pytest.mark.parametrize("q,kv", [(1, 70), (1, 5000), (3, 130), (15, 4100), (64, 64), (70, 300),
+                                  (150, 5000), (300, 300)])
+@pytest.mark.parametrize("causal", [False, True])
+def test_nan_in_seen_and_hidden_tokens(L, q, kv, G, dim, causal):
+    """Infinities and NaN in keys, values and queries: they show where they are seen, and a row that
+    does not see a token has nothing of it, in the pages that its block shares with later rows too."""
+    torch = torch_mod()
+    rng = np.random.default_rng(q + kv)
+    B, H, Hq = 2, 1, G
+    for where in ("v", "k", "q", "all"):
+        pages = (kv + 63) // 64
+        c = OA.new_cache(2 * pages + 1, H, dim, fill=0xFF)
+        table = rng.permutation(2 * pages + 1)[:2 * pages].reshape(2, pages)
+        K, V = (bf16_rne(rng.standard_normal((2 * kv, H * dim)).astype(np.float32)) for _ in range(2))
+        bits = bf16_rne(rng.standard_normal((2 * q, Hq * dim)).astype(np.float32))
+        late = max(0, kv - q) + rng.integers(0, min(q, kv), 3)     # tokens that some rows see
+        if where in ("v", "all"):
+            V[late, rng.integers(0, dim, 3)] = [0x7FC0, 0x7F80, 0xFF80]
+            V[kv - 1, dim - 1] = 0x7FC0
+        if where in ("k", "all"):
+            K[kv + late[:1], rng.integers(0, dim, 1)] = 0x7FC0     # the second sequence's
+        if where in ("q", "all"):
+            bits[[q // 2, 2 * q - 1], [3, Hq * dim - 1]] = [0x7FC0, 0xFF80]
+        OA.kv_write(c, K, V, table, np.array([0, kv, 2 * kv]), [0, 0])
+        cu = np.array([0, q, 2 * q])
+        O, lse = L.attention(dev_bf16(bits), device_cache(L, c), i32(table), i32(cu), i32([kv, kv]),
+                             q, kv, causal=causal, return_lse=True)
+        torch.cuda.synchronize()
+        qf = bf16_bits_to_f32(bits).reshape(2 * q, Hq, dim)
+        with np.errstate(invalid="ignore"):
+            want = OA.attention(qf, c, table, cu, [kv, kv], float(np.float32(dim ** -0.5)), causal)
+        assert np.isnan(want["O"]).any()
+        check_with_nan(want, O.float().cpu().numpy().reshape(2 * q, Hq, dim).astype(np.float64),
+                       lse.cpu().numpy().astype(np.float64), np.nan_to_num(qf, posinf=0, neginf=0),
+                       6.0, dim ** -0.5, kv, where)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("q", [1, 40])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_very_large_scores(L, q, dim, sign):
+    """Scores of one sign up to 2^26, exact in fp32 (one channel, powers of two and their sums of few
+    bits): the largest takes the whole weight, and lse is that score."""
+    torch = torch_mod()
+    n = 200
+    K = np.zeros((n, dim), np.float32)
+    K[:, 5] = sign * 2.0 ** 13 * (1 + (np.arange(n) * 37 % n) / n)
+    V = np.random.default_rng(3).standard_normal((n, dim)).astype(np.float32)
+    Q = np.zeros((q, dim), np.float32)
+    Q[:, 5] = 2.0 ** 12
+    c = OA.new_cache(4, 1, dim)
+    table = np.array([[2, 0, 3, 1]])
+    OA.kv_write(c, bf16_rne(K), bf16_rne(V), table, np.array([0, n]), [0])
+    bits = bf16_rne(Q)
+    O, lse = L.attention(dev_bf16(bits), device_cache(L, c), i32(table), i32([0, q]), i32([n]), q, n,
+                         scale=1.0, return_lse=True)
+    torch.cuda.synchronize()
+    qf = bf16_bits_to_f32(bits).reshape(q, 1, dim)
+    want = OA.attention(qf, c, table, np.array([0, q]), [n], 1.0, False)
+    got = O.float().cpu().numpy().reshape(q, 1, dim)
+    # weights that are equal (the codes of several keys are) or 0: only the roundings of the weights
+    # and of the result are left, 2^-8 each, of Σ p|v|
+    assert np.all(np.abs(got - want["O"]) <= 2.0 ** -6 * want["absO"])
+    # lse = ln 2·(c·z): half a step, 2^-24, each for c, the sum, ln 2 and the product
+    assert np.all(np.abs(lse.cpu().numpy() - want["lse"]) <= 2.0 ** -22 * np.abs(want["lse"]))
+
+
 @pytest.mark.parametrize("q,kv,bound", [(3, 100, 1), (20, 5000, 7), (300, 300, 130), (150, 5000, 129)])
 def test_rows_past_the_bound_are_left(L, q, kv, bound):
     """max_rows below a sequence's rows: the rows past it stay as they were, with a split too, and

@@ -112,6 +112,42 @@ def test_extreme_magnitudes(L):
 
 
 @pytest.mark.parametrize("dim", [64, 128])
+def test_infinities_and_nan(L, dim):
+    """They are stored as the NaN code and read back as NaN; the page's scale and the other tokens'
+    codes are those without them, also where a later token raises the scale over them."""
+    torch = torch_mod()
+    rng = np.random.default_rng(14)
+    H = 2
+    odd = np.array([0x7F80, 0xFF80, 0x7FC0, 0xFFC1, 0x7F81, 0x7F7F, 0xFF7F], np.uint16)
+    for start, n, later in ((0, 64, 0), (0, 40, 3), (10, 130, 2), (63, 1, 0), (0, 1, 1)):
+        for only in (False, True):                      # some values, or every one
+            c = OA.new_cache(5, H, dim, fill=0x55)
+            kv = device_cache(L, c)
+            table = [[3, 1, 4]]
+            if start:
+                _write(L, c, kv, _rand(rng, start, H * dim), _rand(rng, start, H * dim), table,
+                       [0, start], [0])
+            X = [_rand(rng, n, H * dim) for _ in range(2)]
+            for x in X:
+                hit = rng.random(x.shape) < (1.1 if only else 0.02)
+                x[hit] = rng.choice(odd[:5] if only else odd[:rng.choice([5, 7])], int(hit.sum()))
+            _write(L, c, kv, X[0], X[1], table, [0, n], [start])
+            if later:
+                _write(L, c, kv, _rand(rng, later, H * dim, 1e6), _rand(rng, later, H * dim, 30.0),
+                       table, [0, later], [start + n])
+            torch.cuda.synchronize()
+            same(kv, c)
+            total = start + n + later
+            got = L.kv_read(kv, i32(table), i32([0, total]), i32([0]), total, total)
+            torch.cuda.synchronize()
+            for is_v in range(2):
+                for h in range(H):
+                    want, _ = OA.kv_values(c, np.array(table[0]), total, h, is_v)
+                    g = got[is_v][:, h * dim:(h + 1) * dim].float().cpu().numpy()
+                    assert np.array_equal(g, want, equal_nan=True)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
 def test_ragged_batch(L, dim):
     """Sequences of other lengths and starts, one without rows, rows behind the last sequence."""
     torch = torch_mod()

@@ -32,7 +32,7 @@ namespace {
 typedef __attribute__((address_space(1))) void gvoid_t;
 typedef __attribute__((address_space(3))) void lvoid_t;
 
-constexpr float kNoMax = -1.0e30f;  // running maximum before the first visible token
+constexpr float kNoMax = -3.0e38f;  // running maximum before the first visible token
 constexpr float kRaise = 8.0f;
 constexpr float kMostSum = 4096.0f;
 
@@ -106,16 +106,17 @@ __device__ __forceinline__ void query_load(const uint16_t* q, int half, QueryRow
 template <int DIM>
 __device__ __forceinline__ void query_operand(const QueryRow<DIM>& r, QueryOp<DIM>& op) {
   const auto& w = r.w;
-  float m = 0.0f;
+  uint32_t m2 = 0;
 #pragma unroll
   for (int s = 0; s < DIM / 64; ++s)
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        m = fmaxf(m, fmaxf(fabsf(bf16_lo(w[s][j][c])), fabsf(bf16_hi(w[s][j][c]))));
-  m = fmaxf(m, __shfl_xor(m, 32));
-  const int e = page_exponent(m);
+      for (int c = 0; c < 4; ++c) m2 = max_bf16x2(m2, w[s][j][c] & 0x7FFF7FFFu);
+  m2 = max_bf16x2(m2, m2 >> 16) & 0xFFFFu;
+  const uint32_t there = (uint32_t)__shfl_xor((int)m2, 32);
+  m2 = there > m2 ? there : m2;
+  const int e = page_exponent(__uint_as_float(m2 << 16));
   const float up = two_to(-e);
 #pragma unroll
   for (int s = 0; s < DIM / 64; ++s)
@@ -130,8 +131,9 @@ __device__ __forceinline__ void query_operand(const QueryRow<DIM>& r, QueryOp<DI
                                     (x[2] - __builtin_amdgcn_cvt_f32_fp8(h, 2)) * 16.0f,
                                     (x[3] - __builtin_amdgcn_cvt_f32_fp8(h, 3)) * 16.0f);
     }
-  op.s_hi = e + 127;
-  op.s_lo = e + 123;
+  // an infinity or NaN in the row makes every score NaN (the scale operand's NaN)
+  op.s_hi = m2 < kInfBits ? e + 127 : 255;
+  op.s_lo = m2 < kInfBits ? e + 123 : 255;
 }
 
 template <int DIM>
@@ -175,6 +177,22 @@ __device__ __forceinline__ u32x4_t drop_slots(u32x4_t v, int tb, int half, int n
     k = k < 0 ? 0 : (k > 4 ? 4 : k);
     v[d] &= (uint32_t)((1ull << (8 * k)) - 1ull);
   }
+  return v;
+}
+
+// A lane's 16 bytes of a V fragment with its NaN codes made 0; `dirty` becomes true where a lane of
+// the wave had one.  With the causal mask the rows of a block share pages of which some do not
+// see every token, and a weight of 0 does not hide a NaN; those that do see it get it back from
+// `restore_nan`.
+__device__ __forceinline__ u32x4_t clear_nan(u32x4_t v, bool& dirty) {
+  uint32_t any = 0;
+#pragma unroll
+  for (int d = 0; d < 4; ++d) {
+    const uint32_t nan = ((v[d] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+    v[d] &= ~((nan >> 7) * 0xFFu);
+    any |= nan;
+  }
+  dirty = dirty || __builtin_amdgcn_ballot_w64(any != 0) != 0;
   return v;
 }
 
@@ -261,6 +279,32 @@ __device__ __forceinline__ bf16x8_t weights(State<DIM>& st, const f32x16_t (&z)[
   return __builtin_bit_cast(bf16x8_t, w);
 }
 
+// NaN in the channels in which a token that the lane's row sees, in pages [p0, p1), has a NaN code.
+template <int DIM>
+__device__ __forceinline__ void restore_nan(const AttnArgs& a, const Seq& s, State<DIM>& st, int p0,
+                                            int p1, int lim_row, int half) {
+  uint64_t bad = 0;  // bit 16 j + i: accumulator o[j][i]
+  for (int p = p0; p < p1; ++p) {
+    const int page = a.table[(int64_t)s.b * a.max_blocks + p];
+    if (page < 0 || page >= a.n_pages) continue;
+    const uint8_t* codes = a.vc + ((int64_t)page * a.Hkv + s.h) * (kPage * DIM);
+    for (int t = 0; t < kPage; t += 4) {
+      const int64_t n = lim_row - ((int64_t)p * kPage + t);
+      const uint32_t seen = n >= 4 ? ~0u : (n > 0 ? (1u << (8 * n)) - 1u : 0u);
+      for (int k = 0; k < DIM / 2; ++k) {
+        const int d = 32 * (k >> 4) + 8 * ((k >> 2) & 3) + 4 * half + (k & 3);
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(codes + v_offset(t, d)) & seen;
+        if (((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) bad |= 1ull << k;
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < DIM / 32; ++j)
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if ((bad >> (16 * j + i)) & 1) st.o[j][i] = __builtin_nanf("");
+}
+
 constexpr int kPresent = 1 << 16;
 
 // The lane's logical page `at` (of pages [0, end), end >= 1; later ones repeat the last): its
@@ -300,7 +344,7 @@ __device__ __forceinline__ void store_row(const AttnArgs& a, const State<DIM>& s
     }
     return;
   }
-  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+  const float inv = l != 0.0f ? 1.0f / l : 0.0f;
   uint16_t* o = a.O + token * a.ldo + (int64_t)head * DIM;
 #pragma unroll
   for (int j = 0; j < DIM / 32; ++j)
@@ -311,7 +355,7 @@ __device__ __forceinline__ void store_row(const AttnArgs& a, const State<DIM>& s
                 pack_bf16x2(st.o[j][4 * g + 2] * inv, st.o[j][4 * g + 3] * inv)};
   if (a.lse && half == 0)
     a.lse[token * a.Hq + head] =
-        l > 0.0f ? 0.6931471805599453f * (st.m + __builtin_amdgcn_logf(l)) : -__builtin_inff();
+        l != 0.0f ? 0.6931471805599453f * (st.m + __builtin_amdgcn_logf(l)) : -__builtin_inff();
 }
 
 // Many rows: four waves of 32 rows share each page through LDS.  K's codes are copied there as
@@ -329,6 +373,7 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void k_attn_tile(AttnArgs a) {
   // the reads of the other, and does not wait for it in front of them)
   __shared__ __attribute__((aligned(16))) uint8_t k_img0[kBytes], k_img1[kBytes];
   __shared__ __attribute__((aligned(16))) uint8_t v_img[2][2 * kBytes];
+  __shared__ int s_dirty[kTileWaves];
   const int64_t total = (int64_t)a.B * a.Hkv * a.splits * a.tiles;
   const int64_t per_xcd = (total + 7) / 8;
   const int64_t item = (int64_t)(blockIdx.x % 8) * per_xcd + blockIdx.x / 8;
@@ -381,11 +426,18 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void k_attn_tile(AttnArgs a) {
   // the sequence's last page may hold fewer tokens than slots, and a page outside the cache (page 0
   // is read in its place) holds none
   const int whole = s.kv / kPage;
+  // pages that every row of the block sees whole
+  const int shared_pages = __builtin_amdgcn_readfirstlane(limit_of(a, s, r0 / a.G) / kPage);
+  bool dirty = false;
   auto trim_v = [&](int i, int exps) {
-    if (i < whole && (exps & kPresent)) return;
-    const int n = i == whole && (exps & kPresent) ? s.kv % kPage : 0;
+    if (i < shared_pages && (exps & kPresent)) return;
+    const int n = !(exps & kPresent) || i > whole ? 0 : i == whole ? s.kv % kPage : kPage;
 #pragma unroll
     for (int f = 0; f < kCopies; ++f) vr[f] = drop_slots(vr[f], (wave * kCopies + f) & 1, half, n);
+    if (a.causal) {
+#pragma unroll
+      for (int f = 0; f < kCopies; ++f) vr[f] = clear_nan(vr[f], dirty);
+    }
   };
   // fragment f: its two 16-token steps of 1 KB each
   auto widen_v = [&](int exps, int slot) {
@@ -544,6 +596,12 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void k_attn_tile(AttnArgs a) {
       if (i + 1 < p1) step(i + 1, 1, zb, za);
     }
   }
+  if (a.causal) {
+    s_dirty[wave] = dirty;
+    __syncthreads();
+    if (s_dirty[0] | s_dirty[1] | s_dirty[2] | s_dirty[3])
+      restore_nan(a, s, st, p0 > shared_pages ? p0 : shared_pages, p1, lim_row, half);
+  }
   const float l = st.l + other_half(st.l);
   if (live) store_row<DIM>(a, st, l, s.first + tok, head, split, half);
 }
@@ -578,6 +636,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_few(AttnArgs a) {
   state_init(st);
   const int64_t head_off = (int64_t)s.h * kBytes + lane * 16, page_bytes = (int64_t)a.Hkv * kBytes;
   query_operand(qrow, q);
+  bool dirty = false;
   for (int g0 = p0 + wave; g0 < p1; g0 += 256) {
     // lane l: logical page g0 + 4 l
     int meta = page_id(a, s, g0 + 4 * lane, p1);
@@ -605,6 +664,10 @@ __global__ __launch_bounds__(256, 2) void k_attn_few(AttnArgs a) {
 #pragma unroll
         for (int f = 0; f < kFrags; ++f)
           vr[f] = drop_slots(vr[f], f & 1, half, lk > kPage ? kPage : lk);
+        if (a.causal) {
+#pragma unroll
+          for (int f = 0; f < kFrags; ++f) vr[f] = clear_nan(vr[f], dirty);
+        }
       }
       raise(st, largest(z, a.c));
 #pragma unroll
@@ -619,6 +682,10 @@ __global__ __launch_bounds__(256, 2) void k_attn_few(AttnArgs a) {
         }
       load(vr, a.vc, next);
     }
+  }
+  if (dirty) {
+    const int part = lim_first / kPage;
+    restore_nan(a, s, st, p0 > part ? p0 : part, p1, lim_row, half);
   }
   // join the four waves
   st.l += other_half(st.l);
@@ -655,10 +722,10 @@ __global__ __launch_bounds__(256, 2) void k_attn_few(AttnArgs a) {
         ml[1] = l;
       }
     } else {
-      a.O[token * a.ldo + (int64_t)hd * DIM + d] = f32_to_bf16(l > 0.0f ? sum / l : 0.0f);
+      a.O[token * a.ldo + (int64_t)hd * DIM + d] = f32_to_bf16(l != 0.0f ? sum / l : 0.0f);
       if (a.lse && d == 0)
         a.lse[token * a.Hq + hd] =
-            l > 0.0f ? 0.6931471805599453f * (mm + __builtin_amdgcn_logf(l)) : -__builtin_inff();
+            l != 0.0f ? 0.6931471805599453f * (mm + __builtin_amdgcn_logf(l)) : -__builtin_inff();
     }
   }
 }
@@ -686,14 +753,14 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
     for (int j = 0; j < DIM / 64; ++j)
       o[j] += a.part[(i * each + at) * DIM + (DIM / 64) * lane + j] * f;
   }
-  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+  const float inv = l != 0.0f ? 1.0f / l : 0.0f;
   uint16_t* y = a.O + token * a.ldo + (int64_t)head * DIM + (DIM / 64) * lane;
   if (DIM == 128)
     *reinterpret_cast<uint32_t*>(y) = pack_bf16x2(o[0] * inv, o[DIM / 64 - 1] * inv);
   else
     y[0] = f32_to_bf16(o[0] * inv);
   if (a.lse && lane == 0)
-    a.lse[at] = l > 0.0f ? 0.6931471805599453f * (m + __builtin_amdgcn_logf(l)) : -__builtin_inff();
+    a.lse[at] = l != 0.0f ? 0.6931471805599453f * (m + __builtin_amdgcn_logf(l)) : -__builtin_inff();
 }
 
 struct Plan {

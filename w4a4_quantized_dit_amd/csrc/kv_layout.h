@@ -31,6 +31,15 @@ __device__ __forceinline__ int v_offset(int t, int d) {
          ((t >> 3) & 1) * 4 + (t & 3);
 }
 
+constexpr uint32_t kInfBits = 0x7F80;        // |bf16| from here on: infinity or NaN
+
+// The larger of two bf16 magnitudes (sign bits clear) in each half.
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+  typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2_t, a),
+                                                                __builtin_bit_cast(u16x2_t, b)));
+}
+
 // Smallest e with a <= 448·2^e, within [kExpMin, kExpMax] (448 = 0.875·2^9).
 __device__ __forceinline__ int page_exponent(float a) {
   if (!(a > 0.0f)) return kExpMin;

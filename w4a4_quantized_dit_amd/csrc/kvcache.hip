@@ -71,6 +71,30 @@ __device__ __forceinline__ void unit_of(int& t, int& d) {
 template <int DIM>
 constexpr int kUnits = kPage / 4 * (DIM / 8);  // threads of a block: 128 or 256
 
+// Bits of the largest finite magnitude that the cache holds: 448·2^119.
+constexpr uint32_t kTopBits = 0x7F60;
+
+// Two values as the cache takes them: larger finite ones become ±448·2^119, infinities and NaN
+// a NaN, which converts to code 0xFF.  `most` collects the finite magnitudes.
+__device__ __forceinline__ uint32_t tame(uint32_t w, uint32_t& most) {
+  uint32_t o = 0;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const uint32_t x = (w >> (16 * k)) & 0xFFFFu, a = x & 0x7FFFu;
+    const uint32_t y = a >= kInfBits ? 0x7FFFu : (a > kTopBits ? (x & 0x8000u) | kTopBits : x);
+    const uint32_t m = y & 0x7FFFu;
+    if (m <= kTopBits && m > most) most = m;
+    o |= y << (16 * k);
+  }
+  return o;
+}
+
+// Four fp32 values of at most 448, or NaN, as E4M3 codes (no clamp in front of the conversion).
+__device__ __forceinline__ uint32_t fp8x4(float a, float b, float c, float d) {
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(
+      c, d, __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false), true);
+}
+
 __device__ __forceinline__ float at8(u32x4_t v, int j) {
   return j & 1 ? bf16_hi(v[j >> 1]) : bf16_lo(v[j >> 1]);
 }
@@ -78,18 +102,18 @@ __device__ __forceinline__ float at8(u32x4_t v, int j) {
 // Four codes (value times mul, E4M3) of one dword each way: consecutive channels of a token, or
 // consecutive tokens of a channel.
 __device__ __forceinline__ uint32_t k_code4(u32x4_t v, int j, float mul) {
-  return e4m3_pack4(at8(v, j) * mul, at8(v, j + 1) * mul, at8(v, j + 2) * mul, at8(v, j + 3) * mul);
+  return fp8x4(at8(v, j) * mul, at8(v, j + 1) * mul, at8(v, j + 2) * mul, at8(v, j + 3) * mul);
 }
 __device__ __forceinline__ uint32_t v_code4(const u32x4_t (&v)[4], int j, float mul) {
-  return e4m3_pack4(at8(v[0], j) * mul, at8(v[1], j) * mul, at8(v[2], j) * mul, at8(v[3], j) * mul);
+  return fp8x4(at8(v[0], j) * mul, at8(v[1], j) * mul, at8(v[2], j) * mul, at8(v[3], j) * mul);
 }
 
 // One dword of four codes, rounded again for a scale 1/down times as large.
 __device__ __forceinline__ uint32_t requantise4(uint32_t w, float down) {
-  return e4m3_pack4(__builtin_amdgcn_cvt_f32_fp8((int)w, 0) * down,
-                    __builtin_amdgcn_cvt_f32_fp8((int)w, 1) * down,
-                    __builtin_amdgcn_cvt_f32_fp8((int)w, 2) * down,
-                    __builtin_amdgcn_cvt_f32_fp8((int)w, 3) * down);
+  return fp8x4(__builtin_amdgcn_cvt_f32_fp8((int)w, 0) * down,
+               __builtin_amdgcn_cvt_f32_fp8((int)w, 1) * down,
+               __builtin_amdgcn_cvt_f32_fp8((int)w, 2) * down,
+               __builtin_amdgcn_cvt_f32_fp8((int)w, 3) * down);
 }
 
 // Bytes k of a dword with lo <= t + k < hi
@@ -104,7 +128,7 @@ template <int DIM>
 __global__ __launch_bounds__(256) void k_kv_write(KvArgs a) {
   constexpr int kThreads = kUnits<DIM>, kWaves = kThreads / 64, kBytes = kPage * DIM;
   __shared__ __attribute__((aligned(16))) uint8_t img[2][kBytes];
-  __shared__ float s_max[2][kWaves];
+  __shared__ uint32_t s_max[2][kWaves], s_fin[2][kWaves];
   Where w;
   if (!locate(a, w)) return;
   const int h = blockIdx.y, tid = threadIdx.x;
@@ -112,7 +136,6 @@ __global__ __launch_bounds__(256) void k_kv_write(KvArgs a) {
   unit_of<DIM>(t, d);
   const int64_t entry = a.table[(int64_t)blockIdx.z * a.max_blocks + w.p];
   u32x4_t x[2][4];
-  float m[2] = {0.0f, 0.0f};
 #pragma unroll
   for (int kv = 0; kv < 2; ++kv)
 #pragma unroll
@@ -134,25 +157,48 @@ __global__ __launch_bounds__(256) void k_kv_write(KvArgs a) {
       old[kv] = e < kExpMin ? kExpMin : (e > kExpMax ? kExpMax : e);
     }
   }
+  // bits of the largest magnitude, of the wave's values and then of the block's
+  auto wave_max = [&](uint32_t v, uint32_t& slot) {
+#pragma unroll
+    for (int k = 1; k < 64; k *= 2) v = max_bf16x2(v, (uint32_t)__shfl_xor((int)v, k));
+    if ((tid & 63) == 0) slot = max_bf16x2(v, v >> 16) & 0xFFFFu;
+  };
+  auto block_max = [&](const uint32_t (&slots)[kWaves]) {
+    uint32_t v = slots[0];
+#pragma unroll
+    for (int k = 1; k < kWaves; ++k) v = slots[k] > v ? slots[k] : v;
+    return v;
+  };
 #pragma unroll
   for (int kv = 0; kv < 2; ++kv) {
+    uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) m[kv] = fmaxf(m[kv], fabsf(at8(x[kv][i], j)));
-#pragma unroll
-    for (int k = 1; k < 64; k *= 2) m[kv] = fmaxf(m[kv], __shfl_xor(m[kv], k));
-    if ((tid & 63) == 0) s_max[kv][tid >> 6] = m[kv];
+      for (int j = 0; j < 4; ++j) m = max_bf16x2(m, x[kv][i][j] & 0x7FFF7FFFu);
+    wave_max(m, s_max[kv][tid >> 6]);
   }
   __syncthreads();
+  uint32_t top[2] = {block_max(s_max[0]), block_max(s_max[1])};
+  if (top[0] > kTopBits || top[1] > kTopBits) {  // the same for the whole block
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[kv][i][j] = tame(x[kv][i][j], m);
+      wave_max(m, s_fin[kv][tid >> 6]);
+    }
+    __syncthreads();
+    top[0] = block_max(s_fin[0]);
+    top[1] = block_max(s_fin[1]);
+  }
   int e[2];
   float up[2];
 #pragma unroll
   for (int kv = 0; kv < 2; ++kv) {
-    float mm = s_max[kv][0];
-#pragma unroll
-    for (int k = 1; k < kWaves; ++k) mm = fmaxf(mm, s_max[kv][k]);
-    e[kv] = page_exponent(mm);
+    e[kv] = page_exponent(__uint_as_float(top[kv] << 16));
     if (w.lo > 0 && old[kv] > e[kv]) e[kv] = old[kv];
     up[kv] = two_to(-e[kv]);
   }
