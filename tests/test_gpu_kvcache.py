@@ -111,6 +111,33 @@ def test_extreme_magnitudes(L):
     same(kv, c)
 
 
+@pytest.mark.parametrize("start,n,bound", [(0, 64, 1), (10, 100, 60), (63, 10, 1), (64, 200, 65)])
+def test_rows_past_the_bound_are_left(L, start, n, bound):
+    """max_rows below a sequence's rows: the rows past it are neither written nor read, within the
+    last page that the others reach too."""
+    torch = torch_mod()
+    rng = np.random.default_rng(15)
+    dim, rows = 64, 2 * n
+    c = OA.new_cache(12, 1, dim, fill=0x33)
+    kv = device_cache(L, c)
+    table = [[4, 0, 7, 2, 8], [9, 1, 3, 10, 6]]
+    before = _rand(rng, 2 * start, dim)
+    if start:
+        _write(L, c, kv, before, before, table, [0, start, 2 * start], [0, 0])
+    K, V = _rand(rng, rows, dim), _rand(rng, rows, dim)
+    L.kv_write(kv, dev_bf16(K), dev_bf16(V), i32(table), i32([0, n, rows]), i32([start, start]), bound)
+    at = np.r_[0:bound, n:n + bound]
+    OA.kv_write(c, K[at], V[at], np.asarray(table), [0, bound, 2 * bound], [start, start])
+    torch.cuda.synchronize()
+    same(kv, c)
+    out = [torch.full((rows, dim), 5.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    L.kv_read(kv, i32(table), i32([0, n, rows]), i32([start, start]), rows, bound, out=out)
+    torch.cuda.synchronize()
+    for o in out:
+        left = np.setdiff1d(np.arange(rows), at)
+        assert torch.all(o[dev(left)] == 5.0) and torch.all((o[dev(at)] != 5.0).any(dim=1))
+
+
 @pytest.mark.parametrize("dim", [64, 128])
 def test_infinities_and_nan(L, dim):
     """They are stored as the NaN code and read back as NaN; the page's scale and the other tokens'

@@ -35,6 +35,7 @@ struct KvArgs {
   uint8_t* ks;
   uint8_t* vs;
   int heads;
+  int64_t max;           // rows of a sequence that are handled
 };
 
 // The block's part of its sequence: tokens of page-table entry p, slots [lo, hi), from packed row
@@ -47,7 +48,7 @@ struct Where {
 __device__ __forceinline__ bool locate(const KvArgs& a, Where& w) {
   const int b = blockIdx.z;
   const int64_t first = a.cu[b], end = a.cu[b + 1], start = a.start[b];
-  const int64_t n = end - first;
+  const int64_t n = end - first < a.max ? end - first : a.max;
   if (n <= 0 || first < 0 || end > a.rows || start < 0) return false;
   const int64_t p = start / kPage + blockIdx.x, t0 = p * kPage;
   if (t0 >= start + n || p >= a.max_blocks) return false;
@@ -302,7 +303,7 @@ hipError_t launch_kv_write(const uint16_t* K, int64_t ldk, const uint16_t* V, in
                            int64_t max_blocks, int64_t n_pages, uint8_t* kc, uint8_t* vc,
                            uint8_t* ks, uint8_t* vs, hipStream_t s) {
   const KvArgs a{K, V, nullptr, nullptr, ldk, ldv, rows, cu, start, table, max_blocks, n_pages,
-                 kc, vc, ks, vs, heads};
+                 kc, vc, ks, vs, heads, max_new};
   // new tokens that start inside a page reach one page more
   const dim3 grid((unsigned)((max_new + kPage - 2) / kPage + 1), (unsigned)heads, (unsigned)B);
   if (dim == 64)
@@ -319,7 +320,7 @@ hipError_t launch_kv_read(uint16_t* K, int64_t ldk, uint16_t* V, int64_t ldv, in
                           const uint8_t* ks, const uint8_t* vs, hipStream_t s) {
   const KvArgs a{nullptr, nullptr, K, V, ldk, ldv, rows, cu, start, table, max_blocks, n_pages,
                  const_cast<uint8_t*>(kc), const_cast<uint8_t*>(vc), const_cast<uint8_t*>(ks),
-                 const_cast<uint8_t*>(vs), heads};
+                 const_cast<uint8_t*>(vs), heads, max_n};
   const dim3 grid((unsigned)((max_n + kPage - 2) / kPage + 1), (unsigned)heads, (unsigned)B);
   const bool nt = rows * heads * dim * 4 > kPastCaches;
   if (dim == 64)
