@@ -522,11 +522,10 @@ def svdq_score_modal_rel_l2(Y, X, W, rows, row_group, sums, stream=None):
 # ------------------------------------------------------------------------------------------
 
 class _Args:
-    """Checked pointers of one call's tensors, which must all be on one device; as a context, the
-    call runs on that device and its current stream, also when another device is current.
-    (Everything about a tensor is checked in one place and once: a small call's time is its
-    marshalling.)"""
-    __slots__ = ("dev", "back")
+    """Checked pointers of one call's tensors, which must all be on one device; the call runs on
+    that device and its current stream, also when another device is current.  (Everything about a
+    tensor is checked in one place and once: a small call's time is its marshalling.)"""
+    __slots__ = ("dev",)
 
     def __init__(self):
         self.dev = -1
@@ -573,16 +572,16 @@ class _Args:
             raise ValueError(f"{name} must be contiguous")
         return self._at(t, name)
 
-    def __enter__(self):
-        cuda = _torch().cuda
-        self.back = None
-        if self.dev >= 0 and self.dev != cuda.current_device():
-            self.back = cuda.device(self.dev)
-            self.back.__enter__()
-
-    def __exit__(self, *exc):
-        if self.back is not None:
-            self.back.__exit__(*exc)
+    def call(self, name, stream, *args):
+        """The entry point `name` on `stream` (None: the device's current one)."""
+        torch = _torch()
+        fn, now = getattr(load(), name), torch._C._cuda_getDevice()
+        if self.dev == now or self.dev < 0:
+            _check(fn(*args, torch._C._cuda_getCurrentRawStream(now) if stream is None
+                      else stream.cuda_stream))
+        else:
+            with torch.cuda.device(self.dev):
+                _check(fn(*args, _stream(stream)))
 
 
 def svdq_rmsnorm_quant_act(X, residual, H, gamma, eps, lam, lora_down, r, codes, scales, D,
@@ -602,8 +601,7 @@ def svdq_rmsnorm_quant_act(X, residual, H, gamma, eps, lam, lora_down, r, codes,
             a.vec(lam, K, f32, "lambda"), _down(a, lora_down, r, K, bf), int(r),
             a.vec(codes, M * K, u8, "codes"), a.vec(scales, M * K // 32, u8, "scales"),
             a.vec(D, M * r, f32, "D") if r else None)
-    with a:
-        _check(load().svdq_rmsnorm_quant_act(*args, _stream(stream)))
+    a.call("svdq_rmsnorm_quant_act", stream, *args)
 
 
 def _gamma(a, t, K, bf):
@@ -648,8 +646,7 @@ def svdq_rope_axes(X, heads, dim, pos, freq, axis_dims, interleaved, inverse, Y,
         raise ValueError("pos must be contiguous")
     args = (x, M, ldx, int(heads), int(dim), p, a.vec(freq, sum(axis_dims) // 2, torch.float64, "freq"),
             n, arr, int(bool(interleaved)), int(bool(inverse)), y, ldy)
-    with a:
-        _check(load().svdq_rope_axes(*args, _stream(stream)))
+    a.call("svdq_rope_axes", stream, *args)
 
 
 def _cache_args(a, k_codes, v_codes, k_scales, v_scales, dim, block_table, cu_rows, per_seq, what):
@@ -686,10 +683,8 @@ def _kv_call(name, K, V, dim, cu_rows, start, max_rows, block_table, k_codes, v_
     v, ldv = a.mat(V, rows, heads * dim, bf, "V")
     if rows == 0:   # an empty tensor has no address
         return
-    with a:
-        _check(getattr(load(), name)(k, ldk, v, ldv, rows, heads, int(dim), cu, st, B,
-                                     int(max_rows), table, blocks, n_pages, *ptrs,
-                                     _stream(stream)))
+    a.call(name, stream, k, ldk, v, ldv, rows, heads, int(dim), cu, st, B, int(max_rows), table,
+           blocks, n_pages, *ptrs)
 
 
 def svdq_kv_write(K, V, dim, cu_rows, start, max_rows, block_table, k_codes, v_codes, k_scales,
@@ -729,8 +724,6 @@ def svdq_attn_kv8(Q, dim, cu_rows, kv_len, max_rows, max_kv, block_table, k_code
     ws = a.vec(workspace, 0, torch.uint8, "workspace")
     if rows == 0:
         return
-    with a:
-        _check(load().svdq_attn_kv8(q, ldq, rows, q_heads, heads, int(dim), cu, ln, B,
-                                    int(max_rows), int(max_kv), table, blocks, n_pages, *ptrs,
-                                    float(scale), int(bool(causal)), o, ldo, lse_p, ws,
-                                    workspace.numel() if ws is not None else 0, _stream(stream)))
+    a.call("svdq_attn_kv8", stream, q, ldq, rows, q_heads, heads, int(dim), cu, ln, B,
+           int(max_rows), int(max_kv), table, blocks, n_pages, *ptrs, float(scale),
+           int(bool(causal)), o, ldo, lse_p, ws, workspace.numel() if ws is not None else 0)
