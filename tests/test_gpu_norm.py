@@ -74,6 +74,18 @@ def test_every_rank_tile(L, r, M):
     _check(L, _case(M, K, r, True, True, True, seed=r), K)
 
 
+@pytest.mark.parametrize("r", [8, 24, 40, 64, 72, 96, 112, 128])
+@pytest.mark.parametrize("K", [256, 768])
+def test_every_rank_tile_between_few_and_many_rows(L, r, K):
+    _check(L, _case(8500, K, r, True, True, True, seed=r), K)
+
+
+@pytest.mark.parametrize("gamma,smooth", [(False, True), (True, False), (False, False)])
+@pytest.mark.parametrize("M", [2100, 17000])
+def test_many_rows_without_factors(L, gamma, smooth, M):
+    _check(L, _case(M, 256, 128, False, gamma, smooth, seed=9), 256)
+
+
 @pytest.mark.parametrize("residual", [False, True])
 @pytest.mark.parametrize("gamma", [False, True])
 @pytest.mark.parametrize("smooth", [False, True])

@@ -11,8 +11,8 @@
 // borders, are the same for every work split.
 //
 // Memory-bound: 7 bytes per element (x, res in; h, code out).  Each element is read once and held
-// in registers between the sum and the quantisation (16384 x 5120: 123 us, 4.8 TB/s, what a
-// large copy reaches).  D is a kernel of its own over h.
+// in registers between the sum and the quantisation (16384 x 5120: 111 us, 5.3 TB/s; a large copy
+// reaches 4.9).  D is a kernel of its own over h.
 #include "device.h"
 #include "launch.h"
 
@@ -157,8 +157,7 @@ __global__ __launch_bounds__(TPR) void k_norm_row(NormArgs a, int64_t first) {
 // D = bf16(x̂)·L1 on MFMA 16x16x32, from h and the inv left in D.  Fusing it into the row kernel
 // was tried first: a block then holds sixteen rows of h in registers while it reads all of L1
 // from L2, one block a CU, 701 us at 31688 x 5120, rank 128; reading h once more costs 2 bytes
-// an element, most of them from the cache below HBM (the blocks go backwards, the rows written
-// last come first), and lets 64 rows share each piece of L1.
+// an element and lets 128 rows share each piece of L1.
 struct DownArgs {
   const uint16_t* h;
   int64_t ldh;
@@ -175,107 +174,134 @@ __device__ __forceinline__ void xhat8_lds(u32x4_t h, float inv, const float* g, 
   for (int j = 0; j < 8; ++j) x[j] = (x[j] * g[j]) * l[j];
 }
 
-// Many rows: eight waves of 16 rows.  Each 64-channel chunk of h (128 rows) and of L1 goes
-// straight into one of three LDS images, two chunks ahead, in whole 128-byte lines: what bounds
-// such a kernel is the requests a CU can make, about one per four clocks, and h read by the
-// lanes that need it is twice as many, L1 for 64 rows instead of 128 again (117 us instead of
-// 101 at 31688 x 5120, rank 128; one chunk ahead instead of two or three 137).  The 16-byte
-// pieces of a row's 128 bytes lie at piece ^ (row % 8), so that the sixteen rows of a fragment
-// read are on different banks.  γ and 1/λ follow through registers.  Every step issues the same
-// loads (past the end the last chunk's again), so that one count waits for the oldest.  Rows past
-// M and ranks past r repeat the last one; what comes of them is not stored.
-constexpr int kDownWaves = 8, kDownRows = 16 * kDownWaves, kChunk = 64, kImages = 3;
+// Many rows: eight waves, GROUPS of 32 rows times 8 / GROUPS parts of a chunk's channels, 32 each,
+// whose sums are added at the end: 128 rows and chunks of 64 channels, or, where that leaves CUs
+// idle, 64 rows and chunks of 128 in half as many steps.  Each chunk of h and of L1 goes straight
+// into one of three LDS images, two chunks ahead, in whole lines: a CU makes about one request per
+// four clocks, and h read by the lanes that need it is twice as many, L1 for 64 rows instead of 128
+// again.  A wave of 16 rows on whole chunks would read all of L1 from the images for half as many
+// rows (113 us instead of 105 at 31688 x 5120, rank 128; of these 105 about 30 wait for h behind the
+// caches, 20 go to the requests, and without any load 54 are left).  The 16-byte pieces of a row lie
+// at piece ^ (row % pieces), so that the sixteen rows of a fragment read are on different banks.
+// γ and 1/λ follow through registers.  Every step issues the same loads (past the end the last
+// chunk's again), so that one count waits for the oldest.  Rows past M and ranks past r repeat the
+// last one; what comes of them is not stored.
+constexpr int kDownWaves = 8, kChunk = 64, kImages = 3;
 
-template <int NT>
+template <int NT, int GROUPS>
 __global__ __launch_bounds__(64 * kDownWaves, 2) void k_norm_down(NormArgs a, DownArgs d) {
-  constexpr int kL = NT * 16 * kChunk * 2, kH = kDownRows * kChunk * 2;  // bytes of an image
-  constexpr int kCopies = (2 * NT + kDownWaves - 1) / kDownWaves;                               // of L1, per wave
+  constexpr int kRows = 32 * GROUPS, kWidth = 32 * kDownWaves / GROUPS;  // a block's, channels of a chunk
+  constexpr int kLine = 2 * kWidth, kPieces = kLine / 16;                // of a row: bytes, pieces
+  constexpr int kL = NT * 16 * kLine, kH = kRows * kLine;                // bytes of an image
+  constexpr int kAll = kL / 1024;                                        // copies of L1
+  constexpr int kCopies = (kAll + kDownWaves - 1) / kDownWaves;          // per wave
+  static_assert(kH == 2 * kDownWaves * 1024, "two copies of h per wave");
   constexpr int kLoads = kCopies + 4;
   __shared__ __attribute__((aligned(16))) uint8_t s_0[kL + kH], s_1[kL + kH], s_2[kL + kH];
-  __shared__ __attribute__((aligned(16))) float s_g[kDownWaves][kChunk], s_i[kDownWaves][kChunk];
+  __shared__ __attribute__((aligned(16))) float s_g[kDownWaves][32], s_i[kDownWaves][32];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, rl = lane & 15, q = lane >> 4;
-  const int64_t first = (int64_t)(gridDim.x - 1 - blockIdx.x) * kDownRows;
-  const int64_t row0 = first + 16 * wave;
-  const int64_t row = row0 + rl < a.M ? row0 + rl : a.M - 1;
-  const int nch = (int)(a.K / kChunk);
-  const float inv = a.D[row * a.r];
+  const int group = wave % GROUPS, part = wave / GROUPS;
+  const int64_t first = (int64_t)blockIdx.x * kRows;
+  const int64_t row0 = first + 32 * group;
+  const int nch = (int)(a.K / kWidth);
+  float inv[2];
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int64_t row = row0 + 16 * t + rl;
+    inv[t] = a.D[(row < a.M ? row : a.M - 1) * a.r];
+  }
   // without γ or λ something else of K elements is read in their place, and not used
-  const uint16_t* gp = (a.gamma ? a.gamma : d.h) + lane;
-  const float* lp = (a.lambda ? a.lambda : reinterpret_cast<const float*>(a.down)) + lane;
-  // copy f of an image: rows 8f .. 8f + 7, eight lanes each
-  const int piece = 8 * ((lane ^ (lane >> 3)) & 7);
+  const int channel = 32 * part + (lane & 31);
+  const uint16_t* gp = (a.gamma ? a.gamma : d.h) + channel;
+  const float* lp = (a.lambda ? a.lambda : reinterpret_cast<const float*>(a.down)) + channel;
+  // copy f of an image: 64 / kPieces rows from there on, kPieces lanes each
+  constexpr int kEach = 64 / kPieces;
+  auto piece = [&](int f) { return 8 * ((lane ^ (kEach * f + lane / kPieces)) & (kPieces - 1)); };
   const uint16_t *src_l[kCopies], *src_h[2];
   int f_l[kCopies];
 #pragma unroll
   for (int i = 0; i < kCopies; ++i) {
-    f_l[i] = wave + kDownWaves * i < 2 * NT ? wave + kDownWaves * i : wave % (2 * NT);  // some twice, the same bytes
-    const int n = 8 * f_l[i] + lane / 8;
-    src_l[i] = a.down + (n < a.r ? n : a.r - 1) * a.K + piece;
+    f_l[i] = wave + kDownWaves * i < kAll ? wave + kDownWaves * i : wave % kAll;  // some twice, the same bytes
+    const int n = kEach * f_l[i] + lane / kPieces;
+    src_l[i] = a.down + (n < a.r ? n : a.r - 1) * a.K + piece(f_l[i]);
   }
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const int64_t m = first + 16 * wave + 8 * i + lane / 8;
-    src_h[i] = d.h + (m < a.M ? m : a.M - 1) * d.ldh + piece;
+    const int64_t m = first + kEach * (2 * wave + i) + lane / kPieces;
+    src_h[i] = d.h + (m < a.M ? m : a.M - 1) * d.ldh + piece(2 * wave + i);
   }
   uint16_t g[kImages];
   float l[kImages];
-  auto load = [&](int c, int slot, uint8_t* img) {
-    const int64_t k = (int64_t)(c < nch ? c : nch - 1) * kChunk;
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      __builtin_amdgcn_global_load_lds((gvoid_t*)(src_h[i] + k),
-                                       (lvoid_t*)(img + kL + (2 * wave + i) * 1024), 16, 0, 0);
-#pragma unroll
-    for (int i = 0; i < kCopies; ++i)
-      __builtin_amdgcn_global_load_lds((gvoid_t*)(src_l[i] + k), (lvoid_t*)(img + f_l[i] * 1024),
-                                       16, 0, 0);
-    g[slot] = gp[k];
-    l[slot] = lp[k];
+  // part p of a chunk's loads: two pieces of h, kCopies of L1, the factors
+  constexpr int kParts = kCopies + 3;
+  auto load = [&](int p, int c, int slot, uint8_t* img) {
+    const int64_t k = (int64_t)(c < nch ? c : nch - 1) * kWidth;
+    if (p < 2) {
+      __builtin_amdgcn_global_load_lds((gvoid_t*)(src_h[p] + k),
+                                       (lvoid_t*)(img + kL + (2 * wave + p) * 1024), 16, 0, 0);
+    } else if (p < 2 + kCopies) {
+      __builtin_amdgcn_global_load_lds((gvoid_t*)(src_l[p - 2] + k),
+                                       (lvoid_t*)(img + f_l[p - 2] * 1024), 16, 0, 0);
+    } else {
+      g[slot] = gp[k];
+      l[slot] = lp[k];
+    }
   };
-  f32x4_t acc[NT];
+  f32x4_t acc[2][NT];
 #pragma unroll
-  for (int j = 0; j < NT; ++j) acc[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  const int sw = rl & 7;
+  for (int t = 0; t < 2; ++t)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[t][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  const int at = ((4 * part + q) ^ (rl & (kPieces - 1))) * 16;
   auto step = [&](int c, int slot, const uint8_t* img, uint8_t* free_img) {
     wait_vmcnt<kLoads>();  // chunk c is here; c + 1 may be on its way
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);  // no use of the chunk moves up in front of its wait
-    // the wave's own copy of the chunk's factors: channel = lane
-    s_g[wave][lane] = a.gamma ? bf16_to_f32(g[slot]) : 1.0f;
-    s_i[wave][lane] = a.lambda ? 1.0f / l[slot] : 1.0f;
-    load(c + 2, (slot + 2) % kImages, free_img);
-    u32x4_t bv[2][NT], hv[2];
+    // the wave's own copy of its channels' factors (both halves of the wave write the same)
+    s_g[wave][lane & 31] = a.gamma ? bf16_to_f32(g[slot]) : 1.0f;
+    s_i[wave][lane & 31] = a.lambda ? 1.0f / l[slot] : 1.0f;
+    u32x4_t bv[NT], hv[2], av[2];
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      const int at = ((4 * s + q) ^ sw) * 16;
-      hv[s] = *reinterpret_cast<const u32x4_t*>(img + kL + (16 * wave + rl) * 128 + at);
+    for (int t = 0; t < 2; ++t)
+      hv[t] = *reinterpret_cast<const u32x4_t*>(img + kL + (32 * group + 16 * t + rl) * kLine + at);
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
-        bv[s][j] = *reinterpret_cast<const u32x4_t*>(img + (16 * j + rl) * 128 + at);
+    for (int j = 0; j < NT; ++j)
+      bv[j] = *reinterpret_cast<const u32x4_t*>(img + (16 * j + rl) * kLine + at);
+    float gg[8], ll[8];
+#pragma unroll
+    for (int j = 0; j < 8; j += 4) {
+      *reinterpret_cast<f32x4_t*>(gg + j) =
+          *reinterpret_cast<const f32x4_t*>(&s_g[wave][8 * q + j]);
+      *reinterpret_cast<f32x4_t*>(ll + j) =
+          *reinterpret_cast<const f32x4_t*>(&s_i[wave][8 * q + j]);
     }
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      float x[8], gg[8], ll[8];
+    for (int t = 0; t < 2; ++t) {
+      float x[8];
+      xhat8_lds(hv[t], c < nch ? inv[t] : 0.0f, gg, ll, x);
 #pragma unroll
-      for (int j = 0; j < 8; j += 4) {
-        *reinterpret_cast<f32x4_t*>(gg + j) =
-            *reinterpret_cast<const f32x4_t*>(&s_g[wave][32 * s + 8 * q + j]);
-        *reinterpret_cast<f32x4_t*>(ll + j) =
-            *reinterpret_cast<const f32x4_t*>(&s_i[wave][32 * s + 8 * q + j]);
-      }
-      xhat8_lds(hv[s], inv, gg, ll, x);
-      u32x4_t av;
+      for (int j = 0; j < 4; ++j) av[t][j] = pack_bf16x2(x[2 * j], x[2 * j + 1]);
+    }
+    // the loads of chunk c + 2 are issued between the matrix instructions: a wave waits there for
+    // its turn at the one address unit
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) av[j] = c < nch ? pack_bf16x2(x[2 * j], x[2 * j + 1]) : 0u;
+    for (int j = 0; j < NT; ++j) {
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
-        acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, av),
-                                                         __builtin_bit_cast(bf16x8_t, bv[s][j]),
-                                                         acc[j], 0, 0, 0);
+      for (int t = 0; t < 2; ++t)
+        acc[t][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, av[t]),
+                                                            __builtin_bit_cast(bf16x8_t, bv[j]),
+                                                            acc[t][j], 0, 0, 0);
+#pragma unroll
+      for (int p = j * kParts / NT; p < (j + 1) * kParts / NT; ++p)
+        load(p, c + 2, (slot + 2) % kImages, free_img);
+      __builtin_amdgcn_sched_barrier(0);
     }
   };
-  load(0, 0, s_0);
-  load(1, 1, s_1);
+#pragma unroll
+  for (int p = 0; p < kParts; ++p) load(p, 0, 0, s_0);
+#pragma unroll
+  for (int p = 0; p < kParts; ++p) load(p, 1, 1, s_1);
   // (steps past the end add zeros: a branch around them would make the compiler drain the loads
   // where the paths meet)
   for (int c = 0; c < nch; c += 3) {
@@ -283,16 +309,35 @@ __global__ __launch_bounds__(64 * kDownWaves, 2) void k_norm_down(NormArgs a, Do
     step(c + 1, 1, s_1, s_0);
     step(c + 2, 2, s_2, s_1);
   }
-  wait_vmcnt<0>();  // no copy is left in flight when the block ends
+  wait_vmcnt<0>();  // no copy is left in flight when the images are taken for the sums
+  __syncthreads();
+  // (2·NT KB for each group and part but the first, two of them in an image)
+  static_assert(2 * 2 * NT * 1024 <= kL + kH, "two groups' sums fit an image");
+  auto sums = [&](int p) {
+    const int n = (p - 1) * GROUPS + group;
+    return reinterpret_cast<f32x4_t*>((n < 2 ? s_0 : n < 4 ? s_1 : s_2) + (n & 1) * 2 * NT * 1024);
+  };
+  if (part > 0) {
 #pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    const int n = 16 * j + rl;
+    for (int t = 0; t < 2; ++t)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t m = row0 + 4 * q + i;
-      if (m < a.M && n < a.r) a.D[m * a.r + n] = acc[j][i];
-    }
+      for (int j = 0; j < NT; ++j) sums(part)[(t * NT + j) * 64 + lane] = acc[t][j];
   }
+  __syncthreads();
+  if (part > 0) return;
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+#pragma unroll
+      for (int p = 1; p < kDownWaves / GROUPS; ++p) acc[t][j] += sums(p)[(t * NT + j) * 64 + lane];
+      const int n = 16 * j + rl;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int64_t m = row0 + 16 * t + 4 * q + i;
+        if (m < a.M && n < a.r) a.D[m * a.r + n] = acc[t][j][i];
+      }
+    }
 }
 
 // Few rows: a block for each 16 rows and RT ranks, sixteen waves that take alternate 64-channel
@@ -371,19 +416,25 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_norm_down_few(NormArgs a, Do
   }
 }
 
-// Up to 1280 blocks of 16 rows and 16 ranks the kernel for few rows is the faster one (K = 5120,
-// whole call, few against many: rank 128, M 2048 63 and 93 us, M 4096 121 and 102; rank 32,
-// M 4096 51 and 74, M 8192 91 and 90, M 16384 205 and 164).
+// Which of the three (K = 5120, whole call in us; few, many with 64 rows, many with 128):
+//   rank 128  M 1024: 34, 57, 73   2048: 61, 62, 78   8192: 234, 88, 103   16384: -, 131, 143
+//                  20480: -, 197, 165   31688: -, 252, 231
+//   rank 32   M 4096: 49, 50, 74   8192: 93, 68, 91   16384: 180, 112, 131   20480: -, 156, 154
+// The kernel for few rows takes about as long as it has blocks of 16 rows and 16 ranks; the other
+// one a fixed time while its blocks fit the 256 CUs, longer with more ranks, so its larger blocks
+// come in where the smaller ones need a second round.
 template <int NT>
 void launch_down(const NormArgs& a, hipStream_t s) {
   const DownArgs d = a.res ? DownArgs{a.H, a.ldh} : DownArgs{a.X, a.ldx};
   const int64_t rows = (a.M + 15) / 16;
   if (rows * NT < 256)
     k_norm_down_few<4><<<dim3((unsigned)rows, (unsigned)a.r / 4), 64 * kFewWaves, 0, s>>>(a, d);
-  else if (rows * NT <= 1280)
+  else if (rows * NT <= 448 + 72 * NT)
     k_norm_down_few<16><<<dim3((unsigned)rows, NT), 64 * kFewWaves, 0, s>>>(a, d);
+  else if (a.M <= 64 * 256)
+    k_norm_down<NT, 2><<<(unsigned)((a.M + 63) / 64), 64 * kDownWaves, 0, s>>>(a, d);
   else
-    k_norm_down<NT><<<(unsigned)((a.M + kDownRows - 1) / kDownRows), 64 * kDownWaves, 0, s>>>(a, d);
+    k_norm_down<NT, 4><<<(unsigned)((a.M + 127) / 128), 64 * kDownWaves, 0, s>>>(a, d);
 }
 
 }  // namespace

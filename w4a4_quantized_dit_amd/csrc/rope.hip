@@ -8,15 +8,14 @@
 //
 // Memory-bound (4 bytes per element).  A block turns one row: the cos / sin of its pairs are
 // formed once, a pair a thread, and kept in LDS (formed by every thread for its own pairs they
-// held up the loads: 252 us instead of 240 at 31688 rows of 80 heads of 128); a thread owns
-// two pieces of eight channels in the same place of every head that it turns.
+// held up the loads: 5 % more at 31688 rows of 80 heads of 128, which take 222 us, 5.8 TB/s); a
+// thread owns two pieces of eight channels in the same place of every head that it turns.
 #include "device.h"
 #include "launch.h"
 
 namespace svdq {
 
 namespace {
-
 
 struct RopeArgs {
   const uint16_t* X;
