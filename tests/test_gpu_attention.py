@@ -106,7 +106,8 @@ def test_single_tokens(L, dim, kv, Hq, Hkv):
 
 @pytest.mark.parametrize("dim", [64, 128])
 @pytest.mark.parametrize("q,kv", [(1, 1), (2, 1), (33, 33), (64, 64), (127, 300), (128, 128),
-                                  (129, 65), (200, 1000), (257, 257)])
+                                  (129, 65), (200, 1000), (257, 257), (520, 70), (600, 600),
+                                  (700, 1000)])
 @pytest.mark.parametrize("causal", [False, True])
 @pytest.mark.parametrize("G", [1, 3])
 def test_many_rows(L, dim, q, kv, causal, G):
@@ -115,7 +116,7 @@ def test_many_rows(L, dim, q, kv, causal, G):
 
 
 @pytest.mark.parametrize("dim", [64, 128])
-@pytest.mark.parametrize("q", [1, 20, 150])
+@pytest.mark.parametrize("q", [1, 20, 150, 400])
 @pytest.mark.parametrize("causal", [False, True])
 def test_long_cache_is_split(L, dim, q, causal):
     """Few blocks over a long cache: the page range is split and joined."""
@@ -139,9 +140,10 @@ def test_ragged_batches(L, dim, causal, q_lens, kv_lens):
 def test_strided_rows(L):
     run(L, [40], [200], 4, 2, 64, True, pad=24)
     run(L, [1], [200], 4, 2, 128, True, pad=8)
+    run(L, [600], [700], 4, 2, 128, True, pad=8)
 
 
-@pytest.mark.parametrize("q", [1, 100])
+@pytest.mark.parametrize("q", [1, 100, 600])
 def test_peaked_and_flat_scores(L, q):
     """Scores over a wide range (the running maximum rises often), nearly equal ones, and a
     bound on kv_len that is too small (it sizes the split only)."""
@@ -151,7 +153,7 @@ def test_peaked_and_flat_scores(L, q):
     run(L, [q], [900], 2, 1, 64, True, max_kv=10)
 
 
-@pytest.mark.parametrize("q", [1, 70])
+@pytest.mark.parametrize("q", [1, 70, 600])
 def test_rising_scores_every_page(L, q):
     """Keys aligned with the query and growing page by page: every page raises the maximum."""
     torch = torch_mod()
@@ -173,7 +175,7 @@ def test_rising_scores_every_page(L, q):
           lse.cpu().numpy().astype(np.float64), qf, 12 * np.abs(u).max(), 0.125, n)
 
 
-@pytest.mark.parametrize("q", [1, 50])
+@pytest.mark.parametrize("q", [1, 50, 600])
 def test_zero_rows_and_zero_pages(L, q):
     """All-zero queries weigh every token alike; pages of zeros (smallest exponent) beside pages of
     large values keep their weight in the sum."""
@@ -197,7 +199,7 @@ def test_zero_rows_and_zero_pages(L, q):
           lse.cpu().numpy().astype(np.float64), qf, 5000.0, 0.125, 192)
 
 
-@pytest.mark.parametrize("q", [1, 64])
+@pytest.mark.parametrize("q", [1, 64, 600])
 def test_missing_pages_are_masked(L, q):
     torch = torch_mod()
     rng = np.random.default_rng(7)
@@ -219,7 +221,8 @@ def test_missing_pages_are_masked(L, q):
 
 
 @pytest.mark.parametrize("dim", [64, 128])
-@pytest.mark.parametrize("q,kv", [(1, 400), (70, 400), (3, 5000), (150, 5000)])
+@pytest.mark.parametrize("q,kv", [(1, 400), (70, 400), (3, 5000), (150, 5000), (600, 400),
+                                  (600, 5000)])
 @pytest.mark.parametrize("causal", [False, True])
 def test_missing_pages_beside_a_garbage_page(L, q, kv, dim, causal):
     """Page 0, which no sequence owns, holds NaN codes: nothing of it shows where pages are missing."""
@@ -256,7 +259,7 @@ def check_with_nan(want, O, lse, q, kmax, scale, tokens, what=""):
 @pytest.mark.parametrize("dim", [64, 128])
 @pytest.mark.parametrize("G", [1, 2])
 @pytest.mark.parametrize("q,kv", [(1, 70), (1, 5000), (3, 130), (15, 4100), (64, 64), (70, 300),
-                                  (150, 5000), (300, 300)])
+                                  (150, 5000), (300, 300), (600, 700), (600, 5000)])
 @pytest.mark.parametrize("causal", [False, True])
 def test_nan_in_seen_and_hidden_tokens(L, q, kv, G, dim, causal):
     """Infinities and NaN in keys, values and queries: they show where they are seen, and a row that
@@ -293,7 +296,7 @@ def test_nan_in_seen_and_hidden_tokens(L, q, kv, G, dim, causal):
 
 
 @pytest.mark.parametrize("dim", [64, 128])
-@pytest.mark.parametrize("q", [1, 40])
+@pytest.mark.parametrize("q", [1, 40, 600])
 @pytest.mark.parametrize("sign", [1, -1])
 def test_very_large_scores(L, q, dim, sign):
     """Scores of one sign up to 2^26, exact in fp32 (one channel, powers of two and their sums of few
@@ -322,7 +325,8 @@ def test_very_large_scores(L, q, dim, sign):
     assert np.all(np.abs(lse.cpu().numpy() - want["lse"]) <= 2.0 ** -22 * np.abs(want["lse"]))
 
 
-@pytest.mark.parametrize("q,kv,bound", [(3, 100, 1), (20, 5000, 7), (300, 300, 130), (150, 5000, 129)])
+@pytest.mark.parametrize("q,kv,bound", [(3, 100, 1), (20, 5000, 7), (300, 300, 130), (150, 5000, 129),
+                                        (400, 400, 330), (400, 5000, 270)])
 def test_rows_past_the_bound_are_left(L, q, kv, bound):
     """max_rows below a sequence's rows: the rows past it stay as they were, with a split too, and
     the others see what they see without the bound (causal by the true number of rows)."""
@@ -343,7 +347,7 @@ def test_rows_past_the_bound_are_left(L, q, kv, bound):
         assert torch.all((got[:bound] - want[:bound]).abs() <= 2.0 ** -6 * want[:bound].abs() + 1e-2)
 
 
-@pytest.mark.parametrize("q,kv", [(1, 3000), (150, 3000), (300, 300)])
+@pytest.mark.parametrize("q,kv", [(1, 3000), (150, 3000), (300, 300), (700, 3000)])
 def test_repeats_bit_for_bit(L, q, kv):
     torch = torch_mod()
     rng = np.random.default_rng(8)

@@ -397,7 +397,8 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void k_attn_tile(AttnArgs a) {
   const int p0 = __builtin_amdgcn_readfirstlane((int)((int64_t)pages * split / a.splits));
   const int p1 = __builtin_amdgcn_readfirstlane((int)((int64_t)pages * (split + 1) / a.splits));
   const int lim_row = live ? limit_of(a, s, tok) : 0;
-  const int lim_first = __builtin_amdgcn_readfirstlane(w0 < R ? limit_of(a, s, w0 / a.G) : 0);
+  // (a wave without rows hides nothing: it would do so on every page)
+  const int lim_first = __builtin_amdgcn_readfirstlane(w0 < R ? limit_of(a, s, w0 / a.G) : s.kv);
 
   // (rows past the last read token 0's; nothing of them is stored)
   QueryOp<DIM> q;
@@ -606,28 +607,42 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void k_attn_tile(AttnArgs a) {
   if (live) store_row<DIM>(a, st, l, s.first + tok, head, split, half);
 }
 
-// At most 32 rows (single tokens, small groups): the four waves take every fourth page each,
-// straight into registers, and join their sums through LDS.
-template <int DIM>
+// Few rows (single tokens, small groups): blocks of 32, whose four waves take every fourth page each,
+// straight into registers, and join their sums through LDS.  Where a key head has more than 32 rows
+// (TILES) its blocks are neighbours on one XCD, and the pages stay in its cache for them.
+constexpr int kFewRows = 32;
+constexpr int64_t kFewMost = 512;  // of a key head, in blocks of so many (measured to there)
+
+template <int DIM, bool TILES>
 __global__ __launch_bounds__(256, 2) void k_attn_few(AttnArgs a) {
   constexpr int kBytes = kPage * DIM;
   constexpr int kFrags = kBytes / 1024;
   __shared__ float s_o[4][DIM][33];
   __shared__ float s_m[4][32], s_l[4][32];
-  const int64_t item = blockIdx.x;
+  int64_t item = blockIdx.x;
+  int r0 = 0;
+  if (TILES) {
+    const int64_t total = (int64_t)a.B * a.Hkv * a.splits * a.tiles, per_xcd = (total + 7) / 8;
+    item = (int64_t)(blockIdx.x % 8) * per_xcd + blockIdx.x / 8;
+    if (item >= total || blockIdx.x / 8 >= per_xcd) return;
+    r0 = kFewRows * (int)(item % a.tiles);
+    item /= a.tiles;
+  }
   const int split = (int)(item % a.splits);
   Seq s;
   if (!sequence(a, (int)(item / a.splits), s)) return;
-  const int R = s.q * a.G;  // at most 32
+  int R = s.q * a.G - r0;
+  if (R <= 0) return;
+  R = R < kFewRows ? R : kFewRows;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, half = lane >> 5, n = lane & 31;
   const bool live = n < R;
-  const int tok = live ? n / a.G : 0;
-  const int head = s.h * a.G + (live ? n % a.G : 0);
-  const int pages = (int)(((int64_t)limit_of(a, s, (R - 1) / a.G) + kPage - 1) / kPage);
+  const int tok = (r0 + (live ? n : 0)) / a.G;
+  const int head = s.h * a.G + (r0 + (live ? n : 0)) % a.G;
+  const int pages = (int)(((int64_t)limit_of(a, s, (r0 + R - 1) / a.G) + kPage - 1) / kPage);
   const int p0 = (int)((int64_t)pages * split / a.splits);
   const int p1 = (int)((int64_t)pages * (split + 1) / a.splits);
   const int lim_row = live ? limit_of(a, s, tok) : 0;
-  const int lim_first = limit_of(a, s, 0);
+  const int lim_first = limit_of(a, s, r0 / a.G);
 
   QueryOp<DIM> q;
   QueryRow<DIM> qrow;
@@ -645,7 +660,8 @@ __global__ __launch_bounds__(256, 2) void k_attn_few(AttnArgs a) {
     auto load = [&](u32x4_t (&r)[kFrags], const uint8_t* codes, int page) {
 #pragma unroll
       for (int f = 0; f < kFrags; ++f)
-        r[f] = load_nt(codes + page * page_bytes + head_off + f * 1024);
+        r[f] = TILES ? *reinterpret_cast<const u32x4_t*>(codes + page * page_bytes + head_off + f * 1024)
+                     : load_nt(codes + page * page_bytes + head_off + f * 1024);
     };
     const int count = (p1 - g0 + 3) / 4 < 64 ? (p1 - g0 + 3) / 4 : 64;
     load(kr, a.kc, __builtin_amdgcn_readfirstlane(meta));
@@ -711,8 +727,8 @@ __global__ __launch_bounds__(256, 2) void k_attn_few(AttnArgs a) {
       sum += s_o[w][d][rr];
       l += s_l[w][rr] * __builtin_amdgcn_exp2f(s_m[w][rr] - mm);
     }
-    const int64_t token = s.first + rr / a.G;
-    const int hd = s.h * a.G + rr % a.G;
+    const int64_t token = s.first + (r0 + rr) / a.G;
+    const int hd = s.h * a.G + (r0 + rr) % a.G;
     if (a.splits > 1) {
       const int64_t at = ((int64_t)split * a.rows + token) * a.Hq + hd;
       a.part[at * DIM + d] = sum;
@@ -730,9 +746,13 @@ __global__ __launch_bounds__(256, 2) void k_attn_few(AttnArgs a) {
   }
 }
 
-// The splits of every row joined, one wave per row of sequence blockIdx.y.
+// The splits of every row joined, one wave per row of sequence blockIdx.y.  The lanes take the
+// splits' maxima side by side, and groups of DIM / 4 lanes, four channels each, take every second
+// (DIM 128) or fourth split, several loads under way at once (one split after the other with all
+// lanes took 25 us for 128 rows of 48 splits, now 4).
 template <int DIM>
 __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
+  constexpr int kWide = DIM / 4, kGroups = 64 / kWide;
   const int b = blockIdx.y, lane = threadIdx.x & 63;
   const int first = a.cu[b], end = a.cu[b + 1];
   if (first < 0 || end <= first || end > a.rows) return;
@@ -742,23 +762,33 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
   const int64_t at = (int64_t)first * a.Hq + local, token = at / a.Hq;
   const int head = (int)(at % a.Hq);
   const int64_t each = a.rows * a.Hq;
-  const float* ml = a.part + a.splits * each * DIM + at * 2;
+  const float2* ml = reinterpret_cast<const float2*>(a.part + a.splits * each * DIM) + at;
   float m = kNoMax;
-  for (int i = 0; i < a.splits; ++i) m = fmaxf(m, ml[i * each * 2]);
-  float l = 0.0f, o[DIM / 64] = {};
-  for (int i = 0; i < a.splits; ++i) {
-    const float f = __builtin_amdgcn_exp2f(ml[i * each * 2] - m);
-    l += ml[i * each * 2 + 1] * f;
+  for (int i = lane; i < a.splits; i += 64) m = fmaxf(m, ml[i * each].x);
 #pragma unroll
-    for (int j = 0; j < DIM / 64; ++j)
-      o[j] += a.part[(i * each + at) * DIM + (DIM / 64) * lane + j] * f;
+  for (int k = 1; k < 64; k *= 2) m = fmaxf(m, __shfl_xor(m, k));
+  float l = 0.0f;
+  for (int i = lane; i < a.splits; i += 64) {
+    const float2 v = ml[i * each];
+    l += v.y * __builtin_amdgcn_exp2f(v.x - m);
   }
+#pragma unroll
+  for (int k = 1; k < 64; k *= 2) l += __shfl_xor(l, k);
+  const int d = 4 * (lane % kWide);
+  f32x4_t o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int i = lane / kWide; i < a.splits; i += kGroups) {
+    const float f = __builtin_amdgcn_exp2f(ml[i * each].x - m);
+    o += *reinterpret_cast<const f32x4_t*>(a.part + (i * each + at) * DIM + d) * f;
+  }
+#pragma unroll
+  for (int k = kWide; k < 64; k *= 2)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) o[c] += __shfl_xor(o[c], k);
+  if (lane >= kWide) return;
   const float inv = l != 0.0f ? 1.0f / l : 0.0f;
-  uint16_t* y = a.O + token * a.ldo + (int64_t)head * DIM + (DIM / 64) * lane;
-  if (DIM == 128)
-    *reinterpret_cast<uint32_t*>(y) = pack_bf16x2(o[0] * inv, o[DIM / 64 - 1] * inv);
-  else
-    y[0] = f32_to_bf16(o[0] * inv);
+  *reinterpret_cast<uint2*>(a.O + token * a.ldo + (int64_t)head * DIM + d) =
+      uint2{pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv)};
   if (a.lse && lane == 0)
     a.lse[at] = l != 0.0f ? 0.6931471805599453f * (m + __builtin_amdgcn_logf(l)) : -__builtin_inff();
 }
@@ -768,40 +798,50 @@ struct Plan {
   int64_t tiles, splits;
 };
 
-// Few rows per key head go to the kernel that splits pages over its waves; its page range is split
-// further until about three blocks per CU run (768 of 256 CUs), but never below eight pages a
-// block, where the join costs more than the parallelism brings.  The tile kernel runs two blocks
-// a CU, in rounds of that many: of up to 16 splits the one of the least
-//   rounds · (pages a block + 4 for its ends) + the join's traffic, in pages
-// is taken (1008 rows x 31688 tokens x 40 heads are 320 blocks, five eighths of a round, which
-// took 748 us; three splits, two nearly full rounds of a third, 598).
+// The kernel and the splits of the page range are the ones of the least time, in pages of a wave
+// (1.2 us at 64 channels, 2 at 128).  Both kernels run in rounds of 512 blocks, two a CU.
+//   tile: rounds · (pages a block + 4 for its ends), up to 16 splits
+//   few:  rounds · (a quarter of the pages + 5), but no less than its reads take: a page for each 32
+//         rows at 4.9 TB/s from memory, or 9 from the XCD's cache where a key head has several blocks
+// and with splits a join: its launch and the blocks' longer ends (4 and 8), and the fp32 rows written
+// and read at 5 TB/s.  Up to 32 rows there is no choice; above, few has no empty waves but reads each
+// page more often (40 rows x 16 sequences x 8192 tokens x 8 heads of 64: 34 us against 58; 128 rows
+// x 64 sequences x 2000 tokens: 59 against 45).  768 blocks of few instead of 512 took 47 us instead
+// of 39 for 32 rows x 2 sequences x 30000 x 8 heads of 128; one split, two nearly full rounds of a third
+// instead of five eighths of one, took tile from 748 to 598 us for 1008 rows x 31688 x 40 heads.
 Plan plan(int64_t G, int64_t Hkv, int64_t dim, int64_t rows, int64_t B, int64_t max_q,
           int64_t max_kv) {
-  Plan p;
-  p.few = max_q * G <= 32;
-  p.tiles = p.few ? 1 : (max_q * G + kTileRows - 1) / kTileRows;
-  const int64_t items = B * Hkv * p.tiles > 0 ? B * Hkv * p.tiles : 1;
-  const int64_t pages = (max_kv + kPage - 1) / kPage;
-  const int64_t most = pages / 8;
-  p.splits = 1;
-  if (p.few) {
-    const int64_t want = 768 / items;
-    p.splits = want < most ? want : most;
-    if (p.splits < 1) p.splits = 1;
-    return p;
-  }
-  const int64_t slots = 512;
-  double best = 0.0;
-  for (int64_t s = 1; s <= 16 && (s == 1 || s <= most); ++s) {
-    // a block takes about 1.2 us a page; the join writes and reads its fp32 rows at 5 TB/s
-    const double join = s == 1 ? 0.0 : 4.0 + (double)(s * rows * G * Hkv * (dim + 2)) * 8.0 / 6.0e6;
-    const double cost = (double)((items * s + slots - 1) / slots) * ((double)((pages + s - 1) / s) + 4.0) + join;
-    if (s == 1 || cost < best) {
-      best = cost;
-      p.splits = s;
+  constexpr int64_t kSlots = 512;
+  const int64_t R = max_q * G, heads = B * Hkv, pages = (max_kv + kPage - 1) / kPage;
+  const int64_t most = pages / 8 > 1 ? pages / 8 : 1;
+  Plan best{false, 1, 1};
+  double least = -1.0;
+  auto offer = [&](bool few, int64_t tiles, int64_t s) {
+    if (s < 1 || s > most) return;
+    const int64_t items = heads * tiles;
+    const double rounds = (double)((items * s + kSlots - 1) / kSlots);
+    double cost = rounds * (few ? (double)((pages + 4 * s - 1) / (4 * s)) + 5.0
+                                : (double)((pages + s - 1) / s) + 4.0);
+    if (few) {
+      const double reads = (tiles == 1 ? 2.8 : 1.5) * (double)(items * pages) / (4.0 * kSlots);
+      if (cost < reads) cost = reads;
     }
+    if (s > 1) cost += (few ? 4.0 : 8.0) + (double)(s * rows * G * Hkv * (dim + 2)) * 8.0 / 6.0e6;
+    if (least < 0.0 || cost < least) {
+      least = cost;
+      best = Plan{few, tiles, s};
+    }
+  };
+  const int64_t small = (R + kFewRows - 1) / kFewRows, large = (R + kTileRows - 1) / kTileRows;
+  if (R > kFewRows)
+    for (int64_t s = 1; s <= 16; ++s) offer(false, large, s);
+  if (R <= kFewMost && heads * small > 0) {
+    const int64_t one = kSlots / (heads * small);
+    offer(true, small, 1);
+    offer(true, small, one < most ? one : most);
+    offer(true, small, 2 * one + 1 < most ? 2 * one + 1 : most);
   }
-  return p;
+  return best;
 }
 
 }  // namespace
@@ -829,12 +869,17 @@ hipError_t launch_attn(const uint16_t* Q, int64_t ldq, int64_t rows, int64_t Hq,
              max_blocks, n_pages, (int)B, (int)Hq, (int)Hkv, (int)(Hq / Hkv), (int)p.tiles,
              (int)p.splits, causal, (int)max_q, (float)((double)scale * 1.4426950408889634)};
   const int64_t items = B * Hkv * p.tiles * p.splits;
-  const unsigned grid = (unsigned)(p.few ? items : (items + 7) / 8 * 8);
-  if (p.few) {
+  const unsigned grid = (unsigned)((items + 7) / 8 * 8);
+  if (p.few && p.tiles > 1) {
     if (dim == 64)
-      k_attn_few<64><<<grid, 256, 0, s>>>(a);
+      k_attn_few<64, true><<<grid, 256, 0, s>>>(a);
     else
-      k_attn_few<128><<<grid, 256, 0, s>>>(a);
+      k_attn_few<128, true><<<grid, 256, 0, s>>>(a);
+  } else if (p.few) {
+    if (dim == 64)
+      k_attn_few<64, false><<<(unsigned)items, 256, 0, s>>>(a);
+    else
+      k_attn_few<128, false><<<(unsigned)items, 256, 0, s>>>(a);
   } else {
     if (dim == 64)
       k_attn_tile<64><<<grid, 64 * kTileWaves, 0, s>>>(a);
