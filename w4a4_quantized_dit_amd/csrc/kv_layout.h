@@ -7,7 +7,8 @@
 // no swizzle (lane l reads bytes 16 l on: every bank once).
 //
 //   K, code (token t, channel d): fragment ((t/32)·(dim/64) + d/64)·2 + (d/16)%2,
-//      lane 32·((d/32)%2) + t%32, byte d%16 — the operand of a 32x32x64 f8f6f4 MFMA.
+//      lane 32·((d/32)%2) + t%32, byte d%16 — eight bytes are, widened, a lane's operand of a
+//      32x32x16 bf16 MFMA, whose channels are then 8 of each half of a block of 64.
 //   V, code (token t, channel d): fragment (d/32)·2 + t/32, lane 32·((t/4)%2) + d%32,
 //      byte 8·((t/16)%2) + 4·((t/8)%2) + t%4 — two operands of a 32x32x16 bf16 MFMA whose eight
 //      tokens per lane are those that the product K·Qᵀ leaves in one lane's registers.
