@@ -581,6 +581,7 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void k_attn_tile(AttnArgs a) {
       step(i, 0, za, zb);
       if (i + 1 < p1) step(i + 1, 1, zb, za);
     }
+    wait_vmcnt<0>();  // no copy is left in flight when the block ends and its LDS is another's
   }
   if (a.causal) {
     s_dirty[wave] = dirty;
