@@ -8,10 +8,10 @@
 // share every page read and single tokens still fill a matrix operand.
 //
 // Sᵀ = K·Qᵀ runs on the 32x32x16 bf16 MFMA: K's codes are widened exactly, with the page's exponent,
-// by the wave that needs them, and every product is exact in the fp32 sum.  (The FP8 MFMA on the codes
-// themselves, the query split into two E4M3 codes, took 4.39 ms instead of 4.77 for 16384 rows x
-// 16384 tokens x 40 heads of 128, but it aligns the products of neighbouring channels to the largest
-// of them with 13 bits: scores were off by 2^-16 of Σ|q_d k_d| instead of 2^-24.)
+// and every product is exact in the fp32 sum.  (The FP8 MFMA on the codes themselves, the query split
+// into two E4M3 codes, took 4.39 ms instead of 4.73 for 16384 rows x 16384 tokens x 40 heads of 128,
+// but it aligns the products of neighbouring channels to the largest of them with 13 bits: scores
+// were off by 2^-16 of Σ|q_d k_d| instead of 2^-24.)
 //
 // Oᵀ += Vᵀ·Pᵀ runs on the 32x32x16 bf16 MFMA: V's codes are widened exactly (with the page's
 // exponent) and P is rounded to bf16 once, a relative 2^-9 per weight against l's unrounded
@@ -28,9 +28,6 @@
 namespace svdq {
 
 namespace {
-
-typedef __attribute__((address_space(1))) void gvoid_t;
-typedef __attribute__((address_space(3))) void lvoid_t;
 
 constexpr float kNoMax = -3.0e38f;  // running maximum before the first visible token
 constexpr float kRaise = 8.0f;
@@ -345,10 +342,10 @@ __device__ __forceinline__ void store_row(const AttnArgs& a, const State<DIM>& s
     a.lse[token * a.Hq + head] = lse_of(a, st.m, l);
 }
 
-// Many rows: four waves of 32 rows share each page through LDS.  K's codes are copied there as
-// they are, asynchronously, one page ahead.  V's go through registers two pages ahead and are
-// widened to bf16 on the way, once for the four waves (each wave widening all of them for itself
-// took a third of its vector instructions).  Two images of each, one barrier a page.
+// Many rows: four waves of 32 rows share each page through LDS.  Its codes go through registers, V's
+// two pages ahead and K's three, and are widened to bf16 on the way, once for the four waves (each
+// wave widening all of V for itself took a third of its vector instructions, all of K 3 % of the
+// time of 16384 x 16384 x 40 heads of 128).  Two images of each, one barrier a page.
 constexpr int kTileWaves = 4;
 constexpr int kTileRows = 32 * kTileWaves;
 
@@ -356,10 +353,7 @@ template <int DIM>
 __global__ __launch_bounds__(64 * kTileWaves, 2) void k_attn_tile(AttnArgs a) {
   constexpr int kBytes = kPage * DIM;                       // one tensor's page
   constexpr int kCopies = kBytes / 1024 / kTileWaves;       // fragments per wave, K and V each
-  // (arrays of their own: the compiler then sees that the copy into one K image does not touch
-  // the reads of the other, and does not wait for it in front of them)
-  __shared__ __attribute__((aligned(16))) uint8_t k_img0[kBytes], k_img1[kBytes];
-  __shared__ __attribute__((aligned(16))) uint8_t v_img[2][2 * kBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t k_img[2][2 * kBytes], v_img[2][2 * kBytes];
   __shared__ int s_dirty[kTileWaves];
   const int64_t total = (int64_t)a.B * a.Hkv * a.splits * a.tiles;
   const int64_t per_xcd = (total + 7) / 8;
@@ -397,14 +391,12 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void k_attn_tile(AttnArgs a) {
   const int64_t page_bytes = (int64_t)a.Hkv * kBytes;
   const uint8_t* k_src = a.kc + head_off + wave * kCopies * 1024;
   const uint8_t* v_src = a.vc + head_off + wave * kCopies * 1024;
-  auto copy_k = [&](int page, int slot) {
+  u32x4_t kr[kCopies], vr[kCopies];
+  auto load_k = [&](int page) {
 #pragma unroll
     for (int i = 0; i < kCopies; ++i)
-      __builtin_amdgcn_global_load_lds((gvoid_t*)(k_src + page * page_bytes + i * 1024),
-                                       (lvoid_t*)(&(slot ? k_img1 : k_img0)[(wave * kCopies + i) * 1024]),
-                                       16, 0, 0);
+      kr[i] = *reinterpret_cast<const u32x4_t*>(k_src + page * page_bytes + i * 1024);
   };
-  u32x4_t vr[kCopies];
   auto load_v = [&](int page) {
 #pragma unroll
     for (int i = 0; i < kCopies; ++i)
@@ -426,21 +418,30 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void k_attn_tile(AttnArgs a) {
       for (int f = 0; f < kCopies; ++f) vr[f] = clear_nan(vr[f], dirty);
     }
   };
-  // fragment f: its two 16-token steps of 1 KB each
-  auto widen_v = [&](int exps, int slot) {
-    const float scale = two_to(((exps >> 8) & 255) - 127);
-#pragma unroll
-    for (int i = 0; i < kCopies; ++i)
-#pragma unroll
-      for (int g = 0; g < 2; ++g)
-        *reinterpret_cast<bf16x8_t*>(
-            &v_img[slot][(2 * (wave * kCopies + i) + g) * 1024 + lane * 16]) =
-            widen8(vr[i][2 * g], vr[i][2 * g + 1], scale);
+  // step g of the wave's fragment f: 16 tokens of V, or 8 channels of each half of K's block of 64
+  auto widen = [&](uint8_t* img, const u32x4_t& r, int f, int g, float scale) {
+    *reinterpret_cast<bf16x8_t*>(img + (2 * (wave * kCopies + f) + g) * 1024 + lane * 16) =
+        widen8(r[2 * g], r[2 * g + 1], scale);
   };
-  auto page_scores = [&](int exps, int slot, f32x16_t (&z)[2]) {
-    const uint8_t* k = (slot ? k_img1 : k_img0) + lane * 16;
-    scores<DIM>(z, q, two_to((exps & 255) - 127),
-                [&](int f) { return *reinterpret_cast<const u32x4_t*>(k + f * 1024); });
+  auto widen_k = [&](int exps, int slot) {
+#pragma unroll
+    for (int n = 0; n < 2 * kCopies; ++n)
+      widen(k_img[slot], kr[n / 2], n / 2, n % 2, two_to((exps & 255) - 127));
+  };
+  auto widen_v = [&](int exps, int slot) {
+#pragma unroll
+    for (int n = 0; n < 2 * kCopies; ++n)
+      widen(v_img[slot], vr[n / 2], n / 2, n % 2, two_to(((exps >> 8) & 255) - 127));
+  };
+  constexpr int kQk = 8 * (DIM / 64), kPv = 4 * (DIM / 32);
+  auto k_operand = [&](int slot, int n) {
+    return *reinterpret_cast<const bf16x8_t*>(&k_img[slot][n * 1024 + lane * 16]);
+  };
+  auto product = [&](f32x16_t (&z)[2], int n, bf16x8_t k) {
+    const int tb = n / (kQk / 2), m = n % (kQk / 2);
+    if (m == 0) z[tb] = f32x16_t{};
+    z[tb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, __builtin_bit_cast(bf16x8_t, q.w[m / 4][m % 4]),
+                                                    z[tb], 0, 0, 0);
   };
   auto mask = [&](int i, int exps, f32x16_t (&z)[2]) {
     if (!(exps & kPresent) || i >= lim_first / kPage) {
@@ -451,8 +452,8 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void k_attn_tile(AttnArgs a) {
   };
 
   if (p0 < p1) {
-    // lane l: page number and exponents of logical page g0 + l.  The copies need the numbers
-    // only, the exponents come and the query is split while they are on their way.
+    // lane l: page number and exponents of logical page g0 + l.  The loads need the numbers only,
+    // the exponents come and the query is looked over while they are on their way.
     int g0 = p0, meta = page_id(a, s, g0 + lane, p1), meta_e;
     auto lane_of = [&](int i) { return (i < p1 ? i : p1 - 1) - g0; };
     auto page_at = [&](int i) { return __builtin_amdgcn_readlane(meta, lane_of(i)); };
@@ -460,30 +461,33 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void k_attn_tile(AttnArgs a) {
 
     f32x16_t za[2], zb[2];
     {
-      const int first = page_at(p0), second = page_at(p0 + 1);
-      copy_k(first < 0 ? 0 : first, 0);
+      const int first = page_at(p0);
+      load_k(first < 0 ? 0 : first);
       load_v(first < 0 ? 0 : first);
-      copy_k(second < 0 ? 0 : second, 1);
       meta_e = page_exps(a, s, meta);
     }
     query_check(q);
     const int e0 = exps_at(p0);
     trim_v(p0, e0);
+    widen_k(e0, 0);
+    load_k(page_at(p0 + 1));
     widen_v(e0, 0);
     load_v(page_at(p0 + 1));
-    wait_vmcnt<0>();
+    widen_k(exps_at(p0 + 1), 1);
+    load_k(page_at(p0 + 2));
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    page_scores(e0, 0, za);
+#pragma unroll
+    for (int n = 0; n < kQk; ++n) product(za, n, k_operand(0, n));
     mask(p0, e0, za);
     raise(st, largest(za, a.c));
 
     // Page i, whose scores are in z: its exponentials run while the matrix units form the next
-    // page's scores, and the next page's V is widened while they form this page's product.
+    // page's scores, and the next page's V and the keys behind it are widened while they form
+    // this page's product.
     // Pages behind the last repeat it; what is computed of them is not used.
     auto step = [&](int i, int slot, f32x16_t (&z)[2], f32x16_t (&zn)[2]) {
       // K of page i + 1 and V of page i are in LDS for every wave, and every wave is done with
-      // what takes their places (V loads of page i + 1 may still be in flight)
-      wait_vmcnt<kCopies>();
+      // what takes their places (V of page i + 1 and K of page i + 2 may still be on their way)
       asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
       if (i - g0 >= 61) {
         g0 = i;
@@ -494,19 +498,13 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void k_attn_tile(AttnArgs a) {
       trim_v(i + 1, e1);
       // From here to the masks one block without branches, its order fixed: a wave issues in
       // order, so what is to run under a matrix instruction has to stand right behind it.
-      const int ahead = page_at(i + 2);
-      copy_k(ahead, slot);
-      const uint8_t* kp = (slot ? k_img0 : k_img1) + lane * 16;
+      const int v_next = page_at(i + 2), k_next = page_at(i + 3);
+      const float k_scale = two_to((exps_at(i + 2) & 255) - 127);
+      const float v_scale = two_to(((e1 >> 8) & 255) - 127);
       const uint8_t* vp = v_img[slot] + lane * 16;
-      const float k_scale = two_to((e1 & 255) - 127);
-      u32x4_t kr[2][DIM / 32], w[4];
-      bf16x8_t vb[4];
+      u32x4_t w[4];
+      bf16x8_t kb[4], vb[4];
       float sum = 0.0f;
-      auto k_read = [&](int tb) {
-#pragma unroll
-        for (int f = 0; f < DIM / 32; ++f)
-          kr[tb][f] = *reinterpret_cast<const u32x4_t*>(kp + (tb * (DIM / 32) + f) * 1024);
-      };
       // V operand n: channels 32 (n % (DIM/32)) on, token step n / (DIM/32)
       auto v_read = [&](int n) {
         const int j = n % (DIM / 32), t = n / (DIM / 32);
@@ -523,18 +521,13 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void k_attn_tile(AttnArgs a) {
         asm volatile("" : "+v"(sum), "+v"(both));  // formed here, not behind the block
         w[n >> 2][n & 3] = both;
       };
-      constexpr int kQk = 8 * (DIM / 64), kPv = 4 * (DIM / 32);
-      k_read(0);
+#pragma unroll
+      for (int n = 0; n < 4; ++n) kb[n] = k_operand(slot ^ 1, n);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int n = 0; n < kQk; ++n) {
-        const int tb = n / (kQk / 2), sc = n % (kQk / 2) / 4, j = n % 4;
-        const u32x4_t k = kr[tb][2 * sc + j / 2];
-        if (n % (kQk / 2) == 0) zn[tb] = f32x16_t{};
-        zn[tb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-            widen8(k[2 * (j & 1)], k[2 * (j & 1) + 1], k_scale),
-            __builtin_bit_cast(bf16x8_t, q.w[sc][j]), zn[tb], 0, 0, 0);
-        if (n == 0) k_read(1);
+        product(zn, n, kb[n % 4]);
+        if (n + 4 < kQk) kb[n % 4] = k_operand(slot ^ 1, n + 4);
         if (n == kQk - 1) {
 #pragma unroll
           for (int f = 0; f < 4; ++f) v_read(f);
@@ -557,22 +550,18 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void k_attn_tile(AttnArgs a) {
         for (int n = 0; n < 16; ++n) pair(n);
       }
       st.l += sum;
-      // the next page's V has arrived (the copies of K behind it may be in flight)
-      wait_vmcnt<kCopies>();
-      const float scale = two_to(((e1 >> 8) & 255) - 127);
 #pragma unroll
       for (int n = 0; n < kPv; ++n) {
         const int j = n % (DIM / 32), t = n / (DIM / 32);
         st.o[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
             vb[n % 4], __builtin_bit_cast(bf16x8_t, w[t]), st.o[j], 0, 0, 0);
         if (n + 4 < kPv) v_read(n + 4);
-        if (n % 2 == 0 && n / 2 < 2 * kCopies) {  // one 16-token step of the next page's V
-          const int f = n / 4, g = n / 2 % 2;
-          *reinterpret_cast<bf16x8_t*>(
-              &v_img[slot ^ 1][(2 * (wave * kCopies + f) + g) * 1024 + lane * 16]) =
-              widen8(vr[f][2 * g], vr[f][2 * g + 1], scale);
-        }
-        if (n == kPv / 2) load_v(ahead);
+        // the next page's V, then the keys of the one behind it, a step at a time
+        if (n % 2 == 0 && n < kPv / 2) widen(v_img[slot ^ 1], vr[n / 4], n / 4, n / 2 % 2, v_scale);
+        if (n % 2 == 0 && n >= kPv / 2)
+          widen(k_img[slot], kr[(n - kPv / 2) / 4], (n - kPv / 2) / 4, n / 2 % 2, k_scale);
+        if (n == kPv / 2) load_v(v_next);
+        if (n == kPv - 1) load_k(k_next);
         __builtin_amdgcn_sched_barrier(0);
       }
       mask(i + 1, e1, zn);
@@ -581,7 +570,6 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void k_attn_tile(AttnArgs a) {
       step(i, 0, za, zb);
       if (i + 1 < p1) step(i + 1, 1, zb, za);
     }
-    wait_vmcnt<0>();  // no copy is left in flight when the block ends and its LDS is another's
   }
   if (a.causal) {
     s_dirty[wave] = dirty;
