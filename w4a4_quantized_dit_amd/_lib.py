@@ -532,7 +532,7 @@ class _Args:
 
     def _at(self, t, name):
         dev = t.get_device()
-        if dev != self.dev:
+        if dev != self.dev or dev < 0:   # (a host tensor's device is -1, like no device yet)
             if dev < 0:
                 raise ValueError(f"{name} must be a device tensor")
             if self.dev >= 0:
