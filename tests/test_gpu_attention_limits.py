@@ -1,0 +1,52 @@
+"""GPU tests of svdq_attn_kv8 at the limits of its host bounds (oracle and tolerances of
+test_gpu_attention)."""
+import numpy as np
+import pytest
+
+from oracle import attention as OA
+from oracle.formats import bf16_bits_to_f32, bf16_rne
+from tests.gpu_common import dev_bf16, host_bits, torch_mod
+from tests.test_gpu_attention import L, check, device_cache, i32, make_cache  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def test_loose_bounds_of_rows_and_tokens(L):  # noqa: F811
+    """max_rows = 2^26 + 128 and max_kv = 2^20 for 1000 rows over 300 tokens: the page range is split
+    for the bounds' sake, and a block of the joining kernel for each row of the bound would be more
+    than a launch holds."""
+    from w4a4_quantized_dit_amd import _lib
+    torch = torch_mod()
+    dim, rows, kv, bound = 64, 1000, 300, (1 << 26) + 128
+    assert _lib.svdq_attn_kv8_workspace_bytes(rows, 1, 1, dim, 1, bound, 1 << 20) > 0
+    rng = np.random.default_rng(31)
+    c, table = make_cache(rng, [kv], 1, dim)
+    bits = bf16_rne(rng.standard_normal((rows, dim)).astype(np.float32))
+    for causal in (False, True):
+        O, lse = L.attention(dev_bf16(bits), device_cache(L, c), i32(table), i32([0, rows]),
+                             i32([kv]), bound, 1 << 20, causal=causal, return_lse=True)
+        torch.cuda.synchronize()
+        want = OA.attention(bf16_bits_to_f32(bits).reshape(rows, 1, dim), c, table,
+                            np.array([0, rows]), [kv], 0.125, causal)
+        check(want, O.float().cpu().numpy().reshape(rows, 1, dim).astype(np.float64),
+              lse.cpu().numpy().astype(np.float64), kv)
+
+
+def test_more_rows_than_the_join_has_blocks_for(L):  # noqa: F811
+    """2^22 + 200 rows with a split: the joining kernel's blocks take a second sweep."""
+    from w4a4_quantized_dit_amd import _lib
+    torch = torch_mod()
+    dim, rows, kv, n = 64, (1 << 22) + 200, 100, 300
+    assert _lib.svdq_attn_kv8_workspace_bytes(rows, 1, 1, dim, 1, rows, 1 << 18) > 0
+    rng = np.random.default_rng(32)
+    c, table = make_cache(rng, [kv], 1, dim)
+    g = torch.Generator(device="cuda").manual_seed(6)
+    Q = torch.randn(rows, dim, generator=g, device="cuda").to(torch.bfloat16)
+    O, lse = L.attention(Q, device_cache(L, c), i32(table), i32([0, rows]), i32([kv]), rows, 1 << 18,
+                         return_lse=True)
+    torch.cuda.synchronize()
+    for part in (slice(0, n), slice((1 << 22) - n, (1 << 22) + 200)):
+        q = bf16_bits_to_f32(host_bits(Q[part])).reshape(-1, 1, dim)
+        want = OA.attention(q, c, table, np.array([0, len(q)]), [kv], 0.125, False)
+        check(want, O[part].float().cpu().numpy().reshape(-1, 1, dim).astype(np.float64),
+              lse[part].cpu().numpy().astype(np.float64), kv)

@@ -718,10 +718,13 @@ __global__ __launch_bounds__(256, 2) void k_attn_few(AttnArgs a) {
   }
 }
 
-// The splits of every row joined, one wave per row of sequence blockIdx.y.  The lanes take the
-// splits' maxima side by side, and groups of DIM / 4 lanes, four channels each, take every second
-// (DIM 128) or fourth split, several loads under way at once (one split after the other with all
-// lanes took 25 us for 128 rows of 48 splits, now 4).
+// The splits of every row joined, a wave a row of sequence blockIdx.y, the blocks in sweeps of
+// kJoinMost where a sequence has more rows (a launch has fewer than 2^32 threads in a dimension).  The
+// lanes take the splits' maxima side by side, and groups of DIM / 4 lanes, four channels each, take
+// every second (DIM 128) or fourth split, several loads under way at once (one split after the other
+// with all lanes took 25 us for 128 rows of 48 splits, now 4).
+constexpr int64_t kJoinMost = 1 << 20;
+
 template <int DIM>
 __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
   constexpr int kWide = DIM / 4, kGroups = 64 / kWide;
@@ -729,40 +732,41 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
   const int first = a.cu[b], end = a.cu[b + 1];
   if (first < 0 || end <= first || end > a.rows) return;
   const int n = end - first < a.max_q ? end - first : a.max_q;
-  const int64_t local = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (local >= (int64_t)n * a.Hq) return;
-  const int64_t at = (int64_t)first * a.Hq + local, token = at / a.Hq;
-  const int head = (int)(at % a.Hq);
-  const int64_t each = a.rows * a.Hq;
-  const float2* ml = reinterpret_cast<const float2*>(a.part + a.splits * each * DIM) + at;
-  float m = kNoMax;
-  for (int i = lane; i < a.splits; i += 64) m = fmaxf(m, ml[i * each].x);
+  const int64_t each = a.rows * a.Hq, rows = (int64_t)n * a.Hq;
+  for (int64_t local = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); local < rows;
+       local += (int64_t)gridDim.x * 4) {
+    const int64_t at = (int64_t)first * a.Hq + local, token = at / a.Hq;
+    const int head = (int)(at % a.Hq);
+    const float2* ml = reinterpret_cast<const float2*>(a.part + a.splits * each * DIM) + at;
+    float m = kNoMax;
+    for (int i = lane; i < a.splits; i += 64) m = fmaxf(m, ml[i * each].x);
 #pragma unroll
-  for (int k = 1; k < 64; k *= 2) m = fmaxf(m, __shfl_xor(m, k));
-  float l = 0.0f;
-  for (int i = lane; i < a.splits; i += 64) {
-    const float2 v = ml[i * each];
-    l += v.y * __builtin_amdgcn_exp2f(v.x - m);
-  }
+    for (int k = 1; k < 64; k *= 2) m = fmaxf(m, __shfl_xor(m, k));
+    float l = 0.0f;
+    for (int i = lane; i < a.splits; i += 64) {
+      const float2 v = ml[i * each];
+      l += v.y * __builtin_amdgcn_exp2f(v.x - m);
+    }
 #pragma unroll
-  for (int k = 1; k < 64; k *= 2) l += __shfl_xor(l, k);
-  const int d = 4 * (lane % kWide);
-  f32x4_t o = {0.f, 0.f, 0.f, 0.f};
+    for (int k = 1; k < 64; k *= 2) l += __shfl_xor(l, k);
+    const int d = 4 * (lane % kWide);
+    f32x4_t o = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
-  for (int i = lane / kWide; i < a.splits; i += kGroups) {
-    const float f = __builtin_amdgcn_exp2f(ml[i * each].x - m);
-    o += *reinterpret_cast<const f32x4_t*>(a.part + (i * each + at) * DIM + d) * f;
+    for (int i = lane / kWide; i < a.splits; i += kGroups) {
+      const float f = __builtin_amdgcn_exp2f(ml[i * each].x - m);
+      o += *reinterpret_cast<const f32x4_t*>(a.part + (i * each + at) * DIM + d) * f;
+    }
+#pragma unroll
+    for (int k = kWide; k < 64; k *= 2)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) o[c] += __shfl_xor(o[c], k);
+    if (lane >= kWide) continue;
+    const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+    *reinterpret_cast<uint2*>(a.O + token * a.ldo + (int64_t)head * DIM + d) =
+        uint2{pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv)};
+    if (a.lse && lane == 0)
+      a.lse[at] = lse_of(a, m, l);
   }
-#pragma unroll
-  for (int k = kWide; k < 64; k *= 2)
-#pragma unroll
-    for (int c = 0; c < 4; ++c) o[c] += __shfl_xor(o[c], k);
-  if (lane >= kWide) return;
-  const float inv = l != 0.0f ? 1.0f / l : 0.0f;
-  *reinterpret_cast<uint2*>(a.O + token * a.ldo + (int64_t)head * DIM + d) =
-      uint2{pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv)};
-  if (a.lse && lane == 0)
-    a.lse[at] = lse_of(a, m, l);
 }
 
 struct Plan {
@@ -862,7 +866,9 @@ hipError_t launch_attn(const uint16_t* Q, int64_t ldq, int64_t rows, int64_t Hq,
   }
   if (hipError_t e = hipGetLastError()) return e;
   if (p.splits > 1) {
-    const dim3 joins((unsigned)((max_q * Hq + 3) / 4), (unsigned)B);
+    // (no sequence has more than all rows, however loose the caller's bound)
+    const int64_t blocks = ((max_q < rows ? max_q : rows) * Hq + 3) / 4;
+    const dim3 joins((unsigned)(blocks < kJoinMost ? blocks : kJoinMost), (unsigned)B);
     if (dim == 64)
       k_attn_join<64><<<joins, 256, 0, s>>>(a);
     else
