@@ -569,7 +569,9 @@ svdq_status svdq_kv_read(uint16_t* K, int64_t ldk, uint16_t* V, int64_t ldv, int
  * Codes of tokens that a row does not see have no part in its result, NaN codes included; a NaN
  * in a key that it sees, or an infinity or NaN in its query, makes the row and its lse NaN, one in
  * a value that it sees that channel.  Scores up to 2^27 in magnitude (fp32 holds no difference
- * between larger ones).
+ * between larger ones).  The weighted values are summed before the division by the weights' sum: O is
+ * sure to be finite where max|v|·kv_len stays below 2^135 (2^127 with scores past 2^23); values below
+ * 2^-110 may count as 0.
  * Rows of no sequence are left as they were.  lse: fp32 [rows, q_heads], may be NULL.
  * scale > 0 and finite.  max_rows, max_kv: host bounds of one sequence's rows and of kv_len (they
  * size the grid and the split; rows past max_rows are not computed, kv_len itself is not

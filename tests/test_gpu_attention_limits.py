@@ -50,3 +50,60 @@ def test_more_rows_than_the_join_has_blocks_for(L):  # noqa: F811
         want = OA.attention(q, c, table, np.array([0, len(q)]), [kv], 0.125, False)
         check(want, O[part].float().cpu().numpy().reshape(-1, 1, dim).astype(np.float64),
               lse[part].cpu().numpy().astype(np.float64), kv)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("q,kv,G", [(1, 2, 1), (1, 130, 4), (40, 130, 1), (600, 200, 1), (3, 5000, 1),
+                                    (150, 5000, 1)])
+@pytest.mark.parametrize("causal", [False, True])
+def test_values_near_the_caches_largest(L, q, kv, G, dim, causal):  # noqa: F811
+    """Values to 2.9e38: the weighted sum passes fp32's range unless it is scaled, the average does
+    not.  Equal weights (zero queries), and weights over a wide range."""
+    torch = torch_mod()
+    rng = np.random.default_rng(q + kv)
+    pages = (kv + 63) // 64
+    c = OA.new_cache(pages + 1, 1, dim, fill=0xFF)
+    table = rng.permutation(pages + 1)[:pages][None]
+    K = bf16_rne(rng.standard_normal((kv, dim)).astype(np.float32))
+    V = bf16_rne((rng.uniform(1.9e38, 2.9e38, (kv, dim)) * rng.choice([-1, 1], (1, dim)))
+                 .astype(np.float32))
+    OA.kv_write(c, K, V, table, np.array([0, kv]), [0])
+    for spread in (0.0, 3.0):
+        bits = bf16_rne((rng.standard_normal((q, G * dim)) * spread).astype(np.float32))
+        O, lse = L.attention(dev_bf16(bits), device_cache(L, c), i32(table), i32([0, q]), i32([kv]),
+                             q, kv, causal=causal, return_lse=True)
+        torch.cuda.synchronize()
+        assert torch.isfinite(O.float()).all()
+        want = OA.attention(bf16_bits_to_f32(bits).reshape(q, G, dim), c, table, np.array([0, q]),
+                            [kv], float(np.float32(dim ** -0.5)), causal)
+        check(want, O.float().cpu().numpy().reshape(q, G, dim).astype(np.float64),
+              lse.cpu().numpy().astype(np.float64), kv)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("q,kv", [(1, 130), (40, 130), (600, 200), (3, 5000)])
+def test_values_near_the_caches_smallest(L, q, kv, dim):  # noqa: F811
+    """Values from 2^-119 on: right but for what may count as 0, 2^-110 of the weights' whole."""
+    torch = torch_mod()
+    rng = np.random.default_rng(q + kv)
+    pages = (kv + 63) // 64
+    c = OA.new_cache(pages, 1, dim, fill=0xFF)
+    table = rng.permutation(pages)[None]
+    K = bf16_rne(rng.standard_normal((kv, dim)).astype(np.float32))
+    V = bf16_rne((rng.uniform(1, 2, (kv, dim)) * 2.0 ** rng.integers(-119, -95, (kv, dim)))
+                 .astype(np.float32))
+    OA.kv_write(c, K, V, table, np.array([0, kv]), [0])
+    bits = bf16_rne(rng.standard_normal((q, dim)).astype(np.float32))
+    O, lse = L.attention(dev_bf16(bits), device_cache(L, c), i32(table), i32([0, q]), i32([kv]), q, kv,
+                         return_lse=True)
+    torch.cuda.synchronize()
+    want = OA.attention(bf16_bits_to_f32(bits).reshape(q, 1, dim), c, table, np.array([0, q]), [kv],
+                        float(np.float32(dim ** -0.5)), False)
+    got = O.float().cpu().numpy().reshape(q, 1, dim).astype(np.float64)
+    up = 2.0 ** 60     # (the shared check allows 1e-37 on its own)
+    err = np.abs(got - want["O"]) * up
+    dz = want["absz"] * 132 * 2.0 ** -23
+    A, W = want["absO"] * up, np.abs(want["O"]) * up
+    tol = 2.0 ** -8 * (A + W) * (1 + 2.0 ** -7) + (2 * np.expm1(dz)[..., None] + 2.0 ** -20
+                                                  + kv * 2.0 ** -23) * (A + W) + 2.0 ** -110 * up
+    assert np.all(err <= tol)

@@ -33,6 +33,12 @@ constexpr float kNoMax = -3.0e38f;  // running maximum before the first visible 
 constexpr float kRaise = 8.0f;
 constexpr float kMostSum = 4096.0f;
 
+// V is widened as 2^-16 of itself and O brought back where it is stored, exact steps both: the sum of
+// V over its weights is formed before the division by theirs, and cached values reach 2^128.  Sixteen
+// bits are what the smallest page exponent leaves (-110 - 16 is that of fp32's smallest normal).
+constexpr int kDown = 16;
+constexpr float kUp = 65536.0f;
+
 struct AttnArgs {
   const uint16_t* Q;
   uint16_t* O;
@@ -292,13 +298,14 @@ __device__ __forceinline__ int page_id(const AttnArgs& a, const Seq& s, int at, 
   return p >= 0 && p < a.n_pages ? p : -1;
 }
 
-// Exponent bytes (k | v << 8 | kPresent) of a page, no flag outside the cache; the number of a
-// missing page becomes 0, which can be read.
+// Exponent bytes (k | v << 8 | kPresent, V's less kDown) of a page, no flag outside the cache; the
+// number of a missing page becomes 0, which can be read.
 __device__ __forceinline__ int page_exps(const AttnArgs& a, const Seq& s, int& page) {
   const bool there = page >= 0;
   page = there ? page : 0;
   const int64_t i = (int64_t)page * a.Hkv + s.h;
-  const int e = (int)a.ks[i] | (int)a.vs[i] << 8;
+  const int v = (int)a.vs[i] - kDown;  // (below 0: only in a page that was never written)
+  const int e = (int)a.ks[i] | (v < 0 ? 0 : v) << 8;
   return there ? e | kPresent : 0;
 }
 
@@ -330,14 +337,15 @@ __device__ __forceinline__ void store_row(const AttnArgs& a, const State<DIM>& s
     return;
   }
   const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+  auto value = [&](int j, int i) { return st.o[j][i] * inv * kUp; };
   uint16_t* o = a.O + token * a.ldo + (int64_t)head * DIM;
 #pragma unroll
   for (int j = 0; j < DIM / 32; ++j)
 #pragma unroll
     for (int g = 0; g < 4; ++g)
       *reinterpret_cast<uint2*>(o + 32 * j + 8 * g + 4 * half) =
-          uint2{pack_bf16x2(st.o[j][4 * g] * inv, st.o[j][4 * g + 1] * inv),
-                pack_bf16x2(st.o[j][4 * g + 2] * inv, st.o[j][4 * g + 3] * inv)};
+          uint2{pack_bf16x2(value(j, 4 * g), value(j, 4 * g + 1)),
+                pack_bf16x2(value(j, 4 * g + 2), value(j, 4 * g + 3))};
   if (a.lse && half == 0)
     a.lse[token * a.Hq + head] = lse_of(a, st.m, l);
 }
@@ -711,7 +719,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_few(AttnArgs a) {
         ml[1] = l;
       }
     } else {
-      a.O[token * a.ldo + (int64_t)hd * DIM + d] = f32_to_bf16(l != 0.0f ? sum / l : 0.0f);
+      a.O[token * a.ldo + (int64_t)hd * DIM + d] = f32_to_bf16(l != 0.0f ? sum / l * kUp : 0.0f);
       if (a.lse && d == 0)
         a.lse[token * a.Hq + hd] = lse_of(a, mm, l);
     }
@@ -763,7 +771,8 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
     if (lane >= kWide) continue;
     const float inv = l != 0.0f ? 1.0f / l : 0.0f;
     *reinterpret_cast<uint2*>(a.O + token * a.ldo + (int64_t)head * DIM + d) =
-        uint2{pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv)};
+        uint2{pack_bf16x2(o[0] * inv * kUp, o[1] * inv * kUp),
+              pack_bf16x2(o[2] * inv * kUp, o[3] * inv * kUp)};
     if (a.lse && lane == 0)
       a.lse[at] = lse_of(a, m, l);
   }
