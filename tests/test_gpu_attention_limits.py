@@ -5,8 +5,9 @@ import pytest
 
 from oracle import attention as OA
 from oracle.formats import bf16_bits_to_f32, bf16_rne
-from tests.gpu_common import dev_bf16, host_bits, torch_mod
-from tests.test_gpu_attention import L, check, device_cache, i32, make_cache  # noqa: F401
+from tests.gpu_common import dev, dev_bf16, host_bits, torch_mod
+from tests.test_gpu_attention import (Block, L, _chain_inputs, check, device_cache,  # noqa: F401
+                                      i32, make_cache)
 
 pytestmark = pytest.mark.gpu
 
@@ -107,3 +108,61 @@ def test_values_near_the_caches_smallest(L, q, kv, dim):  # noqa: F811
     tol = 2.0 ** -8 * (A + W) * (1 + 2.0 ** -7) + (2 * np.expm1(dz)[..., None] + 2.0 ** -20
                                                   + kv * 2.0 ** -23) * (A + W) + 2.0 ** -110 * up
     assert np.all(err <= tol)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("q", [1, 64, 600])
+@pytest.mark.parametrize("causal", [False, True])
+def test_length_past_the_page_table(L, q, dim, causal):  # noqa: F811
+    """kv_len is limited to the table's 64·max_blocks tokens, the causal mask's last row sees them all;
+    a negative one counts as none."""
+    torch = torch_mod()
+    rng = np.random.default_rng(33)
+    c, table = make_cache(rng, [448, 448, 448], 1, dim)
+    bits = bf16_rne(rng.standard_normal((3 * q, dim)).astype(np.float32))
+    cu, lens = np.array([0, q, 2 * q, 3 * q]), [10 ** 6, 2 ** 31 - 1, -5]
+    O, lse = L.attention(dev_bf16(bits), device_cache(L, c), i32(table), i32(cu), i32(lens), q, 448,
+                         causal=causal, return_lse=True)
+    torch.cuda.synchronize()
+    qf = bf16_bits_to_f32(bits).reshape(3 * q, 1, dim)
+    want = OA.attention(qf, c, table, cu, [448, 448, 0], float(np.float32(dim ** -0.5)), causal)
+    check(want, O.float().cpu().numpy().reshape(3 * q, 1, dim).astype(np.float64),
+          lse.cpu().numpy().astype(np.float64), 448)
+
+
+def test_lse_of_the_chain(L):  # noqa: F811
+    """The attention half as it is used, prompts and then single tokens: the lse that the attention
+    gives there, against the oracle on the rows that the stages before it wrote."""
+    torch = torch_mod()
+
+    class Noted:
+        """The layer, with the lse of its attention kept."""
+        def __getattr__(self, name):
+            return getattr(L, name)
+
+        def attention(self, *a, **k):
+            O, self.lse = L.attention(*a, return_lse=True, **k)
+            return O
+
+    rng = np.random.default_rng(34)
+    noted = Noted()
+    blk = Block(noted)
+    w, Hq, Hkv = blk.dim, blk.Hq, blk.Hkv
+    c = OA.new_cache(9, Hkv, w, fill=0xFF)
+    kv = device_cache(L, c)
+    table = rng.permutation(9)[:6].reshape(2, 3)
+    have = np.array([0, 0])
+    for lens in ([100, 37], [1, 1], [30, 1]):
+        cu = np.concatenate([[0], np.cumsum(lens)])
+        x, res, pos = _chain_inputs(rng, cu[-1], blk.K)
+        _, qkv, O, _ = blk.step(kv, dev_bf16(x), dev_bf16(res), dev(pos), i32(table), i32(cu),
+                                i32(have), i32(have + lens), max(lens), 192)
+        torch.cuda.synchronize()
+        have = have + lens
+        got = host_bits(qkv)
+        for name, t in (("kc", kv.k_codes), ("vc", kv.v_codes), ("ks", kv.k_scales), ("vs", kv.v_scales)):
+            c[name] = t.cpu().numpy()
+        want = OA.attention(bf16_bits_to_f32(got[:, :Hq * w]).reshape(-1, Hq, w), c, table, cu, have,
+                            w ** -0.5, True)
+        check(want, O.float().cpu().numpy().reshape(-1, Hq, w).astype(np.float64),
+              noted.lse.cpu().numpy().astype(np.float64), 192)
