@@ -14,9 +14,11 @@
 // were off by 2^-16 of Σ|q_d k_d| instead of 2^-24.)
 //
 // Oᵀ += Vᵀ·Pᵀ runs on the 32x32x16 bf16 MFMA: V's codes are widened exactly (with the page's
-// exponent) and P is rounded to bf16 once, a relative 2^-9 per weight against l's unrounded
-// sum.  The accumulator of Sᵀ holds, per lane, one row's weights in exactly the token order of
-// the stored V, so P needs no exchange between lanes.
+// exponent) and P is rounded to bf16 once, at most 2^-8 of each weight against l's unrounded sum
+// (1.1 to 1.4e-3 of O in the root mean square, where rounding O itself to bf16 is 1.6e-3; together
+// 2.0 to 2.2e-3).  fp16 would hold three bits more, but not the range of the pages' exponents, which
+// bf16 takes along with the codes.  The accumulator of Sᵀ holds, per lane, one row's weights in exactly
+// the token order of the stored V, so P needs no exchange between lanes.
 //
 // The maximum is only raised when a page exceeds it by more than 2^8 (few rows) or its weights add
 // up to more than 2^12 (many rows): bf16 and fp32 hold the larger weights as well, and most pages
@@ -787,13 +789,19 @@ struct Plan {
 // (1.2 us at 64 channels, 2 at 128).  Both kernels run in rounds of 512 blocks, two a CU.
 //   tile: rounds · (pages a block + 4 for its ends), up to 16 splits
 //   few:  rounds · (a quarter of the pages + 5), but no less than its reads take: a page for each 32
-//         rows at 4.9 TB/s from memory, or 9 from the XCD's cache where a key head has several blocks
+//         rows from memory, or a little over half of that from the XCD's cache where a key head has
+//         several blocks
 // and with splits a join: its launch and the blocks' longer ends (4 and 8), and the fp32 rows written
-// and read at 5 TB/s.  Up to 32 rows there is no choice; above, few has no empty waves but reads each
-// page more often (40 rows x 16 sequences x 8192 tokens x 8 heads of 64: 34 us against 58; 128 rows
-// x 64 sequences x 2000 tokens: 59 against 45).  768 blocks of few instead of 512 took 47 us instead
-// of 39 for 32 rows x 2 sequences x 30000 x 8 heads of 128; one split, two nearly full rounds of a third
-// instead of five eighths of one, took tile from 748 to 598 us for 1008 rows x 31688 x 40 heads.
+// and read.  The constants are fitted, the same for both head sizes: as rates those of the reads are
+// 4.9 and 9 TB/s at 64 channels and a fifth more at 128, those of the rows 5 and 3 TB/s.  For 33 to 512
+// rows (75 shapes of 1 to 64 sequences, 4 to 40 heads, 2000 to 30000 tokens at each head size, every
+// split of both kernels timed) the choice takes 1.05 of the best one's time at 64 channels and 1.04 at
+// 128 on average, 1.16 and 1.14 at the ninth tenth, 1.33 and 1.26 at most.  Up to 32 rows there is no
+// choice; above, few has no empty waves but reads each page more often (40 rows x 16 sequences x 8192
+// tokens x 8 heads of 64: 34 us against 46; 128 rows x 64 sequences x 2000 tokens x 4 heads of 128: 54
+// against 43, taken all the same).  768 blocks of few instead of 512 took 47 us instead of 39 for 32
+// rows x 2 sequences x 30000 x 8 heads of 128; one split, two nearly full rounds of a third instead of
+// five eighths of one, took tile from 748 to 598 us for 1008 rows x 31688 x 40 heads.
 Plan plan(int64_t G, int64_t Hkv, int64_t dim, int64_t rows, int64_t B, int64_t max_q,
           int64_t max_kv) {
   constexpr int64_t kSlots = 512;
