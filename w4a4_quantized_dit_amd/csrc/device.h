@@ -50,9 +50,10 @@ __device__ __forceinline__ void store16(void* p, u32x4_t v) {
     *reinterpret_cast<u32x4_t*>(p) = v;
 }
 // Outputs larger than the cache in front of HBM (256 MB) that this call does not read again are
-// stored past the caches: 649 MB of rotated heads 239 -> 224 us, 336 MB of keys and values read
-// back 91 -> 56 us; smaller ones are kept for their reader (34 MB read back: 13 us, past the
-// caches 15).
+// stored past the caches: 649 MB of rotated heads 240 -> 225 us, 336 MB of keys and values read back
+// 100 -> 77 us (the least of calls one after the other, whose 168 MB of codes stay cached; right
+// behind 1 GB of other stores 112 -> 132); smaller ones are kept for their reader (34 MB read back:
+// 13 us, past the caches 15).
 constexpr int64_t kPastCaches = (int64_t)256 << 20;
 
 // s_waitcnt vmcnt(n) (other counters untouched), gfx9 encoding

@@ -10,7 +10,7 @@
 // whose V codes make whole dwords of the stored order (its token is the lowest index) and whose K
 // codes make half pieces.  A whole page is gathered in an LDS image and written out in contiguous
 // pieces; with units of one token and sixteen channels V went there byte by byte, all lanes on a
-// few banks (1008 + 643 tokens x 40 heads of 128: 17.9 us, now 15.2).  On a page that is
+// few banks (1008 + 719 tokens x 40 heads of 128: 17.9 us, now 15.2).  On a page that is
 // only partly new the units go straight to memory, and the page is read only where codes change.
 #include "device.h"
 #include "kv_layout.h"

@@ -416,7 +416,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_norm_down_few(NormArgs a, Do
   }
 }
 
-// Which of the three (K = 5120, whole call in us; few, many with 64 rows, many with 128):
+// Which of the three (K = 5120, no residual, whole call in us; few, many with 64 rows, many with 128):
 //   rank 128  M 1024: 34, 57, 73   2048: 61, 62, 78   8192: 234, 88, 103   16384: -, 131, 143
 //                  20480: -, 197, 165   31688: -, 252, 231
 //   rank 32   M 4096: 49, 50, 74   8192: 93, 68, 91   16384: 180, 112, 131   20480: -, 156, 154
