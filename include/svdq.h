@@ -512,6 +512,25 @@ svdq_status svdq_rope_frequencies(int64_t n_axes, const int64_t* axis_dims, doub
                                   double* freq);
 
 /*
+ * Root-mean-square norm of every query and key head with the rotary positions of svdq_rope_axes in the
+ * same pass.  For each head x of dim channels:
+ *
+ *   z = x·gamma / sqrt(mean x² + eps)        gamma_q for the first q_heads heads, gamma_k for the next
+ *                                            k_heads (NULL: 1)
+ *   y = z with its first sum(axis_dims) channels turned, as at svdq_rope_axes (no inverse)
+ * rounded to bf16 once.  fp32 throughout, θ and its reduction in fp64; mean x² is formed in fp64 where
+ * its sum passes 1e37, and an infinity or NaN goes through the formula.  X, Y [M, (q_heads + k_heads)·dim]
+ * bf16 with leading dimensions ldx, ldy; Y may be X itself, but must not overlap it otherwise.
+ * gamma_q, gamma_k: bf16 [dim]; eps in [1e-30, 1e30).  q_heads or k_heads may be 0.  pos, freq, dim,
+ * axis_dims, interleaved and M as at svdq_rope_axes.
+ */
+svdq_status svdq_qk_norm_rope(const uint16_t* X, int64_t M, int64_t ldx, int64_t q_heads,
+                              int64_t k_heads, int64_t dim, const uint16_t* gamma_q,
+                              const uint16_t* gamma_k, float eps, const int32_t* pos,
+                              const double* freq, int64_t n_axes, const int64_t* axis_dims,
+                              int interleaved, uint16_t* Y, int64_t ldy, svdq_stream_t stream);
+
+/*
  * Paged 8-bit key / value cache.  A page holds SVDQ_KV_PAGE tokens of every head: for each head
  * 64·dim E4M3 codes of K, as many of V and one exponent byte of each (value = code·2^(byte−127)).
  *   k_codes, v_codes: device uint8 [n_pages, heads, 64·dim]
@@ -590,6 +609,79 @@ svdq_status svdq_attn_kv8(const uint16_t* Q, int64_t ldq, int64_t rows, int64_t 
                           const uint8_t* v_scales, float scale, int causal, uint16_t* O,
                           int64_t ldo, float* lse, void* workspace, int64_t workspace_bytes,
                           svdq_stream_t stream);
+
+/*
+ * Paged 4-bit key / value cache: as the 8-bit one (pages, block_table, cu_rows, start, max_rows, the
+ * tokens that are skipped), with 32 channels of a token and head as one MXFP4 block:
+ *   k_codes, v_codes: device uint8 [n_pages, heads, 32·dim]; a byte has the E2M1 codes of channels
+ *     (d, d + 1), d even in the low nibble
+ *   k_scales, v_scales: device uint8 [n_pages, heads, 2·dim], value = code·2^(byte − 127)
+ * 16-byte aligned each, in the attention kernel's operand order:
+ *   K (token t, channel d): code byte ((t/32·(dim/64) + d/64)·64 + d/32%2·32 + t%32)·16 + d%32/2
+ *                           scale byte (d/32%2·32 + t%32)·(dim/32) + t/32·(dim/64) + d/64
+ *   V (token t, channel d): code byte ((d/64·2 + t/32)·64 + t/4%2·32 + d/2%32)·16
+ *                                     + t/16%2·8 + t/8%2·4 + t%4
+ *                           scale byte (d/32·2 + t/4%2)·32 + t/16·8 + t/8%2·4 + t%4
+ *
+ * svdq_kv4_write: per block a = max|x|; e = floor(log2 a) − 2 within [−110, 85] (−110 for a == 0);
+ * code = E2M1(x·2^−e), nearest even, saturating, the sign kept; scale byte = e + 127.  A block with an
+ * infinity or NaN gets scale byte 255 and codes 0 and stands for 32 NaN.  Every token is quantised by
+ * itself and only its own bytes are written, so a page may be written in several parts, in any order and
+ * by several sequences of a call, as long as no token is written twice in one.  Bit-exact.
+ *
+ * svdq_kv4_read writes the values of tokens start[b] .. of each sequence to K and V (bf16, exact).
+ * Rows of skipped tokens are left as they were.
+ */
+svdq_status svdq_kv4_write(const uint16_t* K, int64_t ldk, const uint16_t* V, int64_t ldv,
+                           int64_t rows, int64_t heads, int64_t dim, const int32_t* cu_rows,
+                           const int32_t* start, int64_t B, int64_t max_rows,
+                           const int32_t* block_table, int64_t max_blocks, int64_t n_pages,
+                           uint8_t* k_codes, uint8_t* v_codes, uint8_t* k_scales,
+                           uint8_t* v_scales, svdq_stream_t stream);
+svdq_status svdq_kv4_read(uint16_t* K, int64_t ldk, uint16_t* V, int64_t ldv, int64_t rows,
+                          int64_t heads, int64_t dim, const int32_t* cu_rows,
+                          const int32_t* start, int64_t B, int64_t max_rows,
+                          const int32_t* block_table, int64_t max_blocks, int64_t n_pages,
+                          const uint8_t* k_codes, const uint8_t* v_codes, const uint8_t* k_scales,
+                          const uint8_t* v_scales, svdq_stream_t stream);
+
+/*
+ * Softmax attention over the paged 4-bit cache: arguments, masks and results as at svdq_attn_kv8.  A
+ * key block that is NaN (scale byte 255) makes the rows that see its token NaN, a value block its 32
+ * channels of them; a token that a row does not see has no part in its result.  O is finite for every
+ * cache that svdq_kv4_write makes and finite queries with scores up to 2^27.
+ */
+int64_t svdq_attn_kv4_workspace_bytes(int64_t rows, int64_t q_heads, int64_t kv_heads,
+                                      int64_t dim, int64_t B, int64_t max_rows, int64_t max_kv);
+svdq_status svdq_attn_kv4(const uint16_t* Q, int64_t ldq, int64_t rows, int64_t q_heads,
+                          int64_t kv_heads, int64_t dim, const int32_t* cu_rows,
+                          const int32_t* kv_len, int64_t B, int64_t max_rows, int64_t max_kv,
+                          const int32_t* block_table, int64_t max_blocks, int64_t n_pages,
+                          const uint8_t* k_codes, const uint8_t* v_codes, const uint8_t* k_scales,
+                          const uint8_t* v_scales, float scale, int causal, uint16_t* O,
+                          int64_t ldo, float* lse, void* workspace, int64_t workspace_bytes,
+                          svdq_stream_t stream);
+
+/*
+ * The layer for a few rows with 16-bit activations: the prepared 4-bit weight times X̂ itself, without
+ * activation quantisation, for single tokens, where the weight's bytes are the work.
+ *
+ *   x̂ = bf16(x·fl32(1/λ))  (lambda NULL: x̂ = x),   D = x̂·lora_downᵀ (fp32)
+ *   Y[m, n] = bf16( Σ_k x̂[m, k]·w[n, k] + Σ_j D[m, j]·lora_up[n, j] )
+ * w: what w_codes, w_scales (and g_w, NVFP4) stand for, from svdq_quantize_weight: NVFP4, INT4_G64 or
+ * MXFP4.  X [M, K] bf16, leading dimension ldx (a multiple of 8), M in [1, 64]; K a multiple of 256, at
+ * most 2^24; N >= 1; lora_down [r, K], lora_up [N, r] bf16, r as at svdq_quantize_weight; Y [M, N] bf16,
+ * leading dimension ldy >= N, not overlapping X.  X, lambda, the weight and the factors 16-byte aligned.
+ * fp32 sums in a fixed order, no atomics: results repeat bit for bit.  workspace: at least
+ * svdq_w4a16_gemv_workspace_bytes(M, K, r, lambda != NULL) bytes (0 without lambda and rank; −1:
+ * unsupported), 256-byte aligned, the caller's, not shared with a call that may run at the same time.
+ */
+int64_t svdq_w4a16_gemv_workspace_bytes(int64_t M, int64_t K, int64_t r, int smooth);
+svdq_status svdq_w4a16_gemv(int fmt, const uint16_t* X, int64_t M, int64_t K, int64_t ldx,
+                            const float* lambda, const uint16_t* lora_down, int64_t r,
+                            const uint8_t* w_codes, const void* w_scales, const float* g_w,
+                            const uint16_t* lora_up, int64_t N, uint16_t* Y, int64_t ldy,
+                            void* workspace, int64_t workspace_bytes, svdq_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -149,10 +149,11 @@ def kv_values(cache, table_row, n, head, is_v):
     return out, ok
 
 
-def attention(Q, cache, table, cu, kv_len, scale, causal):
+def attention(Q, cache, table, cu, kv_len, scale, causal, values=kv_values):
     """Q float [rows, q_heads, dim]: dict(O, lse float64, absO = Σ p|v|, absz = scale·max_t
     Σ_d |q_d k_td| of every row, the magnitudes that rounding errors are relative to).  What a row
-    does not see has no part in it, NaN included; a query with an infinity or NaN is NaN."""
+    does not see has no part in it, NaN included; a query with an infinity or NaN is NaN.  values:
+    what reads the cache."""
     rows, Hq, dim = Q.shape
     H = cache["ks"].shape[1]
     G = Hq // H
@@ -164,8 +165,8 @@ def attention(Q, cache, table, cu, kv_len, scale, causal):
             continue
         see = np.arange(kv)[None, :] < ((kv - n + np.arange(n) + 1)[:, None] if causal else kv)
         for h in range(H):
-            k, ok = kv_values(cache, table[b], kv, h, 0)
-            v, _ = kv_values(cache, table[b], kv, h, 1)
+            k, ok = values(cache, table[b], kv, h, 0)
+            v, _ = values(cache, table[b], kv, h, 1)
             vis = see & ok[None, :]
             for g in range(G):
                 j = h * G + g

@@ -1,0 +1,212 @@
+"""GPU parity of svdq_w4a16_gemv against the float64 oracle.  Tolerance, per element, A the sum of the
+magnitudes of its products: half a bf16 step of the result, 2^-8·|y|; the products are exact in fp32
+(x̂ has 8 bits, a weight value 6, 3 before its scale) and every addition loses at most a whole step,
+2^-23, of a partial sum: a wave adds at most 128·ceil(K / 1024) products in a row (and multiplies a
+group of 64 by its scale), 8 waves and the low-rank branch are joined, whose D has 128·ceil(K / 2048)
+products in a row, 16 waves, and r products with the up factor."""
+import numpy as np
+import pytest
+
+from oracle import layer as OL, tokens as OT
+from oracle.formats import bf16_bits_to_f32, bf16_rne
+from tests.gpu_common import dev, dev_bf16, host_bits, torch_mod
+
+pytestmark = pytest.mark.gpu
+FMTS = ["nvfp4", "int4", "mxfp4"]
+
+
+@pytest.fixture(scope="module")
+def L():
+    torch = torch_mod()
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from w4a4_quantized_dit_amd import _lib, layer
+    _lib.load()
+    return layer
+
+
+def case(rng, fmt, N, K, r, smooth=True, spread=1.0):
+    """Oracle weight and its device form."""
+    W = bf16_rne((rng.standard_normal((N, K)) * K ** -0.5 * spread).astype(np.float32))
+    lam = np.exp(0.5 * rng.standard_normal(K)).astype(np.float32) if smooth else None
+    down = bf16_rne((0.05 * rng.standard_normal((r, K))).astype(np.float32)) if r else None
+    up = bf16_rne((0.1 * rng.standard_normal((N, r))).astype(np.float32)) if r else None
+    one = np.ones(K, np.float32)
+    wt = OL.prepare_weight(W, lam if smooth else one, down if r else np.zeros((0, K), np.uint16),
+                           up if r else np.zeros((N, 0), np.uint16), fmt)
+    return wt, lam, down, up
+
+
+def device_weight(L, fmt, wt, up, N, K, r):
+    code = dict(nvfp4=L.NVFP4, int4=L.INT4_G64, mxfp4=L.MXFP4)[fmt]
+    g = dev(np.array([wt["g"]], np.float32)) if fmt == "nvfp4" else None
+    return L.PreparedWeight(code, N, K, r, dev(wt["codes"]), dev(wt["scales"]), g,
+                            dev_bf16(up) if r else None)
+
+
+def tolerance(y, a, K, r):
+    steps = 128 * -(-K // 1024) + 32 + (128 * -(-K // 2048) + 16 + r if r else 0)
+    return 2.0 ** -8 * np.abs(y) + steps * 2.0 ** -23 * a + 1e-37
+
+
+def run(L, fmt, M, N, K, r, smooth=True, pad=0, seed=0, X=None, ypad=0, spread=1.0):
+    torch = torch_mod()
+    rng = np.random.default_rng(seed)
+    wt, lam, down, up = case(rng, fmt, N, K, r, smooth, spread)
+    if X is None:
+        X = bf16_rne((rng.standard_normal((M, K)) * np.exp(0.75 * rng.standard_normal(K))).astype(np.float32))
+    pw = device_weight(L, fmt, wt, up, N, K, r)
+    wide = dev_bf16(np.concatenate([X, np.full((M, pad), 0x7FC0, np.uint16)], 1))
+    out = torch.full((M + 1, N + ypad), 7.0, dtype=torch.bfloat16, device="cuda")
+    Y = L.gemv(wide[:, :K], pw, dev(lam) if smooth else None, dev_bf16(down) if r else None,
+               out=out[:M, :N])
+    torch.cuda.synchronize()
+    y, a = OT.gemv(X, lam, down, up, OT.weight_values(wt["codes"], wt["scales"], wt["g"], fmt))
+    got = Y.float().cpu().numpy().astype(np.float64)
+    bad = np.abs(got - y) > tolerance(y, a, K, r)
+    assert not bad.any(), (int(bad.sum()), np.abs(got - y)[bad].max(), np.argwhere(bad)[:5].tolist())
+    assert torch.all(out[M:] == 7.0) and torch.all(out[:, N:] == 7.0)
+    return got
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M", [1, 2, 15, 16, 17, 32, 33, 48, 49, 64])
+def test_rows(L, fmt, M):
+    run(L, fmt, M, 40, 512, 16, seed=M)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("N", [1, 7, 8, 15, 16, 17, 31, 32, 33, 250])
+@pytest.mark.parametrize("M", [1, 20])
+def test_outputs(L, fmt, N, M):
+    run(L, fmt, M, N, 256, 8, seed=N, ypad=3)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("K", [256, 768, 1024, 1280, 2304, 5120, 13824])
+@pytest.mark.parametrize("r", [0, 32])
+def test_channels(L, fmt, K, r):
+    run(L, fmt, 3, 24, K, r, seed=K)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("r", [0, 8, 24, 64, 120, 128])
+@pytest.mark.parametrize("smooth", [False, True])
+@pytest.mark.parametrize("M", [1, 40])
+def test_ranks(L, fmt, r, smooth, M):
+    run(L, fmt, M, 33, 768, r, smooth=smooth, seed=r)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_strided_rows(L, fmt):
+    run(L, fmt, 5, 40, 512, 16, pad=8)
+    run(L, fmt, 40, 40, 512, 0, smooth=False, pad=264, ypad=1)
+    run(L, fmt, 1, 40, 512, 0, smooth=False, pad=8)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M", [1, 20, 64])
+def test_wide_outputs(L, fmt, M):
+    """Enough outputs that a block takes two tiles, the last one ragged."""
+    run(L, fmt, M, 16384 + 24, 256, 8)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_every_code_and_place(L, fmt):
+    """Unit rows: output n of row k is the weight w[n, k] itself, every channel in turn."""
+    torch = torch_mod()
+    rng = np.random.default_rng(5)
+    N, K = 17, 256
+    wt, _, _, _ = case(rng, fmt, N, K, 0, False)
+    wt["codes"] = rng.integers(0, 256, wt["codes"].shape).astype(np.uint8)
+    pw = device_weight(L, fmt, wt, None, N, K, 0)
+    w = OT.weight_values(wt["codes"], wt["scales"], wt["g"], fmt)
+    for k0 in range(0, K, 64):
+        X = np.zeros((64, K), np.float32)
+        X[np.arange(64), k0 + np.arange(64)] = 1.0
+        Y = L.gemv(dev_bf16(bf16_rne(X)), pw, None, None)
+        torch.cuda.synchronize()
+        got = Y.float().cpu().numpy().T
+        # one product, one rounding (and with a tensor scale one more in fp32)
+        assert np.all(np.abs(got - w[:, k0:k0 + 64]) <= 2.0 ** -8 * (1 + 2.0 ** -15) * np.abs(w[:, k0:k0 + 64]))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_extremes(L, fmt):
+    """Zero weights and rows; rows of very different sizes; infinities and NaN stay in their row."""
+    torch = torch_mod()
+    rng = np.random.default_rng(6)
+    N, K = 24, 512
+    X = (rng.standard_normal((6, K)) * np.array([1e-30, 1.0, 1e30, 0.0, 1.0, 1.0])[:, None])
+    got = run(L, fmt, 6, N, K, 16, X=bf16_rne(X.astype(np.float32)))
+    assert np.all(got[3] == 0)
+    assert np.all(run(L, fmt, 3, N, K, 0, spread=0.0) == 0)
+    wt, lam, down, up = case(rng, fmt, N, K, 16)
+    pw = device_weight(L, fmt, wt, up, N, K, 16)
+    X[4, 100], X[5, 7] = np.inf, np.nan
+    Y = L.gemv(dev_bf16(bf16_rne(X.astype(np.float32))), pw, dev(lam), dev_bf16(down))
+    clean = L.gemv(dev_bf16(bf16_rne(X[:4].astype(np.float32))), pw, dev(lam), dev_bf16(down))
+    torch.cuda.synchronize()
+    assert torch.equal(Y[:4], clean) and not torch.isfinite(Y[4:]).any()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_rows_do_not_depend_on_each_other(L, fmt):
+    """A row's result is the same bits alone and among others: the sums' order is fixed."""
+    torch = torch_mod()
+    rng = np.random.default_rng(7)
+    N, K = 100, 1280
+    wt, lam, down, up = case(rng, fmt, N, K, 32)
+    pw = device_weight(L, fmt, wt, up, N, K, 32)
+    X = dev_bf16(bf16_rne(rng.standard_normal((64, K)).astype(np.float32)))
+    whole = L.gemv(X, pw, dev(lam), dev_bf16(down))
+    for rows in ([0], [63], list(range(3, 20)), list(range(30))):
+        part = L.gemv(X[rows], pw, dev(lam), dev_bf16(down))
+        torch.cuda.synchronize()
+        assert torch.equal(part, whole[rows])
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_prepared_weight_of_the_library(L, fmt):
+    """The weight that prepare_weight makes, beside forward() with its quantised activations, and
+    leading dimensions."""
+    torch = torch_mod()
+    rng = np.random.default_rng(8)
+    M, N, K, r = 12, 256, 512, 16
+    _, lam, down, up = case(rng, fmt, 8, K, r)
+    up = bf16_rne((0.1 * rng.standard_normal((N, r))).astype(np.float32))
+    W = bf16_rne((rng.standard_normal((N, K)) * K ** -0.5).astype(np.float32))
+    code = dict(nvfp4=L.NVFP4, int4=L.INT4_G64, mxfp4=L.MXFP4)[fmt]
+    pw = L.prepare_weight(dev_bf16(W), dev(lam), dev_bf16(down), dev_bf16(up), code)
+    X = dev_bf16(bf16_rne(rng.standard_normal((3, 4, K)).astype(np.float32)))
+    Y = L.gemv(X, pw, dev(lam), dev_bf16(down))
+    full = L.forward(X, pw, None, dev(lam), dev_bf16(down))
+    torch.cuda.synchronize()
+    assert Y.shape == full.shape == (3, 4, N)
+    x = X.float().cpu().numpy().reshape(M, K).astype(np.float64)
+    ref = x @ bf16_bits_to_f32(W).astype(np.float64).T
+    err = lambda t: np.linalg.norm(t.float().cpu().numpy().reshape(M, N) - ref) / np.linalg.norm(ref)  # noqa: E731
+    assert err(Y) < err(full)              # without the activations' error
+    w = OT.weight_values(pw.codes.cpu().numpy(), pw.scales.cpu().numpy(),
+                         pw.g.cpu().numpy()[0] if pw.g is not None else None, fmt)
+    y, a = OT.gemv(host_bits(X).reshape(M, K), lam, down, up, w)
+    assert np.all(np.abs(Y.float().cpu().numpy().reshape(M, N) - y) <= tolerance(y, a, K, r))
+
+
+def test_workspace_of_the_caller(L):
+    torch = torch_mod()
+    from w4a4_quantized_dit_amd import _lib
+    rng = np.random.default_rng(9)
+    wt, lam, down, up = case(rng, "int4", 40, 512, 16)
+    pw = device_weight(L, "int4", wt, up, 40, 512, 16)
+    X = dev_bf16(bf16_rne(rng.standard_normal((20, 512)).astype(np.float32)))
+    want = L.gemv(X, pw, dev(lam), dev_bf16(down))
+    n = _lib.svdq_w4a16_gemv_workspace_bytes(20, 512, 16, True)
+    buf = torch.full((n + 512,), 0xA5, dtype=torch.uint8, device="cuda")
+    off = (-buf.data_ptr()) % 256
+    got = L.gemv(X, pw, dev(lam), dev_bf16(down), workspace=buf[off:off + n])
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    assert torch.all(buf[:off] == 0xA5) and torch.all(buf[off + n:] == 0xA5)
+    assert L.gemv_workspace(20, pw) is not None
+    assert L.gemv_workspace(20, L.PreparedWeight(1, 40, 512, 0, None, None, None, None), False) is None

@@ -85,7 +85,16 @@ _SIGS = {
                                      _i64, _c_p, _i64, _i64, _c_p, _c_p, _c_p, _c_p,
                                      ctypes.c_float, ctypes.c_int, _c_p, _i64, _c_p, _c_p, _i64,
                                      _c_p]),
+    "svdq_qk_norm_rope": (ctypes.c_int, [_c_p, _i64, _i64, _i64, _i64, _i64, _c_p, _c_p,
+                                         ctypes.c_float, _c_p, _c_p, _i64, _c_p, ctypes.c_int, _c_p,
+                                         _i64, _c_p]),
+    "svdq_w4a16_gemv_workspace_bytes": (_i64, [_i64, _i64, _i64, ctypes.c_int]),
+    "svdq_w4a16_gemv": (ctypes.c_int, [ctypes.c_int, _c_p, _i64, _i64, _i64, _c_p, _c_p, _i64, _c_p,
+                                       _c_p, _c_p, _c_p, _i64, _c_p, _i64, _c_p, _i64, _c_p]),
 }
+# the calls on the 4-bit cache take what those on the 8-bit one take
+for _name in ("svdq_kv_write", "svdq_kv_read", "svdq_attn_kv8_workspace_bytes", "svdq_attn_kv8"):
+    _SIGS[_name.replace("kv8", "kv4").replace("kv_", "kv4_")] = _SIGS[_name]
 
 _lib = None
 
@@ -604,11 +613,11 @@ def svdq_rmsnorm_quant_act(X, residual, H, gamma, eps, lam, lora_down, r, codes,
     a.call("svdq_rmsnorm_quant_act", stream, *args)
 
 
-def _gamma(a, t, K, bf):
-    """Pointer of the norm's weight [K] bf16."""
+def _gamma(a, t, K, bf, name="gamma"):
+    """Pointer of a norm's weight [K] bf16."""
     if t is None:
         return None
-    return a.vec(t, K, t.dtype if getattr(t, "dtype", None) in bf else bf[0], "gamma")
+    return a.vec(t, K, t.dtype if getattr(t, "dtype", None) in bf else bf[0], name)
 
 
 def _down(a, t, r, K, bf):
@@ -649,19 +658,21 @@ def svdq_rope_axes(X, heads, dim, pos, freq, axis_dims, interleaved, inverse, Y,
     a.call("svdq_rope_axes", stream, *args)
 
 
-def _cache_args(a, k_codes, v_codes, k_scales, v_scales, dim, block_table, cu_rows, per_seq, what):
-    """Checked pointers and sizes of the cache operands: (pointers of codes and scales), heads,
-    n_pages, B, max_blocks and the pointers of block_table, cu_rows and per_seq."""
+def _cache_args(a, k_codes, v_codes, k_scales, v_scales, dim, block_table, cu_rows, per_seq, what,
+                bits=8):
+    """Checked pointers and sizes of the operands of a cache of `bits` bits: (pointers of codes and
+    scales), heads, n_pages, B, max_blocks and the pointers of block_table, cu_rows and per_seq."""
     torch = _torch()
     u8, i32 = torch.uint8, torch.int32
-    shape = k_codes.shape
-    if len(shape) != 3 or shape[2] != 64 * dim:
-        raise ValueError(f"k_codes has shape {tuple(shape)}, expected [pages, heads, {64 * dim}]")
+    shape, row = k_codes.shape, 8 * bits * dim
+    if len(shape) != 3 or shape[2] != row:
+        raise ValueError(f"k_codes has shape {tuple(shape)}, expected [pages, heads, {row}]")
     n_pages, heads, _ = shape
     if v_codes.shape != shape:
         raise ValueError("v_codes must have the shape of k_codes")
-    if k_scales.shape != shape[:2] or v_scales.shape != shape[:2]:
-        raise ValueError(f"k_scales and v_scales must be [{n_pages}, {heads}]")
+    scales = (n_pages, heads) if bits == 8 else (n_pages, heads, 2 * dim)
+    if k_scales.shape != scales or v_scales.shape != scales:
+        raise ValueError(f"k_scales and v_scales must be {list(scales)}")
     if block_table.dim() != 2:
         raise ValueError("block_table must be [B, max_blocks]")
     B, blocks = block_table.shape
@@ -672,10 +683,10 @@ def _cache_args(a, k_codes, v_codes, k_scales, v_scales, dim, block_table, cu_ro
 
 
 def _kv_call(name, K, V, dim, cu_rows, start, max_rows, block_table, k_codes, v_codes, k_scales,
-             v_scales, stream):
+             v_scales, stream, bits=8):
     a, bf = _Args(), _bf16()
     ptrs, heads, n_pages, B, blocks, table, cu, st = _cache_args(
-        a, k_codes, v_codes, k_scales, v_scales, dim, block_table, cu_rows, start, "start")
+        a, k_codes, v_codes, k_scales, v_scales, dim, block_table, cu_rows, start, "start", bits)
     rows = K.shape[0]
     k, ldk = a.mat(K, rows, heads * dim, bf, "K")
     if V.shape != K.shape:
@@ -710,10 +721,17 @@ def svdq_attn_kv8(Q, dim, cu_rows, kv_len, max_rows, max_kv, block_table, k_code
                   k_scales, v_scales, scale, causal, O, lse=None, workspace=None, stream=None):
     """Attention of Q [rows, q_heads·dim] bf16 over the paged 8-bit cache into O and lse (fp32
     [rows, q_heads] or None); workspace uint8 (svdq_attn_kv8_workspace_bytes) or None."""
+    _attn_call("svdq_attn_kv8", 8, Q, dim, cu_rows, kv_len, max_rows, max_kv, block_table, k_codes,
+               v_codes, k_scales, v_scales, scale, causal, O, lse, workspace, stream)
+
+
+def _attn_call(name, bits, Q, dim, cu_rows, kv_len, max_rows, max_kv, block_table, k_codes, v_codes,
+               k_scales, v_scales, scale, causal, O, lse, workspace, stream):
     torch = _torch()
     a, bf = _Args(), _bf16()
     ptrs, heads, n_pages, B, blocks, table, cu, ln = _cache_args(
-        a, k_codes, v_codes, k_scales, v_scales, dim, block_table, cu_rows, kv_len, "kv_len")
+        a, k_codes, v_codes, k_scales, v_scales, dim, block_table, cu_rows, kv_len, "kv_len",
+        bits)
     if Q.dim() != 2 or Q.shape[1] % dim != 0:
         raise ValueError(f"Q has shape {tuple(Q.shape)}, expected [rows, heads·{dim}]")
     rows, width = Q.shape
@@ -724,6 +742,90 @@ def svdq_attn_kv8(Q, dim, cu_rows, kv_len, max_rows, max_kv, block_table, k_code
     ws = a.vec(workspace, 0, torch.uint8, "workspace")
     if rows == 0:
         return
-    a.call("svdq_attn_kv8", stream, q, ldq, rows, q_heads, heads, int(dim), cu, ln, B,
+    a.call(name, stream, q, ldq, rows, q_heads, heads, int(dim), cu, ln, B,
            int(max_rows), int(max_kv), table, blocks, n_pages, *ptrs, float(scale),
            int(bool(causal)), o, ldo, lse_p, ws, workspace.numel() if ws is not None else 0)
+
+
+def svdq_kv4_write(K, V, dim, cu_rows, start, max_rows, block_table, k_codes, v_codes, k_scales,
+                   v_scales, stream=None):
+    """Append the packed rows K, V [rows, heads·dim] bf16 to the paged 4-bit cache."""
+    _kv_call("svdq_kv4_write", K, V, dim, cu_rows, start, max_rows, block_table, k_codes, v_codes,
+             k_scales, v_scales, stream, 4)
+
+
+def svdq_kv4_read(K, V, dim, cu_rows, start, max_rows, block_table, k_codes, v_codes, k_scales,
+                  v_scales, stream=None):
+    """Read tokens of the paged 4-bit cache back into K, V [rows, heads·dim] bf16."""
+    _kv_call("svdq_kv4_read", K, V, dim, cu_rows, start, max_rows, block_table, k_codes, v_codes,
+             k_scales, v_scales, stream, 4)
+
+
+def svdq_attn_kv4_workspace_bytes(rows, q_heads, kv_heads, dim, B, max_rows, max_kv):
+    return int(load().svdq_attn_kv4_workspace_bytes(int(rows), int(q_heads), int(kv_heads),
+                                                    int(dim), int(B), int(max_rows), int(max_kv)))
+
+
+def svdq_attn_kv4(Q, dim, cu_rows, kv_len, max_rows, max_kv, block_table, k_codes, v_codes,
+                  k_scales, v_scales, scale, causal, O, lse=None, workspace=None, stream=None):
+    """Attention of Q [rows, q_heads·dim] bf16 over the paged 4-bit cache into O and lse (fp32
+    [rows, q_heads] or None); workspace uint8 (svdq_attn_kv4_workspace_bytes) or None."""
+    _attn_call("svdq_attn_kv4", 4, Q, dim, cu_rows, kv_len, max_rows, max_kv, block_table, k_codes,
+               v_codes, k_scales, v_scales, scale, causal, O, lse, workspace, stream)
+
+
+# ------------------------------------------------------------------------------------------
+# query and key heads, and the layer for a few rows
+# ------------------------------------------------------------------------------------------
+
+def svdq_qk_norm_rope(X, q_heads, k_heads, dim, gamma_q, gamma_k, eps, pos, freq, axis_dims,
+                      interleaved, Y, stream=None):
+    """RMS norm and rotary positions of the query and key heads of each row of X [M, (q_heads +
+    k_heads)·dim] bf16 into Y (X itself: in place); gamma bf16 [dim] or None, pos int32 [M, n_axes],
+    freq fp64 [sum(axis_dims)/2]."""
+    torch = _torch()
+    M, n, bf = X.shape[0], len(axis_dims), _bf16()
+    width = (q_heads + k_heads) * dim
+    arr = (ctypes.c_int64 * max(1, n))(*axis_dims)
+    a = _Args()
+    x, ldx = a.mat(X, M, width, bf, "X")
+    y, ldy = a.mat(Y, M, width, bf, "Y")
+    p, ldp = a.mat(pos, M, n, (torch.int32,), "pos")
+    if ldp != n and M > 1:
+        raise ValueError("pos must be contiguous")
+    args = (x, M, ldx, int(q_heads), int(k_heads), int(dim), _gamma(a, gamma_q, dim, bf, "gamma_q"),
+            _gamma(a, gamma_k, dim, bf, "gamma_k"), float(eps), p,
+            a.vec(freq, sum(axis_dims) // 2, torch.float64, "freq"), n, arr, int(bool(interleaved)),
+            y, ldy)
+    a.call("svdq_qk_norm_rope", stream, *args)
+
+
+def svdq_w4a16_gemv_workspace_bytes(M, K, r, smooth):
+    return int(load().svdq_w4a16_gemv_workspace_bytes(int(M), int(K), int(r), int(bool(smooth))))
+
+
+def svdq_w4a16_gemv(fmt, X, lam, lora_down, r, w_codes, w_scales, g_w, lora_up, N, Y, workspace=None,
+                    stream=None):
+    """The layer of a few rows X [M, K] bf16 with 16-bit activations into Y [M, N] bf16; the weight as
+    from svdq_quantize_weight, lam fp32 [K] or None, lora_down [r, K], lora_up [N, r] bf16, workspace
+    uint8 (svdq_w4a16_gemv_workspace_bytes) or None."""
+    torch = _torch()
+    if X.dim() != 2:
+        raise ValueError("X must be a 2-D matrix with contiguous rows")
+    M, K = X.shape
+    bf, f32, u8 = _bf16(), torch.float32, torch.uint8
+    group, kind = {NVFP4: (16, u8), INT4_G64: (64, torch.float16), MXFP4: (32, u8)}.get(
+        fmt, (32, u8))
+    a = _Args()
+    x, ldx = a.mat(X, M, K, bf, "X")
+    y, ldy = a.mat(Y, M, N, bf, "Y")
+    up = None
+    if r:
+        up, ldu = a.mat(lora_up, N, r, bf, "lora_up")
+        if up is not None and ldu != r and N > 1:
+            raise ValueError("lora_up must be contiguous")
+    args = (int(fmt), x, M, K, ldx, a.vec(lam, K, f32, "lambda"), _down(a, lora_down, r, K, bf), int(r),
+            a.vec(w_codes, N * K // 2, u8, "w_codes"), a.vec(w_scales, N * K // group, kind, "w_scales"),
+            a.vec(g_w, 1, f32, "g_w") if fmt == NVFP4 else None, up, int(N), y, ldy,
+            a.vec(workspace, 0, u8, "workspace"), workspace.numel() if workspace is not None else 0)
+    a.call("svdq_w4a16_gemv", stream, *args)

@@ -119,6 +119,26 @@ svdq_status check_axes(const char* fn, int64_t n_axes, const int64_t* axis_dims)
   return SVDQ_OK;
 }
 
+// Head dimension and axes of a rotation; pairs of each axis.
+svdq_status check_rotary(const char* fn, int64_t dim, int64_t n_axes, const int64_t* axis_dims,
+                         int (&pairs)[4]) {
+  if (dim < 16 || dim > 256 || dim % 16 != 0)
+    return fail(SVDQ_UNSUPPORTED_SHAPE, "%s: dim=%lld must be a multiple of 16 in [16, 256]", fn,
+                (long long)dim);
+  svdq_status s = check_axes(fn, n_axes, axis_dims);
+  if (s != SVDQ_OK) return s;
+  int64_t rot = 0;
+  for (int64_t i = 0; i < 4; ++i) {
+    pairs[i] = i < n_axes ? (int)(axis_dims[i] / 2) : 0;
+    rot += 2 * pairs[i];
+  }
+  if (rot < 16 || rot > dim || rot % 16 != 0)
+    return fail(SVDQ_UNSUPPORTED_SHAPE,
+                "%s: the axes' dimensions add up to %lld, not a multiple of 16 in [16, dim=%lld]",
+                fn, (long long)rot, (long long)dim);
+  return SVDQ_OK;
+}
+
 // The arguments every call on the paged cache shares.
 svdq_status check_cache(const char* fn, int64_t heads, int64_t dim, const int32_t* cu_rows,
                         int64_t B, int64_t rows, int64_t max_rows, const int32_t* block_table,
@@ -147,6 +167,75 @@ svdq_status check_cache(const char* fn, int64_t heads, int64_t dim, const int32_
     svdq_status _s = (x);           \
     if (_s != SVDQ_OK) return _s;   \
   } while (0)
+
+// svdq_kv_write and its relatives: rows is K's and V's element (const for a write), bytes the cache's.
+template <class Row, class Byte, class Launch>
+svdq_status kv_call(const char* fn, Launch launch, bool wide_scales, Row* K, int64_t ldk, Row* V,
+                    int64_t ldv, int64_t rows, int64_t heads, int64_t dim, const int32_t* cu_rows,
+                    const int32_t* start, int64_t B, int64_t max_rows, const int32_t* block_table,
+                    int64_t max_blocks, int64_t n_pages, Byte* k_codes, Byte* v_codes,
+                    Byte* k_scales, Byte* v_scales, svdq_stream_t stream) {
+  REQUIRE_PTR(K); REQUIRE_PTR(V); REQUIRE_PTR(start);
+  REQUIRE_ALIGNED(K); REQUIRE_ALIGNED(V);
+  TRY(check_cache(fn, heads, dim, cu_rows, B, rows, max_rows, block_table, max_blocks, n_pages,
+                  k_codes, v_codes, k_scales, v_scales));
+  if (wide_scales) { REQUIRE_ALIGNED(k_scales); REQUIRE_ALIGNED(v_scales); }
+  TRY(check_ld(fn, "ldk", ldk, heads * dim));
+  TRY(check_ld(fn, "ldv", ldv, heads * dim));
+  if (rows == 0 || max_rows == 0) return ok();
+  return hip_result(launch(K, ldk, V, ldv, rows, (int)heads, (int)dim, cu_rows, start, B, max_rows,
+                           block_table, max_blocks, n_pages, k_codes, v_codes, k_scales, v_scales,
+                           reinterpret_cast<hipStream_t>(stream)),
+                    fn);
+}
+
+// Attention over a paged cache.
+template <class Launch>
+svdq_status attn_call(const char* fn, Launch launch, bool wide_scales, const uint16_t* Q, int64_t ldq,
+                      int64_t rows, int64_t q_heads, int64_t kv_heads, int64_t dim,
+                      const int32_t* cu_rows, const int32_t* kv_len, int64_t B, int64_t max_rows,
+                      int64_t max_kv, const int32_t* block_table, int64_t max_blocks,
+                      int64_t n_pages, const uint8_t* k_codes, const uint8_t* v_codes,
+                      const uint8_t* k_scales, const uint8_t* v_scales, float scale, int causal,
+                      uint16_t* O, int64_t ldo, float* lse, void* workspace,
+                      int64_t workspace_bytes, svdq_stream_t stream) {
+  REQUIRE_PTR(Q); REQUIRE_PTR(O); REQUIRE_PTR(kv_len);
+  REQUIRE_ALIGNED(Q); REQUIRE_ALIGNED(O); REQUIRE_ALIGNED(lse);
+  TRY(check_cache(fn, kv_heads, dim, cu_rows, B, rows, max_rows, block_table, max_blocks, n_pages,
+                  k_codes, v_codes, k_scales, v_scales));
+  if (wide_scales) { REQUIRE_ALIGNED(k_scales); REQUIRE_ALIGNED(v_scales); }
+  if (q_heads < kv_heads || q_heads % kv_heads != 0 || q_heads > 65535)
+    return fail(SVDQ_UNSUPPORTED_SHAPE,
+                "%s: q_heads=%lld must be a multiple of kv_heads=%lld, at most 65535", fn,
+                (long long)q_heads, (long long)kv_heads);
+  TRY(check_ld(fn, "ldq", ldq, q_heads * dim));
+  TRY(check_ld(fn, "ldo", ldo, q_heads * dim));
+  if (max_kv < 0 || max_kv > INT32_MAX)
+    return fail(SVDQ_INVALID_ARG, "%s: max_kv=%lld must lie in [0, 2^31)", fn, (long long)max_kv);
+  if (!(scale > 0.0f && scale < 1e30f))
+    return fail(SVDQ_INVALID_ARG, "%s: scale must be positive and finite", fn);
+  if (Q == O) return fail(SVDQ_INVALID_ARG, "%s: O must not be Q", fn);
+  if (max_rows * q_heads > (1 << 28) || rows * (q_heads / kv_heads) > (1 << 30))
+    return fail(SVDQ_UNSUPPORTED_SHAPE, "%s: more than 2^28 rows and heads in a sequence", fn);
+  if (rows == 0 || max_rows == 0) return ok();
+  const int64_t need =
+      svdq::attn_workspace_bytes(rows, q_heads, kv_heads, dim, B, max_rows, max_kv);
+  if (need > 0) {
+    REQUIRE_PTR(workspace);
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+      return fail(SVDQ_UNSUPPORTED_SHAPE, "%s: workspace must be 256-byte aligned", fn);
+    if (workspace_bytes < need)
+      return fail(SVDQ_UNSUPPORTED_SHAPE, "%s: workspace of %lld bytes, needs %lld", fn,
+                  (long long)workspace_bytes, (long long)need);
+  }
+  if (svdq::attn_blocks(rows, q_heads, kv_heads, dim, B, max_rows, max_kv) >= (1 << 24))
+    return fail(SVDQ_UNSUPPORTED_SHAPE, "%s: more than 2^24 blocks of rows and heads", fn);
+  return hip_result(launch(Q, ldq, rows, q_heads, kv_heads, dim, cu_rows, kv_len, B,
+                                      max_rows, max_kv, block_table, max_blocks, n_pages, k_codes,
+                                      v_codes, k_scales, v_scales, scale, causal != 0, O, ldo, lse,
+                                      workspace, reinterpret_cast<hipStream_t>(stream)),
+                    fn);
+}
 
 }  // namespace
 
@@ -785,23 +874,11 @@ svdq_status svdq_rope_axes(const uint16_t* X, int64_t M, int64_t ldx, int64_t he
   const char* fn = "svdq_rope_axes";
   REQUIRE_PTR(X); REQUIRE_PTR(pos); REQUIRE_PTR(freq); REQUIRE_PTR(axis_dims); REQUIRE_PTR(Y);
   REQUIRE_ALIGNED(X); REQUIRE_ALIGNED(Y); REQUIRE_ALIGNED(freq);
-  if (dim < 16 || dim > 256 || dim % 16 != 0)
-    return fail(SVDQ_UNSUPPORTED_SHAPE, "%s: dim=%lld must be a multiple of 16 in [16, 256]", fn,
-                (long long)dim);
   if (heads < 1 || heads > (1 << 20))
     return fail(SVDQ_UNSUPPORTED_SHAPE, "%s: heads=%lld must lie in [1, 2^20]", fn,
                 (long long)heads);
-  TRY(check_axes(fn, n_axes, axis_dims));
-  int64_t rot = 0;
-  int pairs[4] = {0, 0, 0, 0};
-  for (int64_t i = 0; i < n_axes; ++i) {
-    rot += axis_dims[i];
-    pairs[i] = (int)(axis_dims[i] / 2);
-  }
-  if (rot < 16 || rot > dim || rot % 16 != 0)
-    return fail(SVDQ_UNSUPPORTED_SHAPE,
-                "%s: the axes' dimensions add up to %lld, not a multiple of 16 in [16, dim=%lld]",
-                fn, (long long)rot, (long long)dim);
+  int pairs[4];
+  TRY(check_rotary(fn, dim, n_axes, axis_dims, pairs));
   TRY(check_rows(fn, "M", M, 1));
   TRY(check_ld(fn, "ldx", ldx, heads * dim));
   TRY(check_ld(fn, "ldy", ldy, heads * dim));
@@ -810,6 +887,36 @@ svdq_status svdq_rope_axes(const uint16_t* X, int64_t M, int64_t ldx, int64_t he
   return hip_result(svdq::launch_rope(X, M, ldx, (int)heads, (int)dim, pos, freq, (int)n_axes,
                                       pairs, interleaved != 0, inverse != 0, Y, ldy,
                                       reinterpret_cast<hipStream_t>(stream)),
+                    fn);
+}
+
+svdq_status svdq_qk_norm_rope(const uint16_t* X, int64_t M, int64_t ldx, int64_t q_heads,
+                              int64_t k_heads, int64_t dim, const uint16_t* gamma_q,
+                              const uint16_t* gamma_k, float eps, const int32_t* pos,
+                              const double* freq, int64_t n_axes, const int64_t* axis_dims,
+                              int interleaved, uint16_t* Y, int64_t ldy, svdq_stream_t stream) {
+  const char* fn = "svdq_qk_norm_rope";
+  REQUIRE_PTR(X); REQUIRE_PTR(pos); REQUIRE_PTR(freq); REQUIRE_PTR(axis_dims); REQUIRE_PTR(Y);
+  REQUIRE_ALIGNED(X); REQUIRE_ALIGNED(Y); REQUIRE_ALIGNED(freq);
+  REQUIRE_ALIGNED(gamma_q); REQUIRE_ALIGNED(gamma_k);
+  if (q_heads < 0 || k_heads < 0 || q_heads > (1 << 20) || k_heads > (1 << 20) ||
+      q_heads + k_heads < 1)
+    return fail(SVDQ_UNSUPPORTED_SHAPE,
+                "%s: q_heads=%lld and k_heads=%lld must lie in [0, 2^20], one of them positive", fn,
+                (long long)q_heads, (long long)k_heads);
+  int pairs[4];
+  TRY(check_rotary(fn, dim, n_axes, axis_dims, pairs));
+  TRY(check_rows(fn, "M", M, 1));
+  TRY(check_ld(fn, "ldx", ldx, (q_heads + k_heads) * dim));
+  TRY(check_ld(fn, "ldy", ldy, (q_heads + k_heads) * dim));
+  if (X == Y && ldx != ldy)
+    return fail(SVDQ_INVALID_ARG, "%s: in place needs ldy == ldx", fn);
+  if (!(eps >= 1e-30f && eps < 1e30f))
+    return fail(SVDQ_INVALID_ARG, "%s: eps must lie in [1e-30, 1e30)", fn);
+  return hip_result(svdq::launch_qk_norm_rope(X, M, ldx, (int)q_heads, (int)k_heads, (int)dim,
+                                              gamma_q, gamma_k, eps, pos, freq, (int)n_axes, pairs,
+                                              interleaved != 0, Y, ldy,
+                                              reinterpret_cast<hipStream_t>(stream)),
                     fn);
 }
 
@@ -832,19 +939,9 @@ svdq_status svdq_kv_write(const uint16_t* K, int64_t ldk, const uint16_t* V, int
                           const int32_t* block_table, int64_t max_blocks, int64_t n_pages,
                           uint8_t* k_codes, uint8_t* v_codes, uint8_t* k_scales,
                           uint8_t* v_scales, svdq_stream_t stream) {
-  const char* fn = "svdq_kv_write";
-  REQUIRE_PTR(K); REQUIRE_PTR(V); REQUIRE_PTR(start);
-  REQUIRE_ALIGNED(K); REQUIRE_ALIGNED(V);
-  TRY(check_cache(fn, heads, dim, cu_rows, B, rows, max_rows, block_table, max_blocks, n_pages,
-                  k_codes, v_codes, k_scales, v_scales));
-  TRY(check_ld(fn, "ldk", ldk, heads * dim));
-  TRY(check_ld(fn, "ldv", ldv, heads * dim));
-  if (rows == 0 || max_rows == 0) return ok();
-  return hip_result(svdq::launch_kv_write(K, ldk, V, ldv, rows, (int)heads, (int)dim, cu_rows,
-                                          start, B, max_rows, block_table, max_blocks, n_pages,
-                                          k_codes, v_codes, k_scales, v_scales,
-                                          reinterpret_cast<hipStream_t>(stream)),
-                    fn);
+  return kv_call("svdq_kv_write", svdq::launch_kv_write, false, K, ldk, V, ldv, rows, heads, dim,
+                 cu_rows, start, B, max_rows, block_table, max_blocks, n_pages, k_codes, v_codes,
+                 k_scales, v_scales, stream);
 }
 
 svdq_status svdq_kv_read(uint16_t* K, int64_t ldk, uint16_t* V, int64_t ldv, int64_t rows,
@@ -853,19 +950,31 @@ svdq_status svdq_kv_read(uint16_t* K, int64_t ldk, uint16_t* V, int64_t ldv, int
                          int64_t max_blocks, int64_t n_pages, const uint8_t* k_codes,
                          const uint8_t* v_codes, const uint8_t* k_scales, const uint8_t* v_scales,
                          svdq_stream_t stream) {
-  const char* fn = "svdq_kv_read";
-  REQUIRE_PTR(K); REQUIRE_PTR(V); REQUIRE_PTR(start);
-  REQUIRE_ALIGNED(K); REQUIRE_ALIGNED(V);
-  TRY(check_cache(fn, heads, dim, cu_rows, B, rows, max_rows, block_table, max_blocks, n_pages,
-                  k_codes, v_codes, k_scales, v_scales));
-  TRY(check_ld(fn, "ldk", ldk, heads * dim));
-  TRY(check_ld(fn, "ldv", ldv, heads * dim));
-  if (rows == 0 || max_rows == 0) return ok();
-  return hip_result(svdq::launch_kv_read(K, ldk, V, ldv, rows, (int)heads, (int)dim, cu_rows, start,
-                                         B, max_rows, block_table, max_blocks, n_pages, k_codes,
-                                         v_codes, k_scales, v_scales,
-                                         reinterpret_cast<hipStream_t>(stream)),
-                    fn);
+  return kv_call("svdq_kv_read", svdq::launch_kv_read, false, K, ldk, V, ldv, rows, heads, dim,
+                 cu_rows, start, B, max_rows, block_table, max_blocks, n_pages, k_codes, v_codes,
+                 k_scales, v_scales, stream);
+}
+
+svdq_status svdq_kv4_write(const uint16_t* K, int64_t ldk, const uint16_t* V, int64_t ldv,
+                           int64_t rows, int64_t heads, int64_t dim, const int32_t* cu_rows,
+                           const int32_t* start, int64_t B, int64_t max_rows,
+                           const int32_t* block_table, int64_t max_blocks, int64_t n_pages,
+                           uint8_t* k_codes, uint8_t* v_codes, uint8_t* k_scales,
+                           uint8_t* v_scales, svdq_stream_t stream) {
+  return kv_call("svdq_kv4_write", svdq::launch_kv4_write, true, K, ldk, V, ldv, rows, heads, dim,
+                 cu_rows, start, B, max_rows, block_table, max_blocks, n_pages, k_codes, v_codes,
+                 k_scales, v_scales, stream);
+}
+
+svdq_status svdq_kv4_read(uint16_t* K, int64_t ldk, uint16_t* V, int64_t ldv, int64_t rows,
+                          int64_t heads, int64_t dim, const int32_t* cu_rows,
+                          const int32_t* start, int64_t B, int64_t max_rows,
+                          const int32_t* block_table, int64_t max_blocks, int64_t n_pages,
+                          const uint8_t* k_codes, const uint8_t* v_codes, const uint8_t* k_scales,
+                          const uint8_t* v_scales, svdq_stream_t stream) {
+  return kv_call("svdq_kv4_read", svdq::launch_kv4_read, true, K, ldk, V, ldv, rows, heads, dim,
+                 cu_rows, start, B, max_rows, block_table, max_blocks, n_pages, k_codes, v_codes,
+                 k_scales, v_scales, stream);
 }
 
 int64_t svdq_attn_kv8_workspace_bytes(int64_t rows, int64_t q_heads, int64_t kv_heads,
@@ -885,27 +994,68 @@ svdq_status svdq_attn_kv8(const uint16_t* Q, int64_t ldq, int64_t rows, int64_t 
                           const uint8_t* v_scales, float scale, int causal, uint16_t* O,
                           int64_t ldo, float* lse, void* workspace, int64_t workspace_bytes,
                           svdq_stream_t stream) {
-  const char* fn = "svdq_attn_kv8";
-  REQUIRE_PTR(Q); REQUIRE_PTR(O); REQUIRE_PTR(kv_len);
-  REQUIRE_ALIGNED(Q); REQUIRE_ALIGNED(O); REQUIRE_ALIGNED(lse);
-  TRY(check_cache(fn, kv_heads, dim, cu_rows, B, rows, max_rows, block_table, max_blocks, n_pages,
-                  k_codes, v_codes, k_scales, v_scales));
-  if (q_heads < kv_heads || q_heads % kv_heads != 0 || q_heads > 65535)
-    return fail(SVDQ_UNSUPPORTED_SHAPE,
-                "%s: q_heads=%lld must be a multiple of kv_heads=%lld, at most 65535", fn,
-                (long long)q_heads, (long long)kv_heads);
-  TRY(check_ld(fn, "ldq", ldq, q_heads * dim));
-  TRY(check_ld(fn, "ldo", ldo, q_heads * dim));
-  if (max_kv < 0 || max_kv > INT32_MAX)
-    return fail(SVDQ_INVALID_ARG, "%s: max_kv=%lld must lie in [0, 2^31)", fn, (long long)max_kv);
-  if (!(scale > 0.0f && scale < 1e30f))
-    return fail(SVDQ_INVALID_ARG, "%s: scale must be positive and finite", fn);
-  if (Q == O) return fail(SVDQ_INVALID_ARG, "%s: O must not be Q", fn);
-  if (max_rows * q_heads > (1 << 28) || rows * (q_heads / kv_heads) > (1 << 30))
-    return fail(SVDQ_UNSUPPORTED_SHAPE, "%s: more than 2^28 rows and heads in a sequence", fn);
-  if (rows == 0 || max_rows == 0) return ok();
-  const int64_t need =
-      svdq::attn_workspace_bytes(rows, q_heads, kv_heads, dim, B, max_rows, max_kv);
+  return attn_call("svdq_attn_kv8", svdq::launch_attn, false, Q, ldq, rows, q_heads, kv_heads, dim, cu_rows,
+                   kv_len, B, max_rows, max_kv, block_table, max_blocks, n_pages, k_codes, v_codes,
+                   k_scales, v_scales, scale, causal, O, ldo, lse, workspace, workspace_bytes,
+                   stream);
+}
+
+int64_t svdq_attn_kv4_workspace_bytes(int64_t rows, int64_t q_heads, int64_t kv_heads,
+                                      int64_t dim, int64_t B, int64_t max_rows, int64_t max_kv) {
+  return svdq_attn_kv8_workspace_bytes(rows, q_heads, kv_heads, dim, B, max_rows, max_kv);
+}
+
+svdq_status svdq_attn_kv4(const uint16_t* Q, int64_t ldq, int64_t rows, int64_t q_heads,
+                          int64_t kv_heads, int64_t dim, const int32_t* cu_rows,
+                          const int32_t* kv_len, int64_t B, int64_t max_rows, int64_t max_kv,
+                          const int32_t* block_table, int64_t max_blocks, int64_t n_pages,
+                          const uint8_t* k_codes, const uint8_t* v_codes, const uint8_t* k_scales,
+                          const uint8_t* v_scales, float scale, int causal, uint16_t* O,
+                          int64_t ldo, float* lse, void* workspace, int64_t workspace_bytes,
+                          svdq_stream_t stream) {
+  return attn_call("svdq_attn_kv4", svdq::launch_attn4, true, Q, ldq, rows, q_heads, kv_heads, dim, cu_rows,
+                   kv_len, B, max_rows, max_kv, block_table, max_blocks, n_pages, k_codes, v_codes,
+                   k_scales, v_scales, scale, causal, O, ldo, lse, workspace, workspace_bytes,
+                   stream);
+}
+
+int64_t svdq_w4a16_gemv_workspace_bytes(int64_t M, int64_t K, int64_t r, int smooth) {
+  if (M < 1 || M > svdq::kGemvMostRows || K < 1 || K % 256 != 0 || K > (1 << 24) || r < 0 ||
+      r > 128 || r % 8 != 0)
+    return -1;
+  return svdq::gemv_workspace_bytes(M, K, r, smooth != 0);
+}
+
+svdq_status svdq_w4a16_gemv(int fmt, const uint16_t* X, int64_t M, int64_t K, int64_t ldx,
+                            const float* lambda, const uint16_t* lora_down, int64_t r,
+                            const uint8_t* w_codes, const void* w_scales, const float* g_w,
+                            const uint16_t* lora_up, int64_t N, uint16_t* Y, int64_t ldy,
+                            void* workspace, int64_t workspace_bytes, svdq_stream_t stream) {
+  const char* fn = "svdq_w4a16_gemv";
+  TRY(check_fmt(fn, fmt));
+  if (fmt == SVDQ_MXFP8)
+    return fail(SVDQ_INVALID_ARG, "%s: the weight must be of a 4-bit format", fn);
+  REQUIRE_PTR(X); REQUIRE_PTR(w_codes); REQUIRE_PTR(w_scales); REQUIRE_PTR(Y);
+  if (fmt == SVDQ_NVFP4) REQUIRE_PTR(g_w);
+  REQUIRE_ALIGNED(X); REQUIRE_ALIGNED(lambda); REQUIRE_ALIGNED(w_codes); REQUIRE_ALIGNED(w_scales);
+  if (M < 1 || M > svdq::kGemvMostRows)
+    return fail(SVDQ_UNSUPPORTED_SHAPE, "%s: M=%lld must lie in [1, %lld]", fn, (long long)M,
+                (long long)svdq::kGemvMostRows);
+  TRY(check_k(fn, K));
+  if (K > (1 << 24))
+    return fail(SVDQ_UNSUPPORTED_SHAPE, "%s: K=%lld exceeds 2^24", fn, (long long)K);
+  if (N < 1 || N > (1 << 28))
+    return fail(SVDQ_UNSUPPORTED_SHAPE, "%s: N=%lld must lie in [1, 2^28]", fn, (long long)N);
+  TRY(check_ld(fn, "ldx", ldx, K));
+  if (ldy < N)
+    return fail(SVDQ_UNSUPPORTED_SHAPE, "%s: ldy=%lld must be >= N=%lld", fn, (long long)ldy,
+                (long long)N);
+  TRY(check_rank(fn, r));
+  if (r > 0) {
+    REQUIRE_PTR(lora_down); REQUIRE_PTR(lora_up);
+    REQUIRE_ALIGNED(lora_down); REQUIRE_ALIGNED(lora_up);
+  }
+  const int64_t need = svdq::gemv_workspace_bytes(M, K, r, lambda != nullptr);
   if (need > 0) {
     REQUIRE_PTR(workspace);
     if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
@@ -914,11 +1064,8 @@ svdq_status svdq_attn_kv8(const uint16_t* Q, int64_t ldq, int64_t rows, int64_t 
       return fail(SVDQ_UNSUPPORTED_SHAPE, "%s: workspace of %lld bytes, needs %lld", fn,
                   (long long)workspace_bytes, (long long)need);
   }
-  if (svdq::attn_blocks(rows, q_heads, kv_heads, dim, B, max_rows, max_kv) >= (1 << 24))
-    return fail(SVDQ_UNSUPPORTED_SHAPE, "%s: more than 2^24 blocks of rows and heads", fn);
-  return hip_result(svdq::launch_attn(Q, ldq, rows, q_heads, kv_heads, dim, cu_rows, kv_len, B,
-                                      max_rows, max_kv, block_table, max_blocks, n_pages, k_codes,
-                                      v_codes, k_scales, v_scales, scale, causal != 0, O, ldo, lse,
+  return hip_result(svdq::launch_gemv(fmt, X, M, K, ldx, lambda, lora_down, r, w_codes, w_scales,
+                                      fmt == SVDQ_NVFP4 ? g_w : nullptr, lora_up, N, Y, ldy,
                                       workspace, reinterpret_cast<hipStream_t>(stream)),
                     fn);
 }

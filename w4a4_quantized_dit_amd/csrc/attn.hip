@@ -23,6 +23,7 @@
 // The maximum is only raised when a page exceeds it by more than 2^8 (few rows) or its weights add
 // up to more than 2^12 (many rows): bf16 and fp32 hold the larger weights as well, and most pages
 // skip the rescaling of O, and with many rows the maximum itself.
+#include "attn_common.h"
 #include "device.h"
 #include "kv_layout.h"
 #include "launch.h"
@@ -31,120 +32,11 @@ namespace svdq {
 
 namespace {
 
-constexpr float kNoMax = -3.0e38f;  // running maximum before the first visible token
-constexpr float kRaise = 8.0f;
-constexpr float kMostSum = 4096.0f;
-
 // V is widened as 2^-16 of itself and O brought back where it is stored, exact steps both: the sum of
 // V over its weights is formed before the division by theirs, and cached values reach 2^128.  Sixteen
 // bits are what the smallest page exponent leaves (-110 - 16 is that of fp32's smallest normal).
 constexpr int kDown = 16;
 constexpr float kUp = 65536.0f;
-
-struct AttnArgs {
-  const uint16_t* Q;
-  uint16_t* O;
-  float* lse;            // or NULL
-  float* part;           // splits > 1: [splits][rows][heads][dim], then [splits][rows][heads][2]
-  const int32_t* cu;
-  const int32_t* len;
-  const int32_t* table;
-  const uint8_t* kc;
-  const uint8_t* vc;
-  const uint8_t* ks;
-  const uint8_t* vs;
-  int64_t ldq, ldo, rows, max_blocks, n_pages;
-  int B, Hq, Hkv, G, tiles, splits, causal, max_q;
-  float c;
-  float to_ln, to_ln_lo;  // scale / c, in two parts: c is rounded, and lse in units of scale
-};
-
-// One sequence and key head of a block.  Tokens, rows and pages fit 32 bits (lengths are int32,
-// and the entry point bounds rows·G); addresses are formed in 64.
-struct Seq {
-  int first;   // packed row of its first token
-  int n, kv;   // query tokens, cached tokens
-  int q;       // query tokens that are computed: at most the caller's bound
-  int b, h;
-};
-
-__device__ __forceinline__ bool sequence(const AttnArgs& a, int bh, Seq& s) {
-  s.b = bh / a.Hkv;
-  s.h = bh % a.Hkv;
-  s.first = a.cu[s.b];
-  const int end = a.cu[s.b + 1];
-  if (s.first < 0 || end <= s.first || end > a.rows) return false;
-  s.n = end - s.first;
-  s.q = s.n < a.max_q ? s.n : a.max_q;
-  s.kv = a.len[s.b];
-  const int64_t room = a.max_blocks * kPage;
-  s.kv = s.kv < 0 ? 0 : (s.kv > room ? (int)room : s.kv);
-  return true;
-}
-
-// Tokens [0, limit) are visible to query token i.
-__device__ __forceinline__ int limit_of(const AttnArgs& a, const Seq& s, int i) {
-  if (!a.causal) return s.kv;
-  const int v = s.kv - s.n + i + 1;
-  return v < 0 ? 0 : v;
-}
-
-// A lane's part of its row's query: channels 64s + 32·half + 8j .. + 7, the operand of step j of the
-// products with the 64 channels s.
-template <int DIM>
-struct QueryRow {
-  u32x4_t w[DIM / 64][4];
-};
-
-template <int DIM>
-__device__ __forceinline__ void query_load(const uint16_t* q, int half, QueryRow<DIM>& r) {
-#pragma unroll
-  for (int s = 0; s < DIM / 64; ++s)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) r.w[s][j] = reinterpret_cast<const u32x4_t*>(q + 64 * s + 32 * half)[j];
-}
-
-// An infinity or NaN in the row makes all of it NaN (and so every score).
-template <int DIM>
-__device__ __forceinline__ void query_check(QueryRow<DIM>& r) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int s = 0; s < DIM / 64; ++s)
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) m = max_bf16x2(m, r.w[s][j][c] & 0x7FFF7FFFu);
-  m = max_bf16x2(m, m >> 16) & 0xFFFFu;
-  const uint32_t there = (uint32_t)__shfl_xor((int)m, 32);
-  if ((there > m ? there : m) < kInfBits) return;
-#pragma unroll
-  for (int s = 0; s < DIM / 64; ++s)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) r.w[s][j] = u32x4_t{0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu};
-}
-
-template <int DIM>
-struct State {
-  f32x16_t o[DIM / 32];  // Oᵀ: lane column = row, registers = channels 8(i/4) + 4·half + i%4
-  float m, l;            // maximum (log2 units) and this half's sum
-};
-
-template <int DIM>
-__device__ __forceinline__ void state_init(State<DIM>& st) {
-#pragma unroll
-  for (int j = 0; j < DIM / 32; ++j)
-#pragma unroll
-    for (int i = 0; i < 16; ++i) st.o[j][i] = 0.0f;
-  st.m = kNoMax;
-  st.l = 0.0f;
-}
-
-// The value of the lane's partner in the other half (the same row).
-__device__ __forceinline__ float other_half(float x) {
-  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false,
-                                                  false);
-  return __uint_as_float((threadIdx.x & 32) ? r[0] : r[1]);
-}
 
 // Eight codes of V, widened exactly with the page's scale: one lane's part of a 16-token step.
 __device__ __forceinline__ bf16x8_t widen8(uint32_t lo, uint32_t hi, float scale) {
@@ -203,68 +95,6 @@ __device__ __forceinline__ void scores(f32x16_t (&z)[2], const QueryRow<DIM>& q,
   }
 }
 
-// Scores of the tokens that the lane's row does not see (lim and later) become −inf.
-__device__ __forceinline__ void hide(f32x16_t (&z)[2], int lim, int half) {
-  lim -= 4 * half;  // the registers' tokens are then constants
-#pragma unroll
-  for (int tb = 0; tb < 2; ++tb)
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (32 * tb + 8 * (i >> 2) + (i & 3) >= lim) z[tb][i] = -__builtin_inff();
-}
-
-// The larger of the two halves' values.
-__device__ __forceinline__ float across(float m) {
-  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(m), __float_as_uint(m), false,
-                                                  false);
-  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
-}
-
-// The page's largest score of the lane's row, in log2 units.
-__device__ __forceinline__ float largest(const f32x16_t (&z)[2], float c) {
-  float t[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    t[k] = fmaxf(z[k >> 1][8 * (k & 1)], z[k >> 1][8 * (k & 1) + 1]);
-#pragma unroll
-    for (int i = 2; i < 8; i += 2)
-      t[k] = fmaxf(fmaxf(t[k], z[k >> 1][8 * (k & 1) + i]), z[k >> 1][8 * (k & 1) + i + 1]);
-  }
-  return across(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]))) * c;
-}
-
-// Raises the running maximum to the page's: always, or where some row needs it.
-template <int DIM>
-__device__ __forceinline__ void raise_to(State<DIM>& st, float top) {
-  const float m = fmaxf(st.m, top), f = __builtin_amdgcn_exp2f(st.m - m);
-#pragma unroll
-  for (int j = 0; j < DIM / 32; ++j)
-#pragma unroll
-    for (int i = 0; i < 16; ++i) st.o[j][i] *= f;
-  st.l *= f;
-  st.m = m;
-}
-
-template <int DIM>
-__device__ __forceinline__ void raise(State<DIM>& st, float top) {
-  if (__builtin_amdgcn_ballot_w64(top > st.m + kRaise) != 0) raise_to(st, top);
-}
-
-// Weights of 16 tokens (step g of token block tb) as an operand of the product with V.
-template <int DIM>
-__device__ __forceinline__ bf16x8_t weights(State<DIM>& st, const f32x16_t (&z)[2], int tb, int g,
-                                            float c) {
-  u32x4_t w;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(z[tb][8 * g + 2 * j], c, -st.m));
-    const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(z[tb][8 * g + 2 * j + 1], c, -st.m));
-    st.l += x + y;
-    w[j] = pack_bf16x2(x, y);
-  }
-  return __builtin_bit_cast(bf16x8_t, w);
-}
-
 // NaN in the channels in which a token that the lane's row sees, in pages [p0, p1), has a NaN code.
 template <int DIM>
 __device__ __forceinline__ void restore_nan(const AttnArgs& a, const Seq& s, State<DIM>& st, int p0,
@@ -293,13 +123,6 @@ __device__ __forceinline__ void restore_nan(const AttnArgs& a, const Seq& s, Sta
 
 constexpr int kPresent = 1 << 16;
 
-// The lane's logical page `at` (of pages [0, end), end >= 1; later ones repeat the last): its
-// number in the cache, −1 outside it.
-__device__ __forceinline__ int page_id(const AttnArgs& a, const Seq& s, int at, int end) {
-  const int p = a.table[(int64_t)s.b * a.max_blocks + (at < end ? at : end - 1)];
-  return p >= 0 && p < a.n_pages ? p : -1;
-}
-
 // Exponent bytes (k | v << 8 | kPresent, V's less kDown) of a page, no flag outside the cache; the
 // number of a missing page becomes 0, which can be read.
 __device__ __forceinline__ int page_exps(const AttnArgs& a, const Seq& s, int& page) {
@@ -309,13 +132,6 @@ __device__ __forceinline__ int page_exps(const AttnArgs& a, const Seq& s, int& p
   const int v = (int)a.vs[i] - kDown;  // (below 0: only in a page that was never written)
   const int e = (int)a.ks[i] | (v < 0 ? 0 : v) << 8;
   return there ? e | kPresent : 0;
-}
-
-// lse from the maximum (c·z rounded; l makes up for that) and the sum.
-__device__ __forceinline__ float lse_of(const AttnArgs& a, float m, float l) {
-  if (l == 0.0f) return -__builtin_inff();
-  const float rest = __builtin_fmaf(m, a.to_ln_lo, 0.6931471805599453f * __builtin_amdgcn_logf(l));
-  return __builtin_fmaf(m, a.to_ln, rest);
 }
 
 // Output of one row: bf16 and lse, or the unnormalised sums of a split.
@@ -356,9 +172,6 @@ __device__ __forceinline__ void store_row(const AttnArgs& a, const State<DIM>& s
 // two pages ahead and K's three, and are widened to bf16 on the way, once for the four waves (each
 // wave widening all of V for itself took a third of its vector instructions, all of K 3 % of the
 // time of 16384 x 16384 x 40 heads of 128).  Two images of each, one barrier a page.
-constexpr int kTileWaves = 4;
-constexpr int kTileRows = 32 * kTileWaves;
-
 template <int DIM>
 __global__ __launch_bounds__(64 * kTileWaves, 2) void k_attn_tile(AttnArgs a) {
   constexpr int kBytes = kPage * DIM;                       // one tensor's page
@@ -594,9 +407,6 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void k_attn_tile(AttnArgs a) {
 // Few rows (single tokens, small groups): blocks of 32, whose four waves take every fourth page each,
 // straight into registers, and join their sums through LDS.  Where a key head has more than 32 rows
 // (TILES) its blocks are neighbours on one XCD, and the pages stay in its cache for them.
-constexpr int kFewRows = 32;
-constexpr int64_t kFewMost = 512;  // of a key head, in blocks of so many (measured to there)
-
 template <int DIM, bool TILES>
 __global__ __launch_bounds__(256, 2) void k_attn_few(AttnArgs a) {
   constexpr int kBytes = kPage * DIM;
@@ -773,17 +583,14 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
     if (lane >= kWide) continue;
     const float inv = l != 0.0f ? 1.0f / l : 0.0f;
     *reinterpret_cast<uint2*>(a.O + token * a.ldo + (int64_t)head * DIM + d) =
-        uint2{pack_bf16x2(o[0] * inv * kUp, o[1] * inv * kUp),
-              pack_bf16x2(o[2] * inv * kUp, o[3] * inv * kUp)};
+        uint2{pack_bf16x2(o[0] * inv * a.up, o[1] * inv * a.up),
+              pack_bf16x2(o[2] * inv * a.up, o[3] * inv * a.up)};
     if (a.lse && lane == 0)
       a.lse[at] = lse_of(a, m, l);
   }
 }
 
-struct Plan {
-  bool few;
-  int64_t tiles, splits;
-};
+}  // namespace
 
 // The kernel and the splits of the page range are the ones of the least time, in pages of a wave
 // (1.2 us at 64 channels, 2 at 128).  Both kernels run in rounds of 512 blocks, two a CU.
@@ -802,12 +609,12 @@ struct Plan {
 // against 43, taken all the same).  768 blocks of few instead of 512 took 47 us instead of 39 for 32
 // rows x 2 sequences x 30000 x 8 heads of 128; one split, two nearly full rounds of a third instead of
 // five eighths of one, took tile from 748 to 598 us for 1008 rows x 31688 x 40 heads.
-Plan plan(int64_t G, int64_t Hkv, int64_t dim, int64_t rows, int64_t B, int64_t max_q,
-          int64_t max_kv) {
+AttnPlan attn_plan(int64_t G, int64_t Hkv, int64_t dim, int64_t rows, int64_t B, int64_t max_q,
+                   int64_t max_kv) {
   constexpr int64_t kSlots = 512;
   const int64_t R = max_q * G, heads = B * Hkv, pages = (max_kv + kPage - 1) / kPage;
   const int64_t most = pages / 8 > 1 ? pages / 8 : 1;
-  Plan best{false, 1, 1};
+  AttnPlan best{false, 1, 1};
   double least = -1.0;
   auto offer = [&](bool few, int64_t tiles, int64_t s) {
     if (s < 1 || s > most) return;
@@ -822,7 +629,7 @@ Plan plan(int64_t G, int64_t Hkv, int64_t dim, int64_t rows, int64_t B, int64_t 
     if (s > 1) cost += (few ? 4.0 : 8.0) + (double)(s * rows * G * Hkv * (dim + 2)) * 8.0 / 6.0e6;
     if (least < 0.0 || cost < least) {
       least = cost;
-      best = Plan{few, tiles, s};
+      best = AttnPlan{few, tiles, s};
     }
   };
   const int64_t small = (R + kFewRows - 1) / kFewRows, large = (R + kTileRows - 1) / kTileRows;
@@ -837,17 +644,40 @@ Plan plan(int64_t G, int64_t Hkv, int64_t dim, int64_t rows, int64_t B, int64_t 
   return best;
 }
 
-}  // namespace
+AttnArgs attn_args(const uint16_t* Q, int64_t ldq, int64_t rows, int64_t Hq, int64_t Hkv,
+                   const int32_t* cu, const int32_t* len, int64_t B, int64_t max_q,
+                   const int32_t* table, int64_t max_blocks, int64_t n_pages, const uint8_t* kc,
+                   const uint8_t* vc, const uint8_t* ks, const uint8_t* vs, float scale, int causal,
+                   uint16_t* O, int64_t ldo, float* lse, void* workspace, const AttnPlan& p,
+                   float up) {
+  const float c = (float)((double)scale * 1.4426950408889634);
+  const double to_ln = (double)scale / (double)c;
+  return AttnArgs{Q, O, lse, (float*)workspace, cu, len, table, kc, vc, ks, vs, ldq, ldo, rows,
+                  max_blocks, n_pages, (int)B, (int)Hq, (int)Hkv, (int)(Hq / Hkv), (int)p.tiles,
+                  (int)p.splits, causal, (int)max_q, c, (float)to_ln,
+                  (float)(to_ln - (double)(float)to_ln), up};
+}
+
+hipError_t launch_attn_join(const AttnArgs& a, int64_t dim, hipStream_t s) {
+  // (no sequence has more than all rows, however loose the caller's bound)
+  const int64_t blocks = ((a.max_q < a.rows ? a.max_q : a.rows) * a.Hq + 3) / 4;
+  const dim3 joins((unsigned)(blocks < kJoinMost ? blocks : kJoinMost), (unsigned)a.B);
+  if (dim == 64)
+    k_attn_join<64><<<joins, 256, 0, s>>>(a);
+  else
+    k_attn_join<128><<<joins, 256, 0, s>>>(a);
+  return hipGetLastError();
+}
 
 int64_t attn_workspace_bytes(int64_t rows, int64_t Hq, int64_t Hkv, int64_t dim, int64_t B,
                              int64_t max_q, int64_t max_kv) {
-  const Plan p = plan(Hq / Hkv, Hkv, dim, rows, B, max_q, max_kv);
+  const AttnPlan p = attn_plan(Hq / Hkv, Hkv, dim, rows, B, max_q, max_kv);
   return p.splits > 1 ? p.splits * rows * Hq * (dim + 2) * 4 : 0;
 }
 
 int64_t attn_blocks(int64_t rows, int64_t Hq, int64_t Hkv, int64_t dim, int64_t B, int64_t max_q,
                     int64_t max_kv) {
-  const Plan p = plan(Hq / Hkv, Hkv, dim, rows, B, max_q, max_kv);
+  const AttnPlan p = attn_plan(Hq / Hkv, Hkv, dim, rows, B, max_q, max_kv);
   return B * Hkv * p.tiles * p.splits + 8;
 }
 
@@ -857,12 +687,9 @@ hipError_t launch_attn(const uint16_t* Q, int64_t ldq, int64_t rows, int64_t Hq,
                        int64_t n_pages, const uint8_t* kc, const uint8_t* vc, const uint8_t* ks,
                        const uint8_t* vs, float scale, int causal, uint16_t* O, int64_t ldo,
                        float* lse, void* workspace, hipStream_t s) {
-  const Plan p = plan(Hq / Hkv, Hkv, dim, rows, B, max_q, max_kv);
-  const float c = (float)((double)scale * 1.4426950408889634);
-  const double to_ln = (double)scale / (double)c;
-  AttnArgs a{Q, O, lse, (float*)workspace, cu, len, table, kc, vc, ks, vs, ldq, ldo, rows,
-             max_blocks, n_pages, (int)B, (int)Hq, (int)Hkv, (int)(Hq / Hkv), (int)p.tiles,
-             (int)p.splits, causal, (int)max_q, c, (float)to_ln, (float)(to_ln - (double)(float)to_ln)};
+  const AttnPlan p = attn_plan(Hq / Hkv, Hkv, dim, rows, B, max_q, max_kv);
+  const AttnArgs a = attn_args(Q, ldq, rows, Hq, Hkv, cu, len, B, max_q, table, max_blocks, n_pages,
+                               kc, vc, ks, vs, scale, causal, O, ldo, lse, workspace, p, kUp);
   const int64_t items = B * Hkv * p.tiles * p.splits;
   const unsigned grid = (unsigned)((items + 7) / 8 * 8);
   if (p.few && p.tiles > 1) {
@@ -882,16 +709,7 @@ hipError_t launch_attn(const uint16_t* Q, int64_t ldq, int64_t rows, int64_t Hq,
       k_attn_tile<128><<<grid, 64 * kTileWaves, 0, s>>>(a);
   }
   if (hipError_t e = hipGetLastError()) return e;
-  if (p.splits > 1) {
-    // (no sequence has more than all rows, however loose the caller's bound)
-    const int64_t blocks = ((max_q < rows ? max_q : rows) * Hq + 3) / 4;
-    const dim3 joins((unsigned)(blocks < kJoinMost ? blocks : kJoinMost), (unsigned)B);
-    if (dim == 64)
-      k_attn_join<64><<<joins, 256, 0, s>>>(a);
-    else
-      k_attn_join<128><<<joins, 256, 0, s>>>(a);
-  }
-  return hipGetLastError();
+  return p.splits > 1 ? launch_attn_join(a, dim, s) : hipSuccess;
 }
 
 }  // namespace svdq

@@ -165,4 +165,39 @@ hipError_t launch_attn(const uint16_t* Q, int64_t ldq, int64_t rows, int64_t Hq,
                        const uint8_t* vs, float scale, int causal, uint16_t* O, int64_t ldo,
                        float* lse, void* workspace, hipStream_t s);
 
+// Norm of the query and key heads with their rotary positions.
+hipError_t launch_qk_norm_rope(const uint16_t* X, int64_t M, int64_t ldx, int q_heads, int k_heads,
+                               int dim, const uint16_t* gamma_q, const uint16_t* gamma_k, float eps,
+                               const int32_t* pos, const double* freq, int n_axes,
+                               const int* pairs, int interleaved, uint16_t* Y, int64_t ldy,
+                               hipStream_t s);
+
+// The paged 4-bit cache (layout in kv4_layout.h; dim 64 or 128).
+hipError_t launch_kv4_write(const uint16_t* K, int64_t ldk, const uint16_t* V, int64_t ldv,
+                            int64_t rows, int heads, int dim, const int32_t* cu,
+                            const int32_t* start, int64_t B, int64_t max_new, const int32_t* table,
+                            int64_t max_blocks, int64_t n_pages, uint8_t* kc, uint8_t* vc,
+                            uint8_t* ks, uint8_t* vs, hipStream_t s);
+hipError_t launch_kv4_read(uint16_t* K, int64_t ldk, uint16_t* V, int64_t ldv, int64_t rows,
+                           int heads, int dim, const int32_t* cu, const int32_t* start, int64_t B,
+                           int64_t max_n, const int32_t* table, int64_t max_blocks,
+                           int64_t n_pages, const uint8_t* kc, const uint8_t* vc,
+                           const uint8_t* ks, const uint8_t* vs, hipStream_t s);
+
+// Attention over it; workspace and blocks as for the 8-bit cache.
+hipError_t launch_attn4(const uint16_t* Q, int64_t ldq, int64_t rows, int64_t Hq, int64_t Hkv,
+                        int64_t dim, const int32_t* cu, const int32_t* len, int64_t B,
+                        int64_t max_q, int64_t max_kv, const int32_t* table, int64_t max_blocks,
+                        int64_t n_pages, const uint8_t* kc, const uint8_t* vc, const uint8_t* ks,
+                        const uint8_t* vs, float scale, int causal, uint16_t* O, int64_t ldo,
+                        float* lse, void* workspace, hipStream_t s);
+
+// Rows that the few-row product takes.
+constexpr int64_t kGemvMostRows = 64;
+int64_t gemv_workspace_bytes(int64_t M, int64_t K, int64_t r, bool smooth);
+hipError_t launch_gemv(int fmt, const uint16_t* X, int64_t M, int64_t K, int64_t ldx,
+                       const float* lambda, const uint16_t* down, int64_t r, const uint8_t* codes,
+                       const void* scales, const float* g, const uint16_t* up, int64_t N,
+                       uint16_t* Y, int64_t ldy, void* workspace, hipStream_t s);
+
 }  // namespace svdq

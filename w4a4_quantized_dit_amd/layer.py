@@ -247,6 +247,37 @@ def forward(X, pw, act_amax, lam, lora_down, out=None):
     return Y.reshape(*lead, pw.N)
 
 
+def _bytes(n, device):
+    """A 256-byte aligned workspace of n bytes."""
+    buf = _torch().empty(n + 256, dtype=_torch().uint8, device=device)
+    off = (-buf.data_ptr()) % 256
+    return buf[off:off + n]
+
+
+def gemv_workspace(rows, pw, smooth=True, device="cuda"):
+    """A workspace for gemv() of so many rows (None when none is needed); smooth: with a λ."""
+    nb = _lib.svdq_w4a16_gemv_workspace_bytes(rows, pw.K, pw.r, smooth)
+    if nb < 0:
+        raise ValueError(f"unsupported: {rows} rows (at most 64), K={pw.K}, rank {pw.r}")
+    return _bytes(nb, device) if nb else None
+
+
+def gemv(X, pw, lam, lora_down, out=None, workspace=None):
+    """forward() of at most 64 rows without activation quantisation: Y = X̂·L1·L2 + X̂·Q(R) with the
+    16-bit X̂ = bf16(X / λ) for X [..., K] bf16 and a 4-bit weight pw (NVFP4, INT4_G64, MXFP4); out: bf16
+    [rows, N].  For single tokens and small batches, where the weight's bytes are the work."""
+    torch = _torch()
+    lead = X.shape[:-1]
+    X2 = X if X.dim() == 2 else X.reshape(-1, X.shape[-1])
+    M = X2.shape[0]
+    Y = out if out is not None else torch.empty(M, pw.N, dtype=torch.bfloat16, device=X.device)
+    if workspace is None:
+        workspace = gemv_workspace(M, pw, lam is not None, X.device)
+    _lib.svdq_w4a16_gemv(pw.fmt, X2, lam, lora_down, pw.r, pw.codes, pw.scales, pw.g, pw.lora_up, pw.N,
+                         Y, workspace)
+    return Y if len(lead) == 1 else Y.reshape(*lead, pw.N)
+
+
 # ------------------------------------------------------------------------------------------
 # the attention half of the block
 # ------------------------------------------------------------------------------------------
@@ -289,29 +320,53 @@ def rope(X, pos, freq, axis_dims, dim, interleaved=True, inverse=False, out=None
     return Y
 
 
+def qk_norm_rope(X, pos, freq, axis_dims, dim, q_heads, gamma_q, gamma_k, eps=1e-6, interleaved=True,
+                 out=None):
+    """RMS norm of every head of X [M, heads·dim] bf16 with the rotary positions in the same pass: the
+    first q_heads heads with gamma_q, the others (keys) with gamma_k (bf16 [dim]; None: 1).  pos, freq
+    and axis_dims as rope() takes them.  out=X works in place."""
+    torch = _torch()
+    Y = out if out is not None else torch.empty(X.shape, dtype=X.dtype, device=X.device)
+    _lib.svdq_qk_norm_rope(X, q_heads, X.shape[1] // dim - q_heads, dim, gamma_q, gamma_k, eps, pos,
+                           freq, axis_dims, interleaved, Y)
+    return Y
+
+
 @dataclass
 class KVCache:
-    k_codes: object      # uint8 [pages, heads, 64·dim], operand order (include/svdq.h)
+    k_codes: object      # uint8 [pages, heads, 64·dim], operand order (include/svdq.h); 4 bits: 32·dim
     v_codes: object
-    k_scales: object     # uint8 [pages, heads]: the page's exponent + 127
+    k_scales: object     # uint8 [pages, heads]: the page's exponent + 127; 4 bits: [pages, heads, 2·dim]
     v_scales: object
     dim: int
+    bits: int = 8        # 8: E4M3 codes, a scale per page and head; 4: MXFP4, one per token and 32 channels
 
 
-def kv_cache(n_pages, heads, dim, device="cuda"):
-    """An empty paged 8-bit cache of n_pages pages of 64 tokens."""
+def _by_bits(cache, eight, four):
+    if cache.bits not in (4, 8):
+        raise ValueError(f"a cache of {cache.bits} bits: must be 4 or 8")
+    return eight if cache.bits == 8 else four
+
+
+def kv_cache(n_pages, heads, dim, device="cuda", bits=8):
+    """An empty paged cache of n_pages pages of 64 tokens, of 8 or 4 bits."""
     torch = _torch()
-    codes = [torch.zeros(n_pages, heads, KV_PAGE * dim, dtype=torch.uint8, device=device)
+    if bits not in (4, 8):
+        raise ValueError(f"a cache of {bits} bits: must be 4 or 8")
+    codes = [torch.zeros(n_pages, heads, KV_PAGE * dim * bits // 8, dtype=torch.uint8, device=device)
              for _ in range(2)]
-    scales = [torch.zeros(n_pages, heads, dtype=torch.uint8, device=device) for _ in range(2)]
-    return KVCache(codes[0], codes[1], scales[0], scales[1], dim)
+    shape = (n_pages, heads) if bits == 8 else (n_pages, heads, 2 * dim)
+    scales = [torch.zeros(shape, dtype=torch.uint8, device=device) for _ in range(2)]
+    return KVCache(codes[0], codes[1], scales[0], scales[1], dim, bits)
 
 
 def kv_write(cache, K, V, block_table, cu_rows, start, max_rows):
     """Append the packed rows K, V [rows, heads·dim] bf16: sequence b's rows cu_rows[b] ..
-    cu_rows[b + 1] become its tokens start[b] onward, quantised with one scale a page and head."""
-    _lib.svdq_kv_write(K, V, cache.dim, cu_rows, start, max_rows, block_table, cache.k_codes,
-                       cache.v_codes, cache.k_scales, cache.v_scales)
+    cu_rows[b + 1] become its tokens start[b] onward, quantised with one scale a page and head (8
+    bits) or a token and 32 channels (4 bits)."""
+    _by_bits(cache, _lib.svdq_kv_write, _lib.svdq_kv4_write)(
+        K, V, cache.dim, cu_rows, start, max_rows, block_table, cache.k_codes, cache.v_codes,
+        cache.k_scales, cache.v_scales)
 
 
 def kv_read(cache, block_table, cu_rows, start, rows, max_rows, out=None):
@@ -321,22 +376,20 @@ def kv_read(cache, block_table, cu_rows, start, rows, max_rows, out=None):
         shape = (rows, cache.k_codes.shape[1] * cache.dim)
         out = [torch.empty(shape, dtype=torch.bfloat16, device=cache.k_codes.device)
                for _ in range(2)]
-    _lib.svdq_kv_read(out[0], out[1], cache.dim, cu_rows, start, max_rows, block_table,
-                      cache.k_codes, cache.v_codes, cache.k_scales, cache.v_scales)
+    _by_bits(cache, _lib.svdq_kv_read, _lib.svdq_kv4_read)(
+        out[0], out[1], cache.dim, cu_rows, start, max_rows, block_table, cache.k_codes, cache.v_codes,
+        cache.k_scales, cache.v_scales)
     return out[0], out[1]
 
 
-def attention_workspace(rows, q_heads, kv_heads, dim, B, max_rows, max_kv, device="cuda"):
-    """A workspace for attention() of these sizes (None when none is needed)."""
-    torch = _torch()
-    nb = _lib.svdq_attn_kv8_workspace_bytes(rows, q_heads, kv_heads, dim, B, max_rows, max_kv)
+def attention_workspace(rows, q_heads, kv_heads, dim, B, max_rows, max_kv, device="cuda", bits=8):
+    """A workspace for attention() of these sizes over a cache of `bits` bits (None when none is
+    needed)."""
+    need = _lib.svdq_attn_kv8_workspace_bytes if bits == 8 else _lib.svdq_attn_kv4_workspace_bytes
+    nb = need(rows, q_heads, kv_heads, dim, B, max_rows, max_kv)
     if nb < 0:
         raise ValueError("unsupported attention shape")
-    if nb == 0:
-        return None
-    buf = torch.empty(nb + 256, dtype=torch.uint8, device=device)
-    off = (-buf.data_ptr()) % 256
-    return buf[off:off + nb]
+    return _bytes(nb, device) if nb else None
 
 
 def attention(Q, cache, block_table, cu_rows, kv_len, max_rows, max_kv, scale=None, causal=False,
@@ -352,8 +405,9 @@ def attention(Q, cache, block_table, cu_rows, kv_len, max_rows, max_kv, scale=No
     lse = torch.empty(rows, q_heads, dtype=torch.float32, device=Q.device) if return_lse else None
     if workspace is None:
         workspace = attention_workspace(rows, q_heads, heads, dim, block_table.shape[0], max_rows,
-                                        max_kv, Q.device)
-    _lib.svdq_attn_kv8(Q, dim, cu_rows, kv_len, max_rows, max_kv, block_table, cache.k_codes,
-                       cache.v_codes, cache.k_scales, cache.v_scales,
-                       dim ** -0.5 if scale is None else scale, causal, O, lse, workspace)
+                                        max_kv, Q.device, cache.bits)
+    _by_bits(cache, _lib.svdq_attn_kv8, _lib.svdq_attn_kv4)(
+        Q, dim, cu_rows, kv_len, max_rows, max_kv, block_table, cache.k_codes, cache.v_codes,
+        cache.k_scales, cache.v_scales, dim ** -0.5 if scale is None else scale, causal, O, lse,
+        workspace)
     return (O, lse) if return_lse else O
