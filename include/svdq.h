@@ -669,14 +669,17 @@ svdq_status svdq_attn_kv4(const uint16_t* Q, int64_t ldq, int64_t rows, int64_t 
  *   x̂ = bf16(x·fl32(1/λ))  (lambda NULL: x̂ = x),   D = x̂·lora_downᵀ (fp32)
  *   Y[m, n] = bf16( Σ_k x̂[m, k]·w[n, k] + Σ_j D[m, j]·lora_up[n, j] )
  * w: what w_codes, w_scales (and g_w, NVFP4) stand for, from svdq_quantize_weight: NVFP4, INT4_G64 or
- * MXFP4.  X [M, K] bf16, leading dimension ldx (a multiple of 8), M in [1, 64]; K a multiple of 256, at
- * most 2^24; N >= 1; lora_down [r, K], lora_up [N, r] bf16, r as at svdq_quantize_weight; Y [M, N] bf16,
- * leading dimension ldy >= N, not overlapping X.  X, lambda, the weight and the factors 16-byte aligned.
- * fp32 sums in a fixed order, no atomics: results repeat bit for bit.  workspace: at least
- * svdq_w4a16_gemv_workspace_bytes(M, K, r, lambda != NULL) bytes (0 without lambda and rank; −1:
- * unsupported), 256-byte aligned, the caller's, not shared with a call that may run at the same time.
+ * MXFP4.  X [M, K] bf16, leading dimension ldx (a multiple of 8, at most 2^24), M in [1, 64]; K a
+ * multiple of 256, at most 2^22; N in [1, 2^28]; lora_down [r, K], lora_up [N, r] bf16, r as at
+ * svdq_quantize_weight; Y [M, N] bf16, leading dimension ldy >= N, not overlapping X.  X, lambda, the weight
+ * and the factors 16-byte aligned.  x̂ and w enter exactly, but for NVFP4 and INT4_G64 a channel 2^29 times
+ * smaller than the largest of its 256 (channels 256i to 256i + 255), which loses bits of its eight.
+ * fp32 sums in a fixed order, no atomics: results repeat bit for bit, and a row's result does not depend
+ * on the other rows or their number.  workspace: at least svdq_w4a16_gemv_workspace_bytes(M, N, K, r)
+ * bytes (−1: unsupported), 256-byte aligned, the caller's, not shared with a call that may run at the
+ * same time.
  */
-int64_t svdq_w4a16_gemv_workspace_bytes(int64_t M, int64_t K, int64_t r, int smooth);
+int64_t svdq_w4a16_gemv_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t r);
 svdq_status svdq_w4a16_gemv(int fmt, const uint16_t* X, int64_t M, int64_t K, int64_t ldx,
                             const float* lambda, const uint16_t* lora_down, int64_t r,
                             const uint8_t* w_codes, const void* w_scales, const float* g_w,

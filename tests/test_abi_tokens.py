@@ -125,18 +125,19 @@ def test_gemv_refusals(lib):
     assert call(fmt=4) == INVALID and call(fmt=3) == INVALID and call(fmt=-1) == INVALID
     for M in (0, -1, 65, 1 << 40):
         assert call(M=M) == SHAPE, M
-    for K in (0, 128, 300, (1 << 24) + 256):
-        assert call(K=K, ldx=1 << 25) == SHAPE, K
+    for K in (0, 128, 300, (1 << 22) + 256):
+        assert call(K=K, ldx=1 << 23) == SHAPE, K
+    assert call(ldx=(1 << 24) + 8) == SHAPE
     assert call(N=0) == SHAPE and call(N=(1 << 28) + 1, ldy=1 << 29) == SHAPE
     assert call(ldx=504) == SHAPE and call(ldx=516) == SHAPE and call(ldy=23) == SHAPE
     assert call(r=4) == SHAPE and call(r=136) == SHAPE and call(r=-8) == SHAPE
-    need = lib.svdq_w4a16_gemv_workspace_bytes(4, 512, 8, 1)
-    assert need >= 4 * 512 * 2 + 4 * 8 * 4
+    need = lib.svdq_w4a16_gemv_workspace_bytes(4, 24, 512, 8)
+    assert need >= 4 * 24 * 4 + 4 * 8 * 4
     assert call(wb=need - 1) == SHAPE and call(ws=3 * P + 16) == SHAPE
-    assert lib.svdq_w4a16_gemv_workspace_bytes(4, 512, 0, 0) == 0
-    assert lib.svdq_w4a16_gemv_workspace_bytes(4, 512, 8, 0) == 4 * 8 * 4
-    for bad in ((0, 512, 8, 1), (65, 512, 8, 1), (4, 500, 8, 1), (4, 0, 8, 1), (4, 512, 4, 1),
-                (4, 512, 136, 1), (4, 512, -8, 1), (4, (1 << 24) + 256, 8, 1)):
+    assert 0 < lib.svdq_w4a16_gemv_workspace_bytes(4, 24, 512, 0) < need
+    for bad in ((0, 24, 512, 8), (65, 24, 512, 8), (4, 24, 500, 8), (4, 24, 0, 8), (4, 24, 512, 4),
+                (4, 24, 512, 136), (4, 24, 512, -8), (4, 24, (1 << 22) + 256, 8), (4, 0, 512, 8),
+                (4, (1 << 28) + 1, 512, 8)):
         assert lib.svdq_w4a16_gemv_workspace_bytes(*bad) == -1, bad
 
 

@@ -88,7 +88,7 @@ _SIGS = {
     "svdq_qk_norm_rope": (ctypes.c_int, [_c_p, _i64, _i64, _i64, _i64, _i64, _c_p, _c_p,
                                          ctypes.c_float, _c_p, _c_p, _i64, _c_p, ctypes.c_int, _c_p,
                                          _i64, _c_p]),
-    "svdq_w4a16_gemv_workspace_bytes": (_i64, [_i64, _i64, _i64, ctypes.c_int]),
+    "svdq_w4a16_gemv_workspace_bytes": (_i64, [_i64] * 4),
     "svdq_w4a16_gemv": (ctypes.c_int, [ctypes.c_int, _c_p, _i64, _i64, _i64, _c_p, _c_p, _i64, _c_p,
                                        _c_p, _c_p, _c_p, _i64, _c_p, _i64, _c_p, _i64, _c_p]),
 }
@@ -800,15 +800,15 @@ def svdq_qk_norm_rope(X, q_heads, k_heads, dim, gamma_q, gamma_k, eps, pos, freq
     a.call("svdq_qk_norm_rope", stream, *args)
 
 
-def svdq_w4a16_gemv_workspace_bytes(M, K, r, smooth):
-    return int(load().svdq_w4a16_gemv_workspace_bytes(int(M), int(K), int(r), int(bool(smooth))))
+def svdq_w4a16_gemv_workspace_bytes(M, N, K, r):
+    return int(load().svdq_w4a16_gemv_workspace_bytes(int(M), int(N), int(K), int(r)))
 
 
-def svdq_w4a16_gemv(fmt, X, lam, lora_down, r, w_codes, w_scales, g_w, lora_up, N, Y, workspace=None,
+def svdq_w4a16_gemv(fmt, X, lam, lora_down, r, w_codes, w_scales, g_w, lora_up, N, Y, workspace,
                     stream=None):
     """The layer of a few rows X [M, K] bf16 with 16-bit activations into Y [M, N] bf16; the weight as
     from svdq_quantize_weight, lam fp32 [K] or None, lora_down [r, K], lora_up [N, r] bf16, workspace
-    uint8 (svdq_w4a16_gemv_workspace_bytes) or None."""
+    uint8 (svdq_w4a16_gemv_workspace_bytes)."""
     torch = _torch()
     if X.dim() != 2:
         raise ValueError("X must be a 2-D matrix with contiguous rows")

@@ -1019,11 +1019,11 @@ svdq_status svdq_attn_kv4(const uint16_t* Q, int64_t ldq, int64_t rows, int64_t 
                    stream);
 }
 
-int64_t svdq_w4a16_gemv_workspace_bytes(int64_t M, int64_t K, int64_t r, int smooth) {
-  if (M < 1 || M > svdq::kGemvMostRows || K < 1 || K % 256 != 0 || K > (1 << 24) || r < 0 ||
-      r > 128 || r % 8 != 0)
+int64_t svdq_w4a16_gemv_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t r) {
+  if (M < 1 || M > svdq::kGemvMostRows || N < 1 || N > (1 << 28) || K < 1 || K % 256 != 0 ||
+      K > (1 << 22) || r < 0 || r > 128 || r % 8 != 0)
     return -1;
-  return svdq::gemv_workspace_bytes(M, K, r, smooth != 0);
+  return svdq::gemv_workspace_bytes(M, N, K, r);
 }
 
 svdq_status svdq_w4a16_gemv(int fmt, const uint16_t* X, int64_t M, int64_t K, int64_t ldx,
@@ -1042,11 +1042,13 @@ svdq_status svdq_w4a16_gemv(int fmt, const uint16_t* X, int64_t M, int64_t K, in
     return fail(SVDQ_UNSUPPORTED_SHAPE, "%s: M=%lld must lie in [1, %lld]", fn, (long long)M,
                 (long long)svdq::kGemvMostRows);
   TRY(check_k(fn, K));
-  if (K > (1 << 24))
-    return fail(SVDQ_UNSUPPORTED_SHAPE, "%s: K=%lld exceeds 2^24", fn, (long long)K);
+  if (K > (1 << 22))
+    return fail(SVDQ_UNSUPPORTED_SHAPE, "%s: K=%lld exceeds 2^22", fn, (long long)K);
   if (N < 1 || N > (1 << 28))
     return fail(SVDQ_UNSUPPORTED_SHAPE, "%s: N=%lld must lie in [1, 2^28]", fn, (long long)N);
   TRY(check_ld(fn, "ldx", ldx, K));
+  if (ldx > (1 << 24))  // (with K a buffer of less than 2 GB)
+    return fail(SVDQ_UNSUPPORTED_SHAPE, "%s: ldx=%lld exceeds 2^24", fn, (long long)ldx);
   if (ldy < N)
     return fail(SVDQ_UNSUPPORTED_SHAPE, "%s: ldy=%lld must be >= N=%lld", fn, (long long)ldy,
                 (long long)N);
@@ -1055,15 +1057,13 @@ svdq_status svdq_w4a16_gemv(int fmt, const uint16_t* X, int64_t M, int64_t K, in
     REQUIRE_PTR(lora_down); REQUIRE_PTR(lora_up);
     REQUIRE_ALIGNED(lora_down); REQUIRE_ALIGNED(lora_up);
   }
-  const int64_t need = svdq::gemv_workspace_bytes(M, K, r, lambda != nullptr);
-  if (need > 0) {
-    REQUIRE_PTR(workspace);
-    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
-      return fail(SVDQ_UNSUPPORTED_SHAPE, "%s: workspace must be 256-byte aligned", fn);
-    if (workspace_bytes < need)
-      return fail(SVDQ_UNSUPPORTED_SHAPE, "%s: workspace of %lld bytes, needs %lld", fn,
-                  (long long)workspace_bytes, (long long)need);
-  }
+  const int64_t need = svdq::gemv_workspace_bytes(M, N, K, r);
+  REQUIRE_PTR(workspace);
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return fail(SVDQ_UNSUPPORTED_SHAPE, "%s: workspace must be 256-byte aligned", fn);
+  if (workspace_bytes < need)
+    return fail(SVDQ_UNSUPPORTED_SHAPE, "%s: workspace of %lld bytes, needs %lld", fn,
+                (long long)workspace_bytes, (long long)need);
   return hip_result(svdq::launch_gemv(fmt, X, M, K, ldx, lambda, lora_down, r, w_codes, w_scales,
                                       fmt == SVDQ_NVFP4 ? g_w : nullptr, lora_up, N, Y, ldy,
                                       workspace, reinterpret_cast<hipStream_t>(stream)),

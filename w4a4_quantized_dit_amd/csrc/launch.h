@@ -194,7 +194,7 @@ hipError_t launch_attn4(const uint16_t* Q, int64_t ldq, int64_t rows, int64_t Hq
 
 // Rows that the few-row product takes.
 constexpr int64_t kGemvMostRows = 64;
-int64_t gemv_workspace_bytes(int64_t M, int64_t K, int64_t r, bool smooth);
+int64_t gemv_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t r);
 hipError_t launch_gemv(int fmt, const uint16_t* X, int64_t M, int64_t K, int64_t ldx,
                        const float* lambda, const uint16_t* down, int64_t r, const uint8_t* codes,
                        const void* scales, const float* g, const uint16_t* up, int64_t N,

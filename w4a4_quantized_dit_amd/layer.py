@@ -254,12 +254,12 @@ def _bytes(n, device):
     return buf[off:off + n]
 
 
-def gemv_workspace(rows, pw, smooth=True, device="cuda"):
-    """A workspace for gemv() of so many rows (None when none is needed); smooth: with a λ."""
-    nb = _lib.svdq_w4a16_gemv_workspace_bytes(rows, pw.K, pw.r, smooth)
+def gemv_workspace(rows, pw, device="cuda"):
+    """A workspace for gemv() of so many rows."""
+    nb = _lib.svdq_w4a16_gemv_workspace_bytes(rows, pw.N, pw.K, pw.r)
     if nb < 0:
-        raise ValueError(f"unsupported: {rows} rows (at most 64), K={pw.K}, rank {pw.r}")
-    return _bytes(nb, device) if nb else None
+        raise ValueError(f"unsupported: {rows} rows (at most 64), N={pw.N}, K={pw.K}, rank {pw.r}")
+    return _bytes(nb, device)
 
 
 def gemv(X, pw, lam, lora_down, out=None, workspace=None):
@@ -272,7 +272,7 @@ def gemv(X, pw, lam, lora_down, out=None, workspace=None):
     M = X2.shape[0]
     Y = out if out is not None else torch.empty(M, pw.N, dtype=torch.bfloat16, device=X.device)
     if workspace is None:
-        workspace = gemv_workspace(M, pw, lam is not None, X.device)
+        workspace = gemv_workspace(M, pw, X.device)
     _lib.svdq_w4a16_gemv(pw.fmt, X2, lam, lora_down, pw.r, pw.codes, pw.scales, pw.g, pw.lora_up, pw.N,
                          Y, workspace)
     return Y if len(lead) == 1 else Y.reshape(*lead, pw.N)
