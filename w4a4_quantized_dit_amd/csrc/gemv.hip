@@ -84,12 +84,15 @@ __device__ __forceinline__ u32x4_t widen_mx(uint32_t w, float s) {
                  bits_of(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3))};
 }
 __device__ __forceinline__ u32x4_t widen_int4(uint32_t w) {
-  const uint32_t u = w ^ 0x88888888u;   // code + 8; 0x6400 | u is the fp16 1024 + u
-  const f16x2_t less = {(_Float16)-1032.0f, (_Float16)-1032.0f};
+  const uint32_t u = w ^ 0x88888888u;   // code + 8; as bits of an fp16: 0x6400 + u = 1024 + u, 0x5400 + 16 u = 64 + u
+  const f16x2_t low = {(_Float16)-1032.0f, (_Float16)-1032.0f}, high = {(_Float16)-72.0f, (_Float16)-72.0f};
   u32x4_t r;
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    r[j] = bits_of(__builtin_bit_cast(f16x2_t, ((u >> (4 * j)) & 0x000F000Fu) | 0x64006400u) + less);
+  for (int j = 0; j < 4; j += 2) {
+    const uint32_t v = u >> (4 * j);
+    r[j] = bits_of(__builtin_bit_cast(f16x2_t, (v & 0x000F000Fu) | 0x64006400u) + low);
+    r[j + 1] = bits_of(__builtin_bit_cast(f16x2_t, (v & 0x00F000F0u) | 0x54005400u) + high);
+  }
   return r;
 }
 
@@ -440,7 +443,10 @@ __global__ __launch_bounds__(64 * kWaves, 2) void k_gemv_part(GemvArgs a) {
 }
 
 // The parts' sums and the up factor's product.  A wave has 16 outputs of 16 rows; D, which the block's
-// waves share, is taken to 16 bits in two bf16 (hi + lo), 32 ranks a wave.
+// waves share, is taken to 16 bits in two bf16 (hi + lo), 32 ranks a wave.  Its time is a launch and the
+// latency of loads, so all are on their way at once: eight parts of either, the ones past the last are
+// buffer loads without a request.  (With loops that end at the last part: one row of 5120x5120 NVFP4, rank
+// 32, 14.8 us for 14.3, five of 5120x13824 MXFP4, rank 128, 20.5 for 19.4, both kernels.)
 constexpr int kJoinWaves = 4;
 
 __global__ __launch_bounds__(64 * kJoinWaves) void k_gemv_join(GemvArgs a) {
@@ -450,48 +456,59 @@ __global__ __launch_bounds__(64 * kJoinWaves) void k_gemv_join(GemvArgs a) {
   const int m0 = blockIdx.y * 16, n = (blockIdx.x * kJoinWaves + wave) * 16 + n16;
   const int quads = (a.M + 3) / 4, rq = m0 / 4 + q;
   const bool mine = n < a.N && rq < quads;
-  const u32x4_t none = {0u, 0u, 0u, 0u};
-  f32x4_t sum = {0.f, 0.f, 0.f, 0.f}, low = sum;
-  if (mine) {
-    const f32x4_t* p = reinterpret_cast<const f32x4_t*>(a.sums) + (int64_t)rq * a.N + n;
-#pragma unroll 8
-    for (int s = 0; s < a.parts; ++s) sum += p[(int64_t)s * quads * a.N];
+  const int j = 32 * wave + 8 * q;
+  const bool ranks = j < a.r && m0 + n16 < a.M;   // (r is a multiple of 8)
+  const uint32_t at_d = ranks ? (uint32_t)(((m0 + n16) * a.r + j) * 4) : kNoLoad;
+  const int64_t each_s = (int64_t)quads * a.N, each_d = (int64_t)a.M * a.r;
+  const f32x4_t* sums = reinterpret_cast<const f32x4_t*>(a.sums) + (mine ? (int64_t)rq * a.N + n : 0);
+  f32x4_t sum = {0.f, 0.f, 0.f, 0.f}, low = sum, d0 = sum, d1 = sum;
+  u32x4_t u[kJoinWaves];
+#pragma unroll
+  for (int s = 0; s < kJoinWaves; ++s)
+    u[s] = n < a.N && 32 * s + 8 * q < a.r ? *reinterpret_cast<const u32x4_t*>(a.up + (int64_t)n * a.r + 32 * s + 8 * q)
+                                           : u32x4_t{0u, 0u, 0u, 0u};
+  constexpr int kAtOnce = 8;
+  for (int s0 = 0; s0 < a.parts; s0 += kAtOnce) {
+    f32x4_t v[kAtOnce];
+#pragma unroll
+    for (int s = 0; s < kAtOnce; ++s)   // (past the last: the first again, not added)
+      v[s] = sums[s0 + s < a.parts ? (s0 + s) * each_s : 0];
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int s = 0; s < kAtOnce; ++s)
+      if (s0 + s < a.parts) sum += v[s];
+  }
+  for (int s0 = 0; s0 < a.down_parts; s0 += kAtOnce) {
+    u32x4_t v0[kAtOnce], v1[kAtOnce];
+#pragma unroll
+    for (int s = 0; s < kAtOnce; ++s) {
+      const __amdgpu_buffer_rsrc_t rd = raw_rsrc(a.D + (s0 + s) * each_d, s0 + s < a.down_parts ? (uint32_t)(4 * each_d) : 0u);
+      v0[s] = load16(rd, at_d, 0);
+      v1[s] = load16(rd, at_d, 16);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int s = 0; s < kAtOnce; ++s) {
+      d0 += __builtin_bit_cast(f32x4_t, v0[s]);
+      d1 += __builtin_bit_cast(f32x4_t, v1[s]);
+    }
   }
   if (a.r) {
-    const int j = 32 * wave + 8 * q;
-    if (32 * wave < a.r) {
-      f32x4_t d0 = {0.f, 0.f, 0.f, 0.f}, d1 = d0;
-      if (j < a.r && m0 + n16 < a.M) {   // (r is a multiple of 8)
-        const float* D = a.D + (int64_t)(m0 + n16) * a.r + j;
-#pragma unroll 4
-        for (int s = 0; s < a.down_parts; ++s) {
-          d0 += reinterpret_cast<const f32x4_t*>(D + (int64_t)s * a.M * a.r)[0];
-          d1 += reinterpret_cast<const f32x4_t*>(D + (int64_t)s * a.M * a.r)[1];
-        }
-      }
-      u32x4_t hi, lo;
+    u32x4_t hi, lo;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const float v0 = c < 2 ? d0[2 * (c & 1)] : d1[2 * (c & 1)], v1 = c < 2 ? d0[2 * (c & 1) + 1] : d1[2 * (c & 1) + 1];
-        hi[c] = pack_bf16x2(v0, v1);
-        lo[c] = pack_bf16x2(v0 - bf16_lo(hi[c]), v1 - bf16_hi(hi[c]));
-      }
-      s_d[wave][0][lane] = hi;
-      s_d[wave][1][lane] = lo;
+    for (int c = 0; c < 4; ++c) {
+      const float v0 = c < 2 ? d0[2 * (c & 1)] : d1[2 * (c & 1)], v1 = c < 2 ? d0[2 * (c & 1) + 1] : d1[2 * (c & 1) + 1];
+      hi[c] = pack_bf16x2(v0, v1);
+      lo[c] = pack_bf16x2(v0 - bf16_lo(hi[c]), v1 - bf16_hi(hi[c]));
     }
-    u32x4_t u[kJoinWaves];
-#pragma unroll
-    for (int s = 0; s < kJoinWaves; ++s)
-      u[s] = n < a.N && 32 * s + 8 * q < a.r ? *reinterpret_cast<const u32x4_t*>(a.up + (int64_t)n * a.r + 32 * s + 8 * q)
-                                             : none;
+    s_d[wave][0][lane] = hi;
+    s_d[wave][1][lane] = lo;
     __syncthreads();
 #pragma unroll
     for (int s = 0; s < kJoinWaves; ++s)
       if (32 * s < a.r) {
-        low = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, s_d[s][0][lane]),
-                                                      __builtin_bit_cast(bf16x8_t, u[s]), low, 0, 0, 0);
-        low = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, s_d[s][1][lane]),
-                                                      __builtin_bit_cast(bf16x8_t, u[s]), low, 0, 0, 0);
+        low = product(s_d[s][0][lane], u[s], low, std::false_type{});
+        low = product(s_d[s][1][lane], u[s], low, std::false_type{});
       }
   }
   if (!mine) return;
