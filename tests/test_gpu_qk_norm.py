@@ -153,3 +153,32 @@ def test_more_rows_than_blocks(L):
         want, z = OT.qk_norm_rope(x, 1, None, None, 1e-6, pos[rows].cpu().numpy(), freq, [16], True)
         got = Y[rows].float().cpu().numpy().reshape(n, 2, 16)
         assert np.all(np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -19 * _pair_sums(z, [16], True))
+
+
+@pytest.mark.parametrize("inter", [True, False])
+@pytest.mark.parametrize("M,Hq,Hk,dim,axes", [(1537, 2, 1, 64, [64]), (3085, 5, 2, 96, [32, 32, 16]),
+                                              (6151, 1, 0, 48, [0, 16]), (12293, 1, 1, 64, [16, 24, 24]),
+                                              (24580, 1, 0, 16, [16]), (3073, 20, 1, 128, [64]),
+                                              (12291, 1, 1, 240, [100, 60, 64])])
+def test_several_rows_a_block(L, M, Hq, Hk, dim, axes, inter):
+    """Many rows of few heads, the last block's rows fewer than the others'."""
+    _run(L, M, Hq, Hk, dim, axes, inter, seed=M, tail=1, pad=8, in_place=inter)
+
+
+@pytest.mark.parametrize("M,heads,dim", [((1 << 20) + 21, 2, 16), ((1 << 16) + 5, 513, 16)])
+def test_more_blocks_than_a_grid_has(L, M, heads, dim):
+    """The blocks take a second turn, of several rows or of one."""
+    torch = torch_mod()
+    from w4a4_quantized_dit_amd import _lib
+    n = 40
+    freq = _lib.svdq_rope_frequencies([16], 1000.0)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    X = torch.randn(M, heads * dim, generator=g, device="cuda", dtype=torch.bfloat16)
+    pos = torch.randint(-1000, 1000, (M, 1), generator=g, device="cuda", dtype=torch.int32)
+    Y = L.qk_norm_rope(X, pos, dev(freq), [16], dim, 1, None, None)
+    torch.cuda.synchronize()
+    for rows in (slice(0, n), slice(M - n, M)):
+        x = X[rows].float().cpu().numpy().reshape(n, heads, dim)
+        want, z = OT.qk_norm_rope(x, 1, None, None, 1e-6, pos[rows].cpu().numpy(), freq, [16], True)
+        got = Y[rows].float().cpu().numpy().reshape(n, heads, dim)
+        assert np.all(np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -19 * _pair_sums(z, [16], True))

@@ -7,8 +7,8 @@
 // in fp64).  A sum of squares past fp32's range is formed again in fp64.
 //
 // Memory-bound (4 bytes per element): the norm and the rotation one after the other would move 8.  A
-// block takes a row, or with few rows a part of its heads: the cos / sin of the pairs are formed once, a
-// pair a thread, and kept in LDS, while the first head's loads are on their way.  A thread owns two
+// block takes a row, with few rows a part of its heads, with many rows of few heads several: the cos / sin
+// of the pairs are formed once, a pair a thread, and kept in LDS, while the first head's loads are on their way.  A thread owns two
 // pieces of eight channels, in the same place of every head that it takes, and the 2^n threads of a head
 // are neighbours in a wave, so that the sum is a few lane exchanges.
 #include "device.h"
@@ -29,6 +29,7 @@ struct QkArgs {
   float eps, inv_dim;
   int heads, q_heads, dim, rot, n_axes;
   int lanes;             // threads of a head: dim / 16, rounded up to a power of two
+  int rows;              // of a block (ROWS)
   int end[4];            // pairs up to and including each axis
 };
 
@@ -58,9 +59,11 @@ __device__ __noinline__ float far_inverse(u32x4_t v0, u32x4_t v1, int lanes, flo
   return ldexpf(__builtin_amdgcn_rsqf((float)ldexp(s, -e)), -(e / 2));
 }
 
-template <bool INTERLEAVED, bool NT>
+constexpr int kMostPairs = 512;  // of a block's rows
+
+template <bool INTERLEAVED, bool NT, bool ROWS>
 __global__ __launch_bounds__(256) void k_qk_norm_rope(QkArgs a) {
-  __shared__ __attribute__((aligned(16))) float s_cs[256];  // cos, sin of each pair
+  __shared__ __attribute__((aligned(16))) float s_cs[ROWS ? 2 * kMostPairs : 256];  // cos, sin of each pair (of each row)
   const int unit = (int)threadIdx.x % a.lanes, slot = (int)threadIdx.x / a.lanes;
   const int slots = 256 / a.lanes, step = slots * (int)gridDim.y;
   const int h0 = (int)blockIdx.y * slots + slot;
@@ -83,25 +86,42 @@ __global__ __launch_bounds__(256) void k_qk_norm_rope(QkArgs a) {
       g[1][1] = *reinterpret_cast<const u32x4_t*>(a.gk + p1);
     }
   }
-  for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x) {
+  const int each = ROWS ? a.rows : 1;
+  for (int64_t row = (int64_t)blockIdx.x * each; row < a.M; row += (int64_t)gridDim.x * each) {
     const uint16_t* x = a.X + row * a.ldx;
     uint16_t* y = a.Y + row * a.ldy;
+    const int count = ROWS && a.M - row < each ? (int)(a.M - row) : each;
+    // a head of one of the rows
+    int h = h0, rr = 0;
+    auto settle = [&] {
+      if (ROWS)
+        while (h >= a.heads) {
+          h -= a.heads;
+          ++rr;
+        }
+    };
+    auto there = [&] { return ROWS ? rr < count : h < a.heads; };
     u32x4_t n0 = none, n1 = none;
-    if (own && h0 < a.heads) {
-      n0 = load_nt(x + (int64_t)h0 * a.dim + p0);
-      n1 = load_nt(x + (int64_t)h0 * a.dim + p1);
-    }
-    const int i = threadIdx.x;
-    if (i < a.rot / 2) {
+    auto load = [&] {
+      if (!own || !there()) return;
+      const uint16_t* from = x + (ROWS ? rr * a.ldx : 0) + (int64_t)h * a.dim;
+      n0 = load_nt(from + p0);
+      n1 = load_nt(from + p1);
+    };
+    settle();
+    load();
+    const int pairs = a.rot / 2;
+    for (int t = threadIdx.x; t < count * pairs; t += 256) {
+      const int i = ROWS ? t % pairs : t, r = ROWS ? t / pairs : 0;
       int ax = 0;
 #pragma unroll
       for (int k = 0; k < 3; ++k) ax += (k + 1 < a.n_axes && i >= a.end[k]) ? 1 : 0;
-      const double t = (double)a.pos[row * a.n_axes + ax] * a.freq[i] * 0.15915494309189535;
-      const float f = 2.0f * (float)(t - __builtin_rint(t));
+      const double turns = (double)a.pos[(row + r) * a.n_axes + ax] * a.freq[i] * 0.15915494309189535;
+      const float f = 2.0f * (float)(turns - __builtin_rint(turns));
       float sn, cs;
       sincospif(f, &sn, &cs);
-      s_cs[2 * i] = cs;
-      s_cs[2 * i + 1] = sn;
+      s_cs[2 * t] = cs;
+      s_cs[2 * t + 1] = sn;
     }
     __syncthreads();
     float c[8], s[8];
@@ -110,23 +130,30 @@ __global__ __launch_bounds__(256) void k_qk_norm_rope(QkArgs a) {
       c[j] = 1.0f;
       s[j] = 0.0f;
     }
+    auto angles = [&] {
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      if (own && (k ? turn1 : turn0)) {
-        const int first = INTERLEAVED ? (k ? p1 : p0) / 2 : 8 * unit + 4 * k;
-        const f32x4_t u = *reinterpret_cast<const f32x4_t*>(&s_cs[2 * first]);
-        const f32x4_t v = *reinterpret_cast<const f32x4_t*>(&s_cs[2 * first + 4]);
-        c[4 * k] = u[0]; s[4 * k] = u[1]; c[4 * k + 1] = u[2]; s[4 * k + 1] = u[3];
-        c[4 * k + 2] = v[0]; s[4 * k + 2] = v[1]; c[4 * k + 3] = v[2]; s[4 * k + 3] = v[3];
+      for (int k = 0; k < 2; ++k) {
+        if (own && (k ? turn1 : turn0)) {
+          const int first = (INTERLEAVED ? (k ? p1 : p0) / 2 : 8 * unit + 4 * k) + (ROWS ? rr * pairs : 0);
+          const f32x4_t u = *reinterpret_cast<const f32x4_t*>(&s_cs[2 * first]);
+          const f32x4_t v = *reinterpret_cast<const f32x4_t*>(&s_cs[2 * first + 4]);
+          c[4 * k] = u[0]; s[4 * k] = u[1]; c[4 * k + 1] = u[2]; s[4 * k + 1] = u[3];
+          c[4 * k + 2] = v[0]; s[4 * k + 2] = v[1]; c[4 * k + 3] = v[2]; s[4 * k + 3] = v[3];
+        }
       }
+    };
+    if (!ROWS) {
+      angles();
+      if (row + gridDim.x < a.M) __syncthreads();  // the next row's are written to the same place
     }
-    if (row + gridDim.x < a.M) __syncthreads();  // the next row's are written to the same place
-    for (int h = h0; h < a.heads; h += step) {
+    while (there()) {
       u32x4_t v0 = n0, v1 = n1;
-      if (own && h + step < a.heads) {
-        n0 = load_nt(x + (int64_t)(h + step) * a.dim + p0);
-        n1 = load_nt(x + (int64_t)(h + step) * a.dim + p1);
-      }
+      if (ROWS) angles();
+      uint16_t* const to = y + (ROWS ? rr * a.ldy : 0) + (int64_t)h * a.dim;
+      const bool key = h >= a.q_heads;
+      h += step;
+      settle();
+      load();
       float sum = square_sum(v1, square_sum(v0, 0.0f));
       for (int k = 1; k < a.lanes; k *= 2) sum += __shfl_xor(sum, k);
       float inv = __builtin_amdgcn_rsqf(__builtin_fmaf(sum, a.inv_dim, a.eps));
@@ -134,7 +161,6 @@ __global__ __launch_bounds__(256) void k_qk_norm_rope(QkArgs a) {
         const float far = far_inverse(v0, v1, a.lanes, a.inv_dim, a.eps);
         if (!(sum < 1e37f)) inv = far;
       }
-      const bool key = h >= a.q_heads;
       const u32x4_t g0 = key ? g[1][0] : g[0][0], g1 = key ? g[1][1] : g[0][1];
       float z[16];
 #pragma unroll
@@ -170,10 +196,11 @@ __global__ __launch_bounds__(256) void k_qk_norm_rope(QkArgs a) {
         }
       }
       if (own) {
-        store16<NT>(y + (int64_t)h * a.dim + p0, v0);
-        store16<NT>(y + (int64_t)h * a.dim + p1, v1);
+        store16<NT>(to + p0, v0);
+        store16<NT>(to + p1, v1);
       }
     }
+    if (ROWS && row + (int64_t)gridDim.x * each < a.M) __syncthreads();
   }
 }
 
@@ -185,7 +212,7 @@ hipError_t launch_qk_norm_rope(const uint16_t* X, int64_t M, int64_t ldx, int q_
                                const int* pairs, int interleaved, uint16_t* Y, int64_t ldy,
                                hipStream_t s) {
   QkArgs a{X, Y, gamma_q, gamma_k, pos, freq, M, ldx, ldy, eps, 1.0f / (float)dim,
-           q_heads + k_heads, q_heads, dim, 0, n_axes, 1, {0, 0, 0, 0}};
+           q_heads + k_heads, q_heads, dim, 0, n_axes, 1, 1, {0, 0, 0, 0}};
   int n = 0;
   for (int i = 0; i < n_axes; ++i) a.end[i] = n += pairs[i];
   a.rot = 2 * n;
@@ -194,14 +221,30 @@ hipError_t launch_qk_norm_rope(const uint16_t* X, int64_t M, int64_t ldx, int q_
   // few rows: a row's heads in blocks of their own, as long as the blocks fit the card at once
   int parts = 1;
   while (parts < rounds && M * parts < 1024) ++parts;
-  const dim3 grid((unsigned)(M < (1 << 21) ? M : (1 << 21)), (unsigned)parts);
+  // Many rows of few heads: several rows a block, as long as three blocks a CU remain and the rows are at
+  // most four rounds of its threads.  Rows of 40 heads of 64: 4001 take 11.7 us, four a block, and 14.1 one a
+  // block (eight 12.4), 32000 69 and 84; 32768 of nine heads of 128 34 and 69; 2048 of 18 heads of 64 5.8,
+  // two a block, and 7.3 (four 6.4).  With six rounds 31688 of 48 heads of 128 take 142 us for 131.
+  while (a.rows < 16 && 2 * a.rows * n <= kMostPairs && M >= 2 * a.rows * 768 &&
+         2 * a.rows * a.heads * a.lanes <= 4 * 256)
+    a.rows *= 2;
+  const int64_t blocks = (M + a.rows - 1) / a.rows;
+  const dim3 grid((unsigned)(blocks < (1 << 16) ? blocks : (1 << 16)), (unsigned)parts);
   const bool nt = M * a.heads * dim * 2 > kPastCaches;
-  if (interleaved)
-    nt ? k_qk_norm_rope<true, true><<<grid, 256, 0, s>>>(a)
-       : k_qk_norm_rope<true, false><<<grid, 256, 0, s>>>(a);
-  else
-    nt ? k_qk_norm_rope<false, true><<<grid, 256, 0, s>>>(a)
-       : k_qk_norm_rope<false, false><<<grid, 256, 0, s>>>(a);
+  if (a.rows > 1) {
+    if (interleaved)
+      nt ? k_qk_norm_rope<true, true, true><<<grid, 256, 0, s>>>(a)
+         : k_qk_norm_rope<true, false, true><<<grid, 256, 0, s>>>(a);
+    else
+      nt ? k_qk_norm_rope<false, true, true><<<grid, 256, 0, s>>>(a)
+         : k_qk_norm_rope<false, false, true><<<grid, 256, 0, s>>>(a);
+  } else if (interleaved) {
+    nt ? k_qk_norm_rope<true, true, false><<<grid, 256, 0, s>>>(a)
+       : k_qk_norm_rope<true, false, false><<<grid, 256, 0, s>>>(a);
+  } else {
+    nt ? k_qk_norm_rope<false, true, false><<<grid, 256, 0, s>>>(a)
+       : k_qk_norm_rope<false, false, false><<<grid, 256, 0, s>>>(a);
+  }
   return hipGetLastError();
 }
 
