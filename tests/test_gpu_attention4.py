@@ -488,3 +488,47 @@ def test_empty_batches(L):
     k, v = L.kv_read(kv, i32([[0]]), i32([0, 0]), i32([0]), 0, 0)
     assert k.shape == (0, 64) and v.shape == (0, 64)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("G,q_lens", [(1, [1] * 6), (5, [1] * 6), (16, [1] * 6), (4, [4, 1, 2, 3, 4, 0]),
+                                      (1, [16, 3, 1, 16, 7, 2])])
+@pytest.mark.parametrize("max_kv", [5000, 300000, 64])
+def test_sixteen_rows_over_ragged_splits(L, dim, causal, G, q_lens, max_kv):
+    """Splits of one length: shorter sequences have fewer, the empty one none, whatever the bound says."""
+    run(L, q_lens, [5000, 3, 0, 700, 513, 4999], 2 * G, 2, dim, causal, seed=G, tail=2, max_kv=max_kv)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("causal", [False, True])
+def test_sixteen_rows_of_many_heads(L, dim, causal):
+    """More sequences and heads than compute units."""
+    kv = np.random.default_rng(12).integers(0, 400, 44)
+    run(L, [1] * 22 + [3, 2] * 11, [int(v) for v in kv], 24, 6, dim, causal, seed=4)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_eight_waves_walk_hundreds_of_pages(L, dim):
+    """As many heads and sequences as compute units: one block each, which looks page numbers up twice."""
+    from w4a4_quantized_dit_amd import _lib
+    rng = np.random.default_rng(13)
+    heads, B, kv = 64, 4, 33000
+    assert _lib.svdq_attn_kv4_workspace_bytes(B, heads, heads, dim, B, 1, kv) == 0
+    c, table = make_cache(rng, [kv], 1, dim, garbage=0x55)
+    table = table.copy()
+    table[0, [5, 62, 514]] = -1
+    big = OT.new_cache(len(c["kc"]), 1, dim)
+    for k in ("kc", "vc", "ks", "vs"):
+        big[k] = np.repeat(c[k], heads, axis=1)
+    torch = torch_mod()
+    one = bf16_rne(rng.standard_normal((1, dim)).astype(np.float32))
+    O, lse = L.attention(dev_bf16(np.tile(one, (B, heads))), device_cache(L, big),
+                         i32(np.repeat(table, B, axis=0)), i32(np.arange(B + 1)), i32([kv] * B), 1, kv,
+                         causal=True, return_lse=True)
+    torch.cuda.synchronize()
+    want = OT.attention(bf16_bits_to_f32(one).reshape(1, 1, dim), c, table, [0, 1], [kv],
+                        float(np.float32(dim ** -0.5)), True)
+    O = O.float().cpu().numpy().reshape(B * heads, 1, dim).astype(np.float64)
+    assert np.all(O == O[:1])
+    check(want, O[:1], lse.cpu().numpy().reshape(-1)[:1, None].astype(np.float64), kv)

@@ -191,7 +191,7 @@ svdq_status kv_call(const char* fn, Launch launch, bool wide_scales, Row* K, int
 
 // Attention over a paged cache.
 template <class Launch>
-svdq_status attn_call(const char* fn, Launch launch, bool wide_scales, const uint16_t* Q, int64_t ldq,
+svdq_status attn_call(const char* fn, Launch launch, bool four, const uint16_t* Q, int64_t ldq,
                       int64_t rows, int64_t q_heads, int64_t kv_heads, int64_t dim,
                       const int32_t* cu_rows, const int32_t* kv_len, int64_t B, int64_t max_rows,
                       int64_t max_kv, const int32_t* block_table, int64_t max_blocks,
@@ -203,7 +203,7 @@ svdq_status attn_call(const char* fn, Launch launch, bool wide_scales, const uin
   REQUIRE_ALIGNED(Q); REQUIRE_ALIGNED(O); REQUIRE_ALIGNED(lse);
   TRY(check_cache(fn, kv_heads, dim, cu_rows, B, rows, max_rows, block_table, max_blocks, n_pages,
                   k_codes, v_codes, k_scales, v_scales));
-  if (wide_scales) { REQUIRE_ALIGNED(k_scales); REQUIRE_ALIGNED(v_scales); }
+  if (four) { REQUIRE_ALIGNED(k_scales); REQUIRE_ALIGNED(v_scales); }
   if (q_heads < kv_heads || q_heads % kv_heads != 0 || q_heads > 65535)
     return fail(SVDQ_UNSUPPORTED_SHAPE,
                 "%s: q_heads=%lld must be a multiple of kv_heads=%lld, at most 65535", fn,
@@ -218,8 +218,8 @@ svdq_status attn_call(const char* fn, Launch launch, bool wide_scales, const uin
   if (max_rows * q_heads > (1 << 28) || rows * (q_heads / kv_heads) > (1 << 30))
     return fail(SVDQ_UNSUPPORTED_SHAPE, "%s: more than 2^28 rows and heads in a sequence", fn);
   if (rows == 0 || max_rows == 0) return ok();
-  const int64_t need =
-      svdq::attn_workspace_bytes(rows, q_heads, kv_heads, dim, B, max_rows, max_kv);
+  const int64_t need = (four ? svdq::attn4_workspace_bytes : svdq::attn_workspace_bytes)(
+      rows, q_heads, kv_heads, dim, B, max_rows, max_kv);
   if (need > 0) {
     REQUIRE_PTR(workspace);
     if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
@@ -228,13 +228,22 @@ svdq_status attn_call(const char* fn, Launch launch, bool wide_scales, const uin
       return fail(SVDQ_UNSUPPORTED_SHAPE, "%s: workspace of %lld bytes, needs %lld", fn,
                   (long long)workspace_bytes, (long long)need);
   }
-  if (svdq::attn_blocks(rows, q_heads, kv_heads, dim, B, max_rows, max_kv) >= (1 << 24))
+  if ((four ? svdq::attn4_blocks : svdq::attn_blocks)(rows, q_heads, kv_heads, dim, B, max_rows,
+                                                      max_kv) >= (1 << 24))
     return fail(SVDQ_UNSUPPORTED_SHAPE, "%s: more than 2^24 blocks of rows and heads", fn);
   return hip_result(launch(Q, ldq, rows, q_heads, kv_heads, dim, cu_rows, kv_len, B,
                                       max_rows, max_kv, block_table, max_blocks, n_pages, k_codes,
                                       v_codes, k_scales, v_scales, scale, causal != 0, O, ldo, lse,
                                       workspace, reinterpret_cast<hipStream_t>(stream)),
                     fn);
+}
+
+// Sizes that an attention call takes.
+bool attn_sizes(int64_t rows, int64_t q_heads, int64_t kv_heads, int64_t dim, int64_t B,
+                int64_t max_rows, int64_t max_kv) {
+  return rows >= 0 && kv_heads >= 1 && q_heads >= kv_heads && q_heads % kv_heads == 0 &&
+         q_heads <= 65535 && (dim == 64 || dim == 128) && B >= 1 && B <= 65535 && max_rows >= 0 &&
+         max_kv >= 0 && rows <= (1 << 28) && max_rows <= (1 << 28) && max_kv <= INT32_MAX;
 }
 
 }  // namespace
@@ -979,10 +988,7 @@ svdq_status svdq_kv4_read(uint16_t* K, int64_t ldk, uint16_t* V, int64_t ldv, in
 
 int64_t svdq_attn_kv8_workspace_bytes(int64_t rows, int64_t q_heads, int64_t kv_heads,
                                       int64_t dim, int64_t B, int64_t max_rows, int64_t max_kv) {
-  if (rows < 0 || kv_heads < 1 || q_heads < kv_heads || q_heads % kv_heads != 0 ||
-      q_heads > 65535 || (dim != 64 && dim != 128) || B < 1 || B > 65535 || max_rows < 0 ||
-      max_kv < 0 || rows > (1 << 28) || max_rows > (1 << 28) || max_kv > INT32_MAX)
-    return -1;
+  if (!attn_sizes(rows, q_heads, kv_heads, dim, B, max_rows, max_kv)) return -1;
   return svdq::attn_workspace_bytes(rows, q_heads, kv_heads, dim, B, max_rows, max_kv);
 }
 
@@ -1002,7 +1008,8 @@ svdq_status svdq_attn_kv8(const uint16_t* Q, int64_t ldq, int64_t rows, int64_t 
 
 int64_t svdq_attn_kv4_workspace_bytes(int64_t rows, int64_t q_heads, int64_t kv_heads,
                                       int64_t dim, int64_t B, int64_t max_rows, int64_t max_kv) {
-  return svdq_attn_kv8_workspace_bytes(rows, q_heads, kv_heads, dim, B, max_rows, max_kv);
+  if (!attn_sizes(rows, q_heads, kv_heads, dim, B, max_rows, max_kv)) return -1;
+  return svdq::attn4_workspace_bytes(rows, q_heads, kv_heads, dim, B, max_rows, max_kv);
 }
 
 svdq_status svdq_attn_kv4(const uint16_t* Q, int64_t ldq, int64_t rows, int64_t q_heads,

@@ -552,6 +552,14 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
   const int first = a.cu[b], end = a.cu[b + 1];
   if (first < 0 || end <= first || end > a.rows) return;
   const int n = end - first < a.max_q ? end - first : a.max_q;
+  int splits = a.splits;
+  if (a.chunk > 0) {   // (those with pages)
+    Seq s;
+    sequence(a, b * a.Hkv, s);
+    const int pages = (int)(((int64_t)limit_of(a, s, n - 1) + kPage - 1) / kPage), chunk = attn_chunk(a);
+    const int some = (pages + chunk - 1) / chunk;
+    splits = some < 1 ? 1 : some < splits ? some : splits;
+  }
   const int64_t each = a.rows * a.Hq, rows = (int64_t)n * a.Hq;
   for (int64_t local = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); local < rows;
        local += (int64_t)gridDim.x * 4) {
@@ -559,11 +567,11 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
     const int head = (int)(at % a.Hq);
     const float2* ml = reinterpret_cast<const float2*>(a.part + a.splits * each * DIM) + at;
     float m = kNoMax;
-    for (int i = lane; i < a.splits; i += 64) m = fmaxf(m, ml[i * each].x);
+    for (int i = lane; i < splits; i += 64) m = fmaxf(m, ml[i * each].x);
 #pragma unroll
     for (int k = 1; k < 64; k *= 2) m = fmaxf(m, __shfl_xor(m, k));
     float l = 0.0f;
-    for (int i = lane; i < a.splits; i += 64) {
+    for (int i = lane; i < splits; i += 64) {
       const float2 v = ml[i * each];
       l += v.y * __builtin_amdgcn_exp2f(v.x - m);
     }
@@ -572,7 +580,7 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
     const int d = 4 * (lane % kWide);
     f32x4_t o = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
-    for (int i = lane / kWide; i < a.splits; i += kGroups) {
+    for (int i = lane / kWide; i < splits; i += kGroups) {
       const float f = __builtin_amdgcn_exp2f(ml[i * each].x - m);
       o += *reinterpret_cast<const f32x4_t*>(a.part + (i * each + at) * DIM + d) * f;
     }
@@ -614,7 +622,7 @@ AttnPlan attn_plan(int64_t G, int64_t Hkv, int64_t dim, int64_t rows, int64_t B,
   constexpr int64_t kSlots = 512;
   const int64_t R = max_q * G, heads = B * Hkv, pages = (max_kv + kPage - 1) / kPage;
   const int64_t most = pages / 8 > 1 ? pages / 8 : 1;
-  AttnPlan best{false, 1, 1};
+  AttnPlan best{false, 1, 1, 0};
   double least = -1.0;
   auto offer = [&](bool few, int64_t tiles, int64_t s) {
     if (s < 1 || s > most) return;
@@ -629,7 +637,7 @@ AttnPlan attn_plan(int64_t G, int64_t Hkv, int64_t dim, int64_t rows, int64_t B,
     if (s > 1) cost += (few ? 4.0 : 8.0) + (double)(s * rows * G * Hkv * (dim + 2)) * 8.0 / 6.0e6;
     if (least < 0.0 || cost < least) {
       least = cost;
-      best = AttnPlan{few, tiles, s};
+      best = AttnPlan{few, tiles, s, 0};
     }
   };
   const int64_t small = (R + kFewRows - 1) / kFewRows, large = (R + kTileRows - 1) / kTileRows;
@@ -655,7 +663,7 @@ AttnArgs attn_args(const uint16_t* Q, int64_t ldq, int64_t rows, int64_t Hq, int
   return AttnArgs{Q, O, lse, (float*)workspace, cu, len, table, kc, vc, ks, vs, ldq, ldo, rows,
                   max_blocks, n_pages, (int)B, (int)Hq, (int)Hkv, (int)(Hq / Hkv), (int)p.tiles,
                   (int)p.splits, causal, (int)max_q, c, (float)to_ln,
-                  (float)(to_ln - (double)(float)to_ln), up};
+                  (float)(to_ln - (double)(float)to_ln), up, p.chunk};
 }
 
 hipError_t launch_attn_join(const AttnArgs& a, int64_t dim, hipStream_t s) {

@@ -61,11 +61,11 @@ __device__ __forceinline__ void clear_nan(uint32_t& w, uint32_t& scales, bool& d
   dirty = dirty || __builtin_amdgcn_ballot_w64(nan != 0) != 0;
 }
 
-// NaN in the channels in which a token that the lane's row sees, in pages [p0, p1), has a NaN block.
+// The blocks of channels (bit b: 32 b on) in which a token that the lane's row sees, in pages [p0, p1), has
+// a NaN block.
 template <int DIM>
-__device__ __forceinline__ void restore_nan(const AttnArgs& a, const Seq& s, State<DIM>& st, int p0,
-                                            int p1, int lim_row) {
-  uint32_t bad = 0;  // bit b: channels 32 b on
+__device__ __forceinline__ uint32_t nan_blocks(const AttnArgs& a, const Seq& s, int p0, int p1, int lim_row) {
+  uint32_t bad = 0;
   for (int p = p0; p < p1; ++p) {
     const int page = a.table[(int64_t)s.b * a.max_blocks + p];
     if (page < 0 || page >= a.n_pages) continue;
@@ -76,6 +76,14 @@ __device__ __forceinline__ void restore_nan(const AttnArgs& a, const Seq& s, Sta
       for (int b = 0; b < DIM / 32; ++b)
         if (scales[v4_scale_offset(t, 32 * b)] == kNan4) bad |= 1u << b;
   }
+  return bad;
+}
+
+// NaN in those channels.
+template <int DIM>
+__device__ __forceinline__ void restore_nan(const AttnArgs& a, const Seq& s, State<DIM>& st, int p0,
+                                            int p1, int lim_row) {
+  const uint32_t bad = nan_blocks<DIM>(a, s, p0, p1, lim_row);
   // accumulator j has channels 64 (j/2) + 2 m + j%2, register i of it m = 8(i/4) + 4·half + i%4
 #pragma unroll
   for (int j = 0; j < DIM / 32; ++j)
@@ -372,6 +380,37 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void k_attn4_tile(AttnArgs a) {
   if (live) store_row<DIM>(a, st, l, s.first + tok, head, split, half);
 }
 
+// Element e of a block's [rows, DIM] outputs from its four waves' sums: the bf16, or a split's part.
+template <int DIM, int PITCH, int WAVES>
+__device__ __forceinline__ void store_joined(const AttnArgs& a, const Seq& s, const float (&s_o)[WAVES][DIM][PITCH],
+                                             const float (&s_m)[WAVES][PITCH - 1],
+                                             const float (&s_l)[WAVES][PITCH - 1], int e, int r0, int split) {
+      const int rr = e / DIM, d = e % DIM;
+      float sum = 0.0f, l = 0.0f;
+      float mm = s_m[0][rr];
+#pragma unroll
+  for (int w = 1; w < WAVES; ++w) mm = fmaxf(mm, s_m[w][rr]);
+  #pragma unroll
+      for (int w = 0; w < WAVES; ++w) {
+        sum += s_o[w][d][rr];
+        l += s_l[w][rr] * __builtin_amdgcn_exp2f(s_m[w][rr] - mm);
+      }
+      const int64_t token = s.first + (r0 + rr) / a.G;
+      const int hd = s.h * a.G + (r0 + rr) % a.G;
+      if (a.splits > 1) {
+        const int64_t at = ((int64_t)split * a.rows + token) * a.Hq + hd;
+        a.part[at * DIM + d] = sum;
+        if (d == 0) {
+          float* ml = a.part + (int64_t)a.splits * a.rows * a.Hq * DIM + at * 2;
+          ml[0] = mm;
+          ml[1] = l;
+        }
+      } else {
+        a.O[token * a.ldo + (int64_t)hd * DIM + d] = f32_to_bf16(l != 0.0f ? sum / l : 0.0f);
+        if (a.lse && d == 0) a.lse[token * a.Hq + hd] = lse_of(a, mm, l);
+      }
+}
+
 // Few rows (single tokens, small groups): blocks of 32, whose four waves take every fourth page each,
 // straight into registers, and join their sums through LDS.  Where a key head has more than 32 rows
 // (TILES) its blocks are neighbours on one XCD, and the pages stay in its cache for them.
@@ -514,33 +553,276 @@ __global__ __launch_bounds__(256, 2) void k_attn4_few(AttnArgs a) {
     for (int i = 0; i < 16; ++i)
       s_o[wave][64 * (j >> 1) + 2 * (8 * (i >> 2) + 4 * half + (i & 3)) + (j & 1)][n] = st.o[j][i] * f;
   __syncthreads();
-  for (int o = threadIdx.x; o < R * DIM; o += 256) {
-    const int rr = o / DIM, d = o % DIM;
-    float sum = 0.0f, l = 0.0f;
-    const float mm = fmaxf(fmaxf(s_m[0][rr], s_m[1][rr]), fmaxf(s_m[2][rr], s_m[3][rr]));
+  for (int at = threadIdx.x; at < R * DIM; at += 256) store_joined<DIM, 33, 4>(a, s, s_o, s_m, s_l, at, r0, split);
+}
+
+// At most 16 rows of a key head (single tokens whose query heads share it): the same on the 16x16x32 MFMA, in
+// half the matrix instructions, exponentials and registers, so that three waves a SIMD have their loads on
+// the way and not two.  A block takes `chunk` pages (attn_chunk), its waves every eighth or fourth of them.
+//
+// The lanes of K's and V's operands differ from the stored ones in one bit of the lane and one of the dword,
+// which lane swaps of the codes exchange: lane 16·g + n of K has token n of sixteen at 8 channels, of V
+// four tokens 4·g on at channels 2·n, 2·n + 1 of 32.  V's scales come as a word a lane and pass through LDS.
+//
+// Bound by the vector instructions, 460 a page, which take a SIMD 0.9 us (a lone block of four waves or of
+// eight walks 64 pages in 15 us): 32 sequences of 8191 tokens, 8 key heads of 128 with 5 rows each, 50.6 us,
+// 5.6 TB/s (with the 32 rows' kernel 54.6), ragged ones 47.4 (53.7).
+constexpr int kLeastRows = 16;
+
+struct Words2 {
+  uint32_t a, b;
+};
+__device__ __forceinline__ Words2 swap16(uint32_t x, uint32_t y) {
+  const auto r = __builtin_amdgcn_permlane16_swap(x, y, false, false);
+  return Words2{r[0], r[1]};
+}
+__device__ __forceinline__ Words2 swap32(uint32_t x, uint32_t y) {
+  const auto r = __builtin_amdgcn_permlane32_swap(x, y, false, false);
+  return Words2{r[0], r[1]};
+}
+// Of the four lanes of a row.
+__device__ __forceinline__ float row_largest(float m) {
+  const Words2 a = swap16(__float_as_uint(m), __float_as_uint(m));
+  m = fmaxf(__uint_as_float(a.a), __uint_as_float(a.b));
+  const Words2 b = swap32(__float_as_uint(m), __float_as_uint(m));
+  return fmaxf(__uint_as_float(b.a), __uint_as_float(b.b));
+}
+
+template <int DIM, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, 3) void k_attn4_row16(AttnArgs a) {
+  constexpr int kBytes = kPage * DIM / 2, kScales = 2 * DIM, kFrags = DIM / 32;
+  __shared__ float s_o[WAVES][DIM][kLeastRows + 1];
+  __shared__ float s_m[WAVES][kLeastRows], s_l[WAVES][kLeastRows];
+  __shared__ __attribute__((aligned(16))) uint32_t s_vs[WAVES][DIM / 2];
+  const int split = (int)(blockIdx.x % a.splits);
+  Seq s;
+  if (!sequence(a, (int)(blockIdx.x / a.splits), s)) return;
+  const int R = s.q * a.G;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4, n = lane & 15;
+  const bool live = n < R;
+  const int tok = (live ? n : 0) / a.G;
+  const int head = s.h * a.G + (live ? n : 0) % a.G;
+  const int pages = (int)(((int64_t)limit_of(a, s, (R - 1) / a.G) + kPage - 1) / kPage);
+  const int chunk = a.splits > 1 ? __builtin_amdgcn_readfirstlane(attn_chunk(a)) : 0;
+  const int p0 = split * chunk;
+  if (split > 0 && p0 >= pages) return;   // (the join knows)
+  const int p1 = split == a.splits - 1 || pages - p0 < chunk ? pages : p0 + chunk;
+  const int lim_row = live ? limit_of(a, s, tok) : 0;
+  const int lim_first = limit_of(a, s, 0);
+
+  // step (c, j): channels 64 c + 32 (g/2) + 16 j + 8 (g%2) on
+  u32x4_t q[DIM / 64][2];
+  {
+    const uint16_t* from = a.Q + (int64_t)(s.first + tok) * a.ldq + (int64_t)head * DIM + 32 * (g >> 1) + 8 * (g & 1);
+    uint32_t m = 0;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      sum += s_o[w][d][rr];
-      l += s_l[w][rr] * __builtin_amdgcn_exp2f(s_m[w][rr] - mm);
-    }
-    const int64_t token = s.first + (r0 + rr) / a.G;
-    const int hd = s.h * a.G + (r0 + rr) % a.G;
-    if (a.splits > 1) {
-      const int64_t at = ((int64_t)split * a.rows + token) * a.Hq + hd;
-      a.part[at * DIM + d] = sum;
-      if (d == 0) {
-        float* ml = a.part + (int64_t)a.splits * a.rows * a.Hq * DIM + at * 2;
-        ml[0] = mm;
-        ml[1] = l;
+    for (int c = 0; c < DIM / 64; ++c)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        q[c][j] = *reinterpret_cast<const u32x4_t*>(from + 64 * c + 16 * j);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) m = max_bf16x2(m, q[c][j][k] & 0x7FFF7FFFu);
       }
-    } else {
-      a.O[token * a.ldo + (int64_t)hd * DIM + d] = f32_to_bf16(l != 0.0f ? sum / l : 0.0f);
-      if (a.lse && d == 0) a.lse[token * a.Hq + hd] = lse_of(a, mm, l);
+    // an infinity or NaN in the row makes all of it NaN (and so every score)
+    m = max_bf16x2(m, m >> 16) & 0xFFFFu;
+    const Words2 u = swap16(m, m);
+    m = u.a > u.b ? u.a : u.b;
+    const Words2 v = swap32(m, m);
+    if ((v.a > v.b ? v.a : v.b) >= kInfBits) {
+#pragma unroll
+      for (int c = 0; c < DIM / 64; ++c)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) q[c][j] = u32x4_t{0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu};
     }
   }
+  // Oᵀ: accumulator 4 u + 2 b + k has channels 64 u + 32 b + 2 (4 g + i) + k
+  f32x4_t o[DIM / 16];
+#pragma unroll
+  for (int j = 0; j < DIM / 16; ++j) o[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  float m = kNoMax, l = 0.0f;
+
+  const int64_t page_bytes = (int64_t)a.Hkv * kBytes, page_scales = (int64_t)a.Hkv * kScales;
+  const int64_t code_off = (int64_t)s.h * kBytes + lane * 16;
+  const uint8_t* ks_src = a.ks + (int64_t)s.h * kScales + lane * (DIM / 32);
+  // V's scales: word lane = [block of channels][t/4 %2][t/16][t/8 %2], in LDS the last two in the other order
+  const int word = lane % (DIM / 2);
+  const uint8_t* vs_src = a.vs + (int64_t)s.h * kScales + 4 * word;
+  uint32_t* const vs_put = &s_vs[wave][(word & ~7) + 4 * (word & 1) + ((word >> 1) & 3)];
+  const uint32_t* const vs_get = &s_vs[wave][8 * (g & 1) + 4 * (g >> 1)];
+  bool dirty = false;
+  for (int g0 = p0 + wave; g0 < p1; g0 += 64 * WAVES) {
+    // lane l: logical page g0 + WAVES·l
+    const int meta = page_id(a, s, g0 + WAVES * lane, p1);
+    u32x4_t kr[kFrags], vr[kFrags];
+    uint32_t ksr, vsr;
+    auto load_k = [&](int page) {
+      page = page < 0 ? 0 : page;
+#pragma unroll
+      for (int f = 0; f < kFrags; ++f) kr[f] = load_nt(a.kc + page * page_bytes + code_off + f * 1024);
+      const uint8_t* p = ks_src + page * page_scales;
+      ksr = DIM == 128 ? *reinterpret_cast<const uint32_t*>(p) : *reinterpret_cast<const uint16_t*>(p);
+    };
+    auto load_v = [&](int page) {
+      page = page < 0 ? 0 : page;
+#pragma unroll
+      for (int f = 0; f < kFrags; ++f) vr[f] = load_nt(a.vc + page * page_bytes + code_off + f * 1024);
+      vsr = *reinterpret_cast<const uint32_t*>(vs_src + page * page_scales);
+    };
+    const int count = (p1 - g0 + WAVES - 1) / WAVES < 64 ? (p1 - g0 + WAVES - 1) / WAVES : 64;
+    load_k(__builtin_amdgcn_readfirstlane(meta));
+    load_v(__builtin_amdgcn_readfirstlane(meta));
+    for (int d = 0; d < count; ++d) {
+      const int page = __builtin_amdgcn_readlane(meta, d);
+      const int next = __builtin_amdgcn_readlane(meta, d + 1 < count ? d + 1 : d);
+      const int t0 = (g0 + WAVES * d) * kPage;
+      // z[t]: tokens 16 t + 4 g + i
+      f32x4_t z[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) z[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      const Words2 sk = swap16(ksr, ksr);
+#pragma unroll
+      for (int f = 0; f < kFrags; ++f) {
+        const int tb = f / (DIM / 64), c = f % (DIM / 64);
+        const float s0 = scale4(sk.a, f), s1 = scale4(sk.b, f);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const Words2 w = swap16(kr[f][2 * j], kr[f][2 * j + 1]);
+          const bf16x8_t x = __builtin_bit_cast(bf16x8_t, q[c][j]);
+          z[2 * tb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8(w.a, s0), x, z[2 * tb], 0, 0, 0);
+          z[2 * tb + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8(w.b, s1), x, z[2 * tb + 1], 0, 0, 0);
+        }
+      }
+      load_k(next);
+      *vs_put = vsr;
+      __builtin_amdgcn_wave_barrier();   // (LDS keeps a wave's order)
+      const bool part = page < 0 || t0 > lim_first - kPage;
+      if (part) {
+        asm volatile("");   // (a branch, not 32 instructions on every page)
+        const int lr = page >= 0 ? lim_row - t0 : 0;
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (16 * t + 4 * g + i >= lr) z[t][i] = -__builtin_inff();
+      }
+      float top = fmaxf(z[0][0], z[0][1]);
+#pragma unroll
+      for (int i = 2; i < 16; i += 2) top = fmaxf(fmaxf(top, z[i >> 2][i & 3]), z[i >> 2][(i & 3) + 1]);
+      top = row_largest(top) * a.c;
+      if (__builtin_amdgcn_ballot_w64(top > m + kRaise) != 0) {
+        const float up = fmaxf(m, top), f = __builtin_amdgcn_exp2f(m - up);
+#pragma unroll
+        for (int j = 0; j < DIM / 16; ++j) o[j] *= f;
+        l *= f;
+        m = up;
+      }
+      u32x4_t p[2];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(z[j >> 1][2 * (j & 1)], a.c, -m));
+        const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(z[j >> 1][2 * (j & 1) + 1], a.c, -m));
+        l += x + y;
+        p[j >> 2][j & 3] = pack_bf16x2(x, y);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      const int lk = page < 0 ? 0 : s.kv - t0 > kPage ? kPage : s.kv - t0;
+#pragma unroll
+      for (int u = 0; u < DIM / 64; ++u) {
+        // w[b][t]: tokens 16 t + 4 g on at channels 64 u + 32 b + 2 n, + 1
+        uint32_t w[2][4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const u32x4_t& v = vr[2 * u + (t >> 1)];
+          const Words2 x = swap32(v[2 * (t & 1)], v[2 * (t & 1) + 1]), y = swap16(x.a, x.b);
+          w[0][t] = y.a;
+          w[1][t] = y.b;
+        }
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          u32x4_t sv = *reinterpret_cast<const u32x4_t*>(vs_get + 16 * (2 * u + b));
+          if (part) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+              uint32_t sc = sv[t];
+              drop_slots(w[b][t], sc, 16 * t + 4 * g, lk);
+              if (a.causal) clear_nan(w[b][t], sc, dirty);
+              sv[t] = sc;
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            uint32_t e0[2], o0[2], e1[2], o1[2];
+            widen_pairs(w[b][2 * k], sv[2 * k], e0, o0);
+            widen_pairs(w[b][2 * k + 1], sv[2 * k + 1], e1, o1);
+            const bf16x8_t weight = __builtin_bit_cast(bf16x8_t, p[k]);
+            const int at = 2 * (2 * u + b);
+            o[at] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                __builtin_bit_cast(bf16x8_t, u32x4_t{e0[0], e0[1], e1[0], e1[1]}), weight, o[at], 0, 0, 0);
+            o[at + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                __builtin_bit_cast(bf16x8_t, u32x4_t{o0[0], o0[1], o1[0], o1[1]}), weight, o[at + 1], 0, 0, 0);
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      load_v(next);
+    }
+  }
+  if (dirty) {
+    const int whole = lim_first / kPage;
+    const uint32_t bad = nan_blocks<DIM>(a, s, p0 > whole ? p0 : whole, p1, lim_row);
+#pragma unroll
+    for (int j = 0; j < DIM / 16; ++j)
+      if ((bad >> (j / 2)) & 1) o[j] = o[j] * __builtin_nanf("");
+  }
+  // join the waves
+  l += __shfl_xor(l, 16);
+  l += __shfl_xor(l, 32);
+  if (g == 0) {
+    s_m[wave][n] = m;
+    s_l[wave][n] = l;
+  }
+  __syncthreads();
+  float most = s_m[0][n];
+#pragma unroll
+  for (int w = 1; w < WAVES; ++w) most = fmaxf(most, s_m[w][n]);
+  const float f = __builtin_amdgcn_exp2f(m - most);
+#pragma unroll
+  for (int j = 0; j < DIM / 16; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s_o[wave][32 * (j >> 1) + 2 * (4 * g + i) + (j & 1)][n] = o[j][i] * f;
+  __syncthreads();
+  for (int at = threadIdx.x; at < R * DIM; at += 64 * WAVES)
+    store_joined<DIM, kLeastRows + 1, WAVES>(a, s, s_o, s_m, s_l, at, 0, split);
 }
 
 }  // namespace
+
+// Up to 16 rows of a key head: blocks of eight waves for at most one a CU, the pages of the longest sequence
+// split where that leaves some idle (a second block a CU takes longer: 32 ragged sequences of up to 8191
+// tokens, 8 key heads of 128, 58 us for 47), blocks of four, three a CU, beyond (64 sequences of 4096 tokens,
+// 16 heads of 64, 57 us for 71; the other way round 32 ragged ones 56 for 47).  At least eight pages a
+// block: one for each wave.  More rows: as for the 8-bit cache.
+static AttnPlan attn4_plan(int64_t G, int64_t Hkv, int64_t dim, int64_t rows, int64_t B, int64_t max_q,
+                           int64_t max_kv) {
+  constexpr int64_t kCus = 256, kLeast = 8;
+  if (max_q * G > kLeastRows) return attn_plan(G, Hkv, dim, rows, B, max_q, max_kv);
+  const int64_t pages = (max_kv + kPage - 1) / kPage;
+  int64_t splits = kCus / (B * Hkv);
+  if (splits > pages / kLeast) splits = pages / kLeast;
+  return AttnPlan{true, 1, splits > 1 ? splits : 1, (int)kLeast};
+}
+
+int64_t attn4_workspace_bytes(int64_t rows, int64_t Hq, int64_t Hkv, int64_t dim, int64_t B,
+                              int64_t max_q, int64_t max_kv) {
+  const AttnPlan p = attn4_plan(Hq / Hkv, Hkv, dim, rows, B, max_q, max_kv);
+  return p.splits > 1 ? p.splits * rows * Hq * (dim + 2) * 4 : 0;
+}
+
+int64_t attn4_blocks(int64_t rows, int64_t Hq, int64_t Hkv, int64_t dim, int64_t B, int64_t max_q,
+                     int64_t max_kv) {
+  const AttnPlan p = attn4_plan(Hq / Hkv, Hkv, dim, rows, B, max_q, max_kv);
+  return B * Hkv * p.tiles * p.splits + 8;
+}
 
 hipError_t launch_attn4(const uint16_t* Q, int64_t ldq, int64_t rows, int64_t Hq, int64_t Hkv,
                         int64_t dim, const int32_t* cu, const int32_t* len, int64_t B,
@@ -548,12 +830,24 @@ hipError_t launch_attn4(const uint16_t* Q, int64_t ldq, int64_t rows, int64_t Hq
                         int64_t n_pages, const uint8_t* kc, const uint8_t* vc, const uint8_t* ks,
                         const uint8_t* vs, float scale, int causal, uint16_t* O, int64_t ldo,
                         float* lse, void* workspace, hipStream_t s) {
-  const AttnPlan p = attn_plan(Hq / Hkv, Hkv, dim, rows, B, max_q, max_kv);
+  const AttnPlan p = attn4_plan(Hq / Hkv, Hkv, dim, rows, B, max_q, max_kv);
   const AttnArgs a = attn_args(Q, ldq, rows, Hq, Hkv, cu, len, B, max_q, table, max_blocks, n_pages,
                                kc, vc, ks, vs, scale, causal, O, ldo, lse, workspace, p, 1.0f);
   const int64_t items = B * Hkv * p.tiles * p.splits;
   const unsigned grid = (unsigned)((items + 7) / 8 * 8);
-  if (p.few && p.tiles > 1) {
+  if (p.chunk > 0) {
+    if (items > 256) {
+      if (dim == 64)
+        k_attn4_row16<64, 4><<<(unsigned)items, 256, 0, s>>>(a);
+      else
+        k_attn4_row16<128, 4><<<(unsigned)items, 256, 0, s>>>(a);
+    } else {
+      if (dim == 64)
+        k_attn4_row16<64, 8><<<(unsigned)items, 512, 0, s>>>(a);
+      else
+        k_attn4_row16<128, 8><<<(unsigned)items, 512, 0, s>>>(a);
+    }
+  } else if (p.few && p.tiles > 1) {
     if (dim == 64)
       k_attn4_few<64, true><<<grid, 256, 0, s>>>(a);
     else

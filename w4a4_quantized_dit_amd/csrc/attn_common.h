@@ -29,6 +29,7 @@ struct AttnArgs {
   float c;
   float to_ln, to_ln_lo;  // scale / c, in two parts: c is rounded, and lse in units of scale
   float up;               // O's sums are brought back by this
+  int chunk;              // > 0: a split takes attn_chunk() pages, at least so many; 0: they share them evenly
 };
 
 // One sequence and key head of a block.  Tokens, rows and pages fit 32 bits (lengths are int32,
@@ -59,6 +60,25 @@ __device__ __forceinline__ int limit_of(const AttnArgs& a, const Seq& s, int i) 
   if (!a.causal) return s.kv;
   const int v = s.kv - s.n + i + 1;
   return v < 0 ? 0 : v;
+}
+
+// Pages of a split: the longest sequence's shared by the splits.  Shorter sequences have fewer splits, of
+// the same length, so that the blocks end together; lengths that the host only bounds are shared all the same.
+__device__ __forceinline__ int attn_chunk(const AttnArgs& a) {
+  int most = 0;
+  for (int i = threadIdx.x & 63; i < a.B; i += 64) {
+    const int n = a.len[i];
+    most = n > most ? n : most;
+  }
+#pragma unroll
+  for (int k = 1; k < 64; k *= 2) {
+    const int n = __shfl_xor(most, k);
+    most = n > most ? n : most;
+  }
+  int64_t pages = ((int64_t)most + kPage - 1) / kPage;
+  if (pages > a.max_blocks) pages = a.max_blocks;
+  const int each = (int)((pages + a.splits - 1) / a.splits);
+  return each > a.chunk ? each : a.chunk;
 }
 
 // A lane's part of its row's query: channels 64s + 32·half + 8j .. + 7, the operand of step j of the
@@ -204,6 +224,7 @@ constexpr int64_t kFewMost = 512;  // of a key head, in blocks of so many (measu
 struct AttnPlan {
   bool few;
   int64_t tiles, splits;
+  int chunk;   // AttnArgs::chunk
 };
 
 AttnPlan attn_plan(int64_t G, int64_t Hkv, int64_t dim, int64_t rows, int64_t B, int64_t max_q,

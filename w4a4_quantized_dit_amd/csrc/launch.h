@@ -185,6 +185,10 @@ hipError_t launch_kv4_read(uint16_t* K, int64_t ldk, uint16_t* V, int64_t ldv, i
                            const uint8_t* ks, const uint8_t* vs, hipStream_t s);
 
 // Attention over it; workspace and blocks as for the 8-bit cache.
+int64_t attn4_workspace_bytes(int64_t rows, int64_t Hq, int64_t Hkv, int64_t dim, int64_t B,
+                              int64_t max_q, int64_t max_kv);
+int64_t attn4_blocks(int64_t rows, int64_t Hq, int64_t Hkv, int64_t dim, int64_t B, int64_t max_q,
+                     int64_t max_kv);
 hipError_t launch_attn4(const uint16_t* Q, int64_t ldq, int64_t rows, int64_t Hq, int64_t Hkv,
                         int64_t dim, const int32_t* cu, const int32_t* len, int64_t B,
                         int64_t max_q, int64_t max_kv, const int32_t* table, int64_t max_blocks,
