@@ -209,3 +209,78 @@ def test_workspace_of_the_caller(L):
     assert torch.equal(got, want)
     assert torch.all(buf[:off] == 0xA5) and torch.all(buf[off + n:] == 0xA5)
     assert L.gemv_workspace(20, pw).numel() == n
+
+
+def test_rows_far_apart(L):
+    """The largest leading dimension: the last row starts two gigabytes behind the first."""
+    torch = torch_mod()
+    rng = np.random.default_rng(14)
+    N, K, ld = 24, 512, 1 << 24
+    wt, lam, down, up = case(rng, "nvfp4", N, K, 8)
+    pw = device_weight(L, "nvfp4", wt, up, N, K, 8)
+    X = dev_bf16(bf16_rne(rng.standard_normal((64, K)).astype(np.float32)))
+    wide = torch.empty(64, ld, dtype=torch.bfloat16, device="cuda")[:, :K]
+    wide.copy_(X)
+    a, b = L.gemv(wide, pw, dev(lam), dev_bf16(down)), L.gemv(X, pw, dev(lam), dev_bf16(down))
+    torch.cuda.synchronize()
+    assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_the_longest_rows(L, fmt):
+    """K of 2^22: units in a few channels from the first to the last, in a row each and all in one; every
+    partial sum is of at most nine values, and the factors' sums of units are exact."""
+    torch = torch_mod()
+    rng = np.random.default_rng(15)
+    N, K, r, M = 17, 1 << 22, 128, 10
+    at = np.array([0, 255, 256, 4097, 1 << 20, (1 << 21) + 77, 3 << 20, K - 257, K - 1])
+    block = dict(nvfp4=16, int4=64, mxfp4=32)[fmt]
+    codes = rng.integers(0, 256, (N, K // 2)).astype(np.uint8)
+    if fmt == "int4":
+        scales = (2.0 ** rng.integers(-9, 3, (N, K // block))).astype(np.float16)
+    else:
+        scales = rng.integers(0x30, 0x48, (N, K // block)).astype(np.uint8) + np.uint8(80 if fmt == "mxfp4" else 0)
+    g = np.float32(0.5) if fmt == "nvfp4" else None
+    down = np.zeros((r, K), np.float32)
+    down[:, at] = rng.integers(-8, 9, (r, len(at)))
+    up = rng.integers(-2, 3, (N, r)).astype(np.float32) / 64
+    w = np.stack([OT.weight_values(codes[:, c // 256 * 128:c // 256 * 128 + 128],
+                                   scales[:, c // 256 * (256 // block):(c // 256 + 1) * (256 // block)],
+                                   g, fmt)[:, c % 256] for c in at], 1)
+    x = np.zeros((M, len(at)))
+    x[:len(at)] = np.eye(len(at))
+    x[-1] = 1.0
+    X = torch.zeros(M, K, dtype=torch.bfloat16, device="cuda")
+    X[:, torch.as_tensor(at)] = torch.as_tensor(x, dtype=torch.bfloat16, device="cuda")
+    code = dict(nvfp4=L.NVFP4, int4=L.INT4_G64, mxfp4=L.MXFP4)[fmt]
+    pw = L.PreparedWeight(code, N, K, r, dev(codes), dev(scales), dev(np.array([g])) if g else None,
+                          dev_bf16(bf16_rne(up)))
+    Y = L.gemv(X, pw, None, dev_bf16(bf16_rne(down)))
+    torch.cuda.synchronize()
+    D = x @ down[:, at].T.astype(np.float64)
+    y, a = x @ w.T + D @ up.T.astype(np.float64), np.abs(x) @ np.abs(w.T) + np.abs(D) @ np.abs(up.T)
+    # half a bf16 step, and 9 + 128 additions and the tensor's scale in fp32
+    assert np.all(np.abs(Y.float().cpu().numpy() - y) <= 2.0 ** -8 * np.abs(y) + 140 * 2.0 ** -23 * a)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_small_channels_beside_a_large_one(L, fmt):
+    """A channel that the weight ignores beside one up to 2^40 times smaller: NVFP4 and int4 take x̂ in
+    fp16 with the largest of 256 channels in [2^14, 2^15), off by less than 2^-24 there, 2^-38 of it."""
+    torch = torch_mod()
+    rng = np.random.default_rng(16)
+    N, K = 40, 512
+    wt, _, _, _ = case(rng, fmt, N, K, 0, False)
+    wt["codes"][:, 0] &= 0xF0   # channel 0 in the low nibble
+    pw = device_weight(L, fmt, wt, None, N, K, 0)
+    w = OT.weight_values(wt["codes"], wt["scales"], wt["g"], fmt)
+    assert np.all(w[:, 0] == 0)
+    v = 1.9921875 * 2.0 ** -np.arange(0, 41)
+    X = np.zeros((41, K), np.float32)
+    X[:, 0], X[:, 201] = 1.5, v
+    Y = L.gemv(dev_bf16(bf16_rne(X)), pw, None, None)
+    torch.cuda.synchronize()
+    y = v[:, None] * w[:, 201]
+    exact = 2.0 ** -8 * np.abs(y) * (1 + 2.0 ** -15)
+    lost = 0.0 if fmt == "mxfp4" else np.where(v[:, None] < 2.0 ** -29, 2.0 ** -37 * np.abs(w[:, 201]), 0.0)
+    assert np.all(np.abs(Y.float().cpu().numpy() - y) <= exact + lost)

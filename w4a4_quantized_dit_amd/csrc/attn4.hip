@@ -134,6 +134,8 @@ __device__ __forceinline__ void store_row(const AttnArgs& a, const State<DIM>& s
 // Many rows: the schedule of the 8-bit cache's kernel.  Four waves of 32 rows share each page through
 // LDS, where it lies widened: each wave widens a quarter of K and of V on the way, V's codes loaded two
 // pages ahead and K's three.  Two images of each, one barrier a page.
+// Bound as there, by the power and the vector unit: 16384 rows over 16384 tokens, 40 heads of 128, 4.6 to 4.8 ms,
+// 1.16 PFLOP/s; two causal streams of 4001 and 2854 rows, 32 heads on 8 of 64, 161 us.
 template <int DIM>
 __global__ __launch_bounds__(64 * kTileWaves, 2) void k_attn4_tile(AttnArgs a) {
   constexpr int kBytes = kPage * DIM / 2, kScales = 2 * DIM;  // one tensor's page
