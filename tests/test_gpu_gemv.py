@@ -284,3 +284,25 @@ def test_small_channels_beside_a_large_one(L, fmt):
     exact = 2.0 ** -8 * np.abs(y) * (1 + 2.0 ** -15)
     lost = 0.0 if fmt == "mxfp4" else np.where(v[:, None] < 2.0 ** -29, 2.0 ** -37 * np.abs(w[:, 201]), 0.0)
     assert np.all(np.abs(Y.float().cpu().numpy() - y) <= exact + lost)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("K", [256, 768, 1024])
+@pytest.mark.parametrize("M", [1, 40])
+def test_scales_that_are_no_numbers_stay_in_their_output(L, fmt, K, M):
+    """Channels end inside a chunk of four pieces: the next row's scales lie where the load goes on.
+    (NVFP4's are at most 0x7E, 448, as the library makes them; 0x7F counts on as 480 in this layer.)"""
+    torch = torch_mod()
+    rng = np.random.default_rng(17)
+    N = 21
+    wt, _, _, _ = case(rng, fmt, N, K, 0, False)
+    X = dev_bf16(bf16_rne(rng.standard_normal((M, K)).astype(np.float32)))
+    want = L.gemv(X, device_weight(L, fmt, wt, None, N, K, 0), None, None)
+    bad = [1, 6, 16, 20]
+    wt["scales"] = wt["scales"].copy()
+    wt["scales"][bad] = np.float16(np.nan) if fmt == "int4" else 0x7F if fmt == "nvfp4" else 0xFF
+    got = L.gemv(X, device_weight(L, fmt, wt, None, N, K, 0), None, None)
+    torch.cuda.synchronize()
+    good = [n for n in range(N) if n not in bad]
+    assert torch.isnan(got[:, bad]).all() or fmt == "nvfp4"
+    assert torch.equal(got[:, good], want[:, good])
