@@ -568,8 +568,8 @@ __global__ __launch_bounds__(256, 2) void k_attn4_few(AttnArgs a) {
 // four tokens 4·g on at channels 2·n, 2·n + 1 of 32.  V's scales come as a word a lane and pass through LDS.
 //
 // Bound by the vector instructions, 460 a page, which take a SIMD 0.9 us (a lone block of four waves or of
-// eight walks 64 pages in 15 us): 32 sequences of 8191 tokens, 8 key heads of 128 with 5 rows each, 50.6 us,
-// 5.6 TB/s (with the 32 rows' kernel 54.6), ragged ones 47.4 (53.7).
+// eight walks 64 pages in 15 us): 32 sequences of 8191 tokens, 8 key heads of 128 with 5 rows each, 50.2 us,
+// 5.7 TB/s (with the 32 rows' kernel 54.6), ragged ones 45.5 (53.7).
 constexpr int kLeastRows = 16;
 
 struct Words2 {
@@ -597,11 +597,19 @@ __global__ __launch_bounds__(64 * WAVES, 3) void k_attn4_row16(AttnArgs a) {
   __shared__ float s_o[WAVES][DIM][kLeastRows + 1];
   __shared__ float s_m[WAVES][kLeastRows], s_l[WAVES][kLeastRows];
   __shared__ __attribute__((aligned(16))) uint32_t s_vs[WAVES][DIM / 2];
-  const int split = (int)(blockIdx.x % a.splits);
-  Seq s;
-  if (!sequence(a, (int)(blockIdx.x / a.splits), s)) return;
-  const int R = s.q * a.G;
+  const int split = (int)(blockIdx.x % a.splits), bh = (int)(blockIdx.x / a.splits);
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4, n = lane & 15;
+  // lane l: table entry of the logical page at + WAVES·l (past the table the last), the page if it exists
+  auto look_up = [&](int at) {
+    const int64_t i = (int64_t)at + WAVES * lane;
+    return a.table[(int64_t)(bh / a.Hkv) * a.max_blocks + (i < a.max_blocks ? i : a.max_blocks - 1)];
+  };
+  auto existing = [&](int page) { return page < a.n_pages ? page : -1; };
+  // (asked for beside the lengths, for the case that nothing is split: a block starts with a chain of loads)
+  int meta = look_up(wave);
+  Seq s;
+  if (!sequence(a, bh, s)) return;
+  const int R = s.q * a.G;
   const bool live = n < R;
   const int tok = (live ? n : 0) / a.G;
   const int head = s.h * a.G + (live ? n : 0) % a.G;
@@ -615,29 +623,7 @@ __global__ __launch_bounds__(64 * WAVES, 3) void k_attn4_row16(AttnArgs a) {
 
   // step (c, j): channels 64 c + 32 (g/2) + 16 j + 8 (g%2) on
   u32x4_t q[DIM / 64][2];
-  {
-    const uint16_t* from = a.Q + (int64_t)(s.first + tok) * a.ldq + (int64_t)head * DIM + 32 * (g >> 1) + 8 * (g & 1);
-    uint32_t m = 0;
-#pragma unroll
-    for (int c = 0; c < DIM / 64; ++c)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        q[c][j] = *reinterpret_cast<const u32x4_t*>(from + 64 * c + 16 * j);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) m = max_bf16x2(m, q[c][j][k] & 0x7FFF7FFFu);
-      }
-    // an infinity or NaN in the row makes all of it NaN (and so every score)
-    m = max_bf16x2(m, m >> 16) & 0xFFFFu;
-    const Words2 u = swap16(m, m);
-    m = u.a > u.b ? u.a : u.b;
-    const Words2 v = swap32(m, m);
-    if ((v.a > v.b ? v.a : v.b) >= kInfBits) {
-#pragma unroll
-      for (int c = 0; c < DIM / 64; ++c)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) q[c][j] = u32x4_t{0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu};
-    }
-  }
+  const uint16_t* const q_row = a.Q + (int64_t)(s.first + tok) * a.ldq + (int64_t)head * DIM + 32 * (g >> 1) + 8 * (g & 1);
   // Oᵀ: accumulator 4 u + 2 b + k has channels 64 u + 32 b + 2 (4 g + i) + k
   f32x4_t o[DIM / 16];
 #pragma unroll
@@ -653,27 +639,52 @@ __global__ __launch_bounds__(64 * WAVES, 3) void k_attn4_row16(AttnArgs a) {
   uint32_t* const vs_put = &s_vs[wave][(word & ~7) + 4 * (word & 1) + ((word >> 1) & 3)];
   const uint32_t* const vs_get = &s_vs[wave][8 * (g & 1) + 4 * (g >> 1)];
   bool dirty = false;
-  for (int g0 = p0 + wave; g0 < p1; g0 += 64 * WAVES) {
-    // lane l: logical page g0 + WAVES·l
-    const int meta = page_id(a, s, g0 + WAVES * lane, p1);
-    u32x4_t kr[kFrags], vr[kFrags];
-    uint32_t ksr, vsr;
-    auto load_k = [&](int page) {
-      page = page < 0 ? 0 : page;
+  u32x4_t kr[kFrags], vr[kFrags];
+  uint32_t ksr = 0, vsr = 0;
+  auto load_k = [&](int page) {
+    page = page < 0 ? 0 : page;
 #pragma unroll
-      for (int f = 0; f < kFrags; ++f) kr[f] = load_nt(a.kc + page * page_bytes + code_off + f * 1024);
-      const uint8_t* p = ks_src + page * page_scales;
-      ksr = DIM == 128 ? *reinterpret_cast<const uint32_t*>(p) : *reinterpret_cast<const uint16_t*>(p);
-    };
-    auto load_v = [&](int page) {
-      page = page < 0 ? 0 : page;
+    for (int f = 0; f < kFrags; ++f) kr[f] = load_nt(a.kc + page * page_bytes + code_off + f * 1024);
+    const uint8_t* p = ks_src + page * page_scales;
+    ksr = DIM == 128 ? *reinterpret_cast<const uint32_t*>(p) : *reinterpret_cast<const uint16_t*>(p);
+  };
+  auto load_v = [&](int page) {
+    page = page < 0 ? 0 : page;
 #pragma unroll
-      for (int f = 0; f < kFrags; ++f) vr[f] = load_nt(a.vc + page * page_bytes + code_off + f * 1024);
-      vsr = *reinterpret_cast<const uint32_t*>(vs_src + page * page_scales);
-    };
+    for (int f = 0; f < kFrags; ++f) vr[f] = load_nt(a.vc + page * page_bytes + code_off + f * 1024);
+    vsr = *reinterpret_cast<const uint32_t*>(vs_src + page * page_scales);
+  };
+  int g0 = p0 + wave;
+  // (a wave without pages too: the counts of loads under way stay known)
+  meta = existing(a.splits > 1 ? look_up(g0) : meta);
+  load_k(__builtin_amdgcn_readfirstlane(meta));
+#pragma unroll
+  for (int c = 0; c < DIM / 64; ++c)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) q[c][j] = *reinterpret_cast<const u32x4_t*>(q_row + 64 * c + 16 * j);
+  load_v(__builtin_amdgcn_readfirstlane(meta));
+  {
+    // an infinity or NaN in the row makes all of it NaN (and so every score)
+    uint32_t most = 0;
+#pragma unroll
+    for (int c = 0; c < DIM / 64; ++c)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) most = max_bf16x2(most, q[c][j][k] & 0x7FFF7FFFu);
+    most = max_bf16x2(most, most >> 16) & 0xFFFFu;
+    const Words2 u = swap16(most, most);
+    most = u.a > u.b ? u.a : u.b;
+    const Words2 v = swap32(most, most);
+    if ((v.a > v.b ? v.a : v.b) >= kInfBits) {
+#pragma unroll
+      for (int c = 0; c < DIM / 64; ++c)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) q[c][j] = u32x4_t{0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu};
+    }
+  }
+  for (; g0 < p1; g0 += 64 * WAVES) {
     const int count = (p1 - g0 + WAVES - 1) / WAVES < 64 ? (p1 - g0 + WAVES - 1) / WAVES : 64;
-    load_k(__builtin_amdgcn_readfirstlane(meta));
-    load_v(__builtin_amdgcn_readfirstlane(meta));
     for (int d = 0; d < count; ++d) {
       const int page = __builtin_amdgcn_readlane(meta, d);
       const int next = __builtin_amdgcn_readlane(meta, d + 1 < count ? d + 1 : d);
@@ -769,6 +780,11 @@ __global__ __launch_bounds__(64 * WAVES, 3) void k_attn4_row16(AttnArgs a) {
       }
       load_v(next);
     }
+    if (g0 + 64 * WAVES < p1) {
+      meta = existing(look_up(g0 + 64 * WAVES));
+      load_k(__builtin_amdgcn_readfirstlane(meta));
+      load_v(__builtin_amdgcn_readfirstlane(meta));
+    }
   }
   if (dirty) {
     const int whole = lim_first / kPage;
@@ -804,14 +820,16 @@ __global__ __launch_bounds__(64 * WAVES, 3) void k_attn4_row16(AttnArgs a) {
 // split where that leaves some idle (a second block a CU takes longer: 32 ragged sequences of up to 8191
 // tokens, 8 key heads of 128, 58 us for 47), blocks of four, three a CU, beyond (64 sequences of 4096 tokens,
 // 16 heads of 64, 57 us for 71; the other way round 32 ragged ones 56 for 47).  At least eight pages a
-// block: one for each wave.  More rows: as for the 8-bit cache.
+// block, one for each wave, and none split below 24: the join is a launch (one head over 16 pages 10.7 us in two
+// splits and 9.5 in one, over 32 11.5 in four and 13.4).  More rows: as for the 8-bit cache.
 static AttnPlan attn4_plan(int64_t G, int64_t Hkv, int64_t dim, int64_t rows, int64_t B, int64_t max_q,
                            int64_t max_kv) {
-  constexpr int64_t kCus = 256, kLeast = 8;
+  constexpr int64_t kCus = 256, kLeast = 8, kLeastSplit = 24;
   if (max_q * G > kLeastRows) return attn_plan(G, Hkv, dim, rows, B, max_q, max_kv);
   const int64_t pages = (max_kv + kPage - 1) / kPage;
   int64_t splits = kCus / (B * Hkv);
   if (splits > pages / kLeast) splits = pages / kLeast;
+  if (pages < kLeastSplit) splits = 1;
   return AttnPlan{true, 1, splits > 1 ? splits : 1, (int)kLeast};
 }
 

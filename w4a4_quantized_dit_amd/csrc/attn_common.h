@@ -46,10 +46,10 @@ __device__ __forceinline__ bool sequence(const AttnArgs& a, int bh, Seq& s) {
   s.h = bh % a.Hkv;
   s.first = a.cu[s.b];
   const int end = a.cu[s.b + 1];
+  s.kv = a.len[s.b];   // (asked for with them)
   if (s.first < 0 || end <= s.first || end > a.rows) return false;
   s.n = end - s.first;
   s.q = s.n < a.max_q ? s.n : a.max_q;
-  s.kv = a.len[s.b];
   const int64_t room = a.max_blocks * kPage;
   s.kv = s.kv < 0 ? 0 : (s.kv > room ? (int)room : s.kv);
   return true;
