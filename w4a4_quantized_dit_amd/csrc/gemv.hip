@@ -11,7 +11,9 @@
 // code times an E4M3 scale has six significant bits and lies in fp16's range, int4 codes go without their
 // scale, which multiplies the sum of a group's 64 products.  x̂ then is an fp16 too: its rows are
 // scaled by a power of two for every 256 channels so that the largest lies below 2^15, and the sums of
-// those are scaled back; what is 2^29 times smaller than the largest of its 256 loses bits of its eight.
+// those are scaled back; what is 2^29 times smaller than the largest of its 256 loses bits of its eight.  NVFP4's
+// tensor scale g is about 2^-16 of the weight, and sums without it would pass fp32's range long before the result:
+// they are scaled back with g's power of two, exactly, and the join multiplies by the rest of g, in [1, 2).
 //
 // Measured (both kernels, graphs): one row of 5120x5120 NVFP4, rank 32, 14.2 us, five of 5120x13824 MXFP4, rank
 // 128, 19.4 (without it 14.8, 2.5 TB/s), 32 of 13824x5120 int4, rank 32, 28, where widening the codes and forming
@@ -117,13 +119,16 @@ struct GemvArgs {
   int down_parts, down_each;
 };
 
+// The power of two of the tensor's scale (any number for zero, infinity and NaN, which stay what they are).
+__device__ __forceinline__ int exponent_of(float g) { return __builtin_amdgcn_frexp_expf(g) - 1; }
+
 // Bytes of a row of x̂ in LDS, CH pieces: rows start in banks of their own.
 template <int CH>
 constexpr int kRowBytes = CH * kPiece * 2 + 16;
 
 // x̂ of a chunk of CH pieces on its way into LDS: a thread brings eight channels of every kStep-th row.
-// NVFP4 and int4: as fp16 with a power of two for each row and pair of pieces, which goes to s_back; int4's
-// order of the channels.
+// NVFP4 and int4: as fp16 with a power of two for each row and pair of pieces, of which the exponent of the way
+// back goes to s_back (with g's, g_exp); int4's order of the channels.
 template <int FMT, int MT, int CH, int SETS, bool SMOOTH>
 struct Activations {
   static constexpr bool kHalf = FMT == kFmtNv || FMT == kFmtInt4;
@@ -164,7 +169,7 @@ struct Activations {
     return max_bf16x2(m, m >> 16) & 0xFFFFu;
   }
   // (rows past M and channels past the last piece become zeros)
-  __device__ __forceinline__ void store(int p, int set, uint8_t* buf, float* s_back) {
+  __device__ __forceinline__ void store(int p, int set, uint8_t* buf, int* s_back, int g_exp) {
     float inv[8];
     if (SMOOTH) {
       const bool there = p * kPiece + 8 * col < last * kPiece;
@@ -188,7 +193,7 @@ struct Activations {
         const int f = 268 - (int)(top >> 7);
         const uint32_t field = top >= kInfBits ? 127u : (uint32_t)(f > 253 ? 253 : f);
         const float up = __uint_as_float(field << 23);
-        if (col % 32 == 0) s_back[col / 32 * (16 * MT) + row0 + kStep * i] = __uint_as_float((254u - field) << 23);
+        if (col % 32 == 0) s_back[col / 32 * (16 * MT) + row0 + kStep * i] = 127 - (int)field + g_exp;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const auto h = __builtin_amdgcn_cvt_pkrtz(bf16_lo(v[j]) * up, bf16_hi(v[j]) * up);
@@ -217,7 +222,7 @@ __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(
 // bound).  The scales of a row's chunk come in one lane and go to the others through LDS.
 template <int FMT, int MT, int CH, int AHEAD, bool SMOOTH>
 __device__ __forceinline__ void outputs(const GemvArgs& a, int n0, int first, int last, uint8_t* s_x,
-                                        float* s_back, uint8_t* s_scale, f32x4_t (&total)[MT]) {
+                                        int* s_back, uint8_t* s_scale, f32x4_t (&total)[MT]) {
   constexpr int kSets = AHEAD / CH, kScaleWords = scale_words(FMT), kWords = CH * kScaleWords;
   constexpr int kLanes = kWords > 4 ? kWords / 4 : 1;   // of a row's scales, 16 bytes each
   constexpr bool kHalf = FMT != kFmtMx;
@@ -257,12 +262,14 @@ __device__ __forceinline__ void outputs(const GemvArgs& a, int n0, int first, in
 #pragma unroll
     for (int d = 0; d < CH; ++d) load_w(first + k * CH + d, k * CH + d);
   }
+  // (behind the loads, which would wait for it)
+  const int g_exp = FMT == kFmtNv ? __builtin_amdgcn_readfirstlane(exponent_of(a.g[0])) : 0;
   const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
   f32x4_t acc[MT];   // of a pair of pieces
   auto chunk = [&](int p0, int set, int buffer) {
     uint8_t* buf = s_x + buffer * (16 * MT * kRowBytes<CH>);
-    float* back = s_back + buffer * (CH / 2 * 16 * MT);
-    x.store(p0, set, buf, back);
+    int* back = s_back + buffer * (CH / 2 * 16 * MT);
+    x.store(p0, set, buf, back, g_exp);
     if (kScaleWords == 1 && p0 + 2 >= last) sw[set][2] = sw[set][3] = 0u;  // (another row's, or nothing)
     if (lane < 16 * kLanes) *reinterpret_cast<u32x4_t*>(s_scale + 16 * lane) = sw[set];
     __builtin_amdgcn_sched_barrier(0);
@@ -328,9 +335,9 @@ __device__ __forceinline__ void outputs(const GemvArgs& a, int n0, int first, in
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
           if constexpr (kHalf) {
-            const f32x4_t f = *reinterpret_cast<const f32x4_t*>(back + (d / 2) * (16 * MT) + 16 * m + 4 * q);
+            const u32x4_t e = *reinterpret_cast<const u32x4_t*>(back + (d / 2) * (16 * MT) + 16 * m + 4 * q);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) total[m][j] = __builtin_fmaf(acc[m][j], f[j], total[m][j]);
+            for (int j = 0; j < 4; ++j) total[m][j] += __builtin_amdgcn_ldexpf(acc[m][j], (int)e[j]);
           } else {
             total[m] += acc[m];
           }
@@ -382,7 +389,7 @@ __device__ __forceinline__ void down_part(const GemvArgs& a, int part, uint8_t* 
   load(first);
   for (int p0 = first; p0 < last; p0 += CH) {
     if (p0 != first) lds_barrier();
-    x.store(p0, 0, s_x, nullptr);
+    x.store(p0, 0, s_x, nullptr, 0);
     x.load(a, p0 + CH, 0);
     lds_barrier();
 #pragma unroll
@@ -421,7 +428,7 @@ template <int FMT, int MT, int CH, bool SMOOTH>
 __global__ __launch_bounds__(64 * kWaves, 2) void k_gemv_part(GemvArgs a) {
   constexpr int kScaleBytes = 16 * 4 * (CH * scale_words(FMT) > 4 ? CH * scale_words(FMT) : 4);
   __shared__ __attribute__((aligned(16))) uint8_t s_x[2 * 16 * MT * kRowBytes<CH>], s_scale[kWaves * kScaleBytes];
-  __shared__ __attribute__((aligned(16))) float s_back[CH * 16 * MT];
+  __shared__ __attribute__((aligned(16))) int s_back[CH * 16 * MT];
   static_assert(sizeof(s_x) >= 8192 * MT, "the down factor's sums are joined in it");
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int block = (int)blockIdx.x - a.down_parts;
@@ -516,7 +523,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void k_gemv_join(GemvArgs a) {
       }
   }
   if (!mine) return;
-  const float g = a.g ? a.g[0] : 1.0f;
+  const float g = a.g ? __builtin_amdgcn_ldexpf(a.g[0], -exponent_of(a.g[0])) : 1.0f;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     if (4 * rq + i < a.M)
