@@ -454,14 +454,16 @@ __global__ __launch_bounds__(64 * kWaves, 2) void k_gemv_part(GemvArgs a) {
 }
 
 // The parts' sums and the up factor's product.  A wave has 16 outputs of 16 rows; D, which the block's
-// waves share, is taken to 16 bits in two bf16 (hi + lo), 32 ranks a wave.  Its time is a launch and the
+// waves share, is cut into three bf16 of eight bits each, 32 ranks a wave, so that its products are exact in
+// the fp32 sum (two would be 16 bits of it; the third takes no time that shows).  Its time is a launch and the
 // latency of loads, so all are on their way at once: eight parts of either, the ones past the last are
 // buffer loads without a request.  (With loops that end at the last part: one row of 5120x5120 NVFP4, rank
 // 32, 14.8 us for 14.3, five of 5120x13824 MXFP4, rank 128, 20.5 for 19.4, both kernels.)
 constexpr int kJoinWaves = 4;
 
 __global__ __launch_bounds__(64 * kJoinWaves) void k_gemv_join(GemvArgs a) {
-  __shared__ __attribute__((aligned(16))) u32x4_t s_d[kJoinWaves][2][64];
+  constexpr int kCuts = 3;   // of D
+  __shared__ __attribute__((aligned(16))) u32x4_t s_d[kJoinWaves][kCuts][64];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int n16 = lane & 15, q = lane >> 4;
   const int m0 = blockIdx.y * 16, n = (blockIdx.x * kJoinWaves + wave) * 16 + n16;
@@ -505,22 +507,26 @@ __global__ __launch_bounds__(64 * kJoinWaves) void k_gemv_join(GemvArgs a) {
     }
   }
   if (a.r) {
-    u32x4_t hi, lo;
+    // (cut off, not rounded: a number near fp32's largest stays one)
+    u32x4_t cut[kCuts];
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      const float v0 = c < 2 ? d0[2 * (c & 1)] : d1[2 * (c & 1)], v1 = c < 2 ? d0[2 * (c & 1) + 1] : d1[2 * (c & 1) + 1];
-      hi[c] = pack_bf16x2(v0, v1);
-      lo[c] = pack_bf16x2(v0 - bf16_lo(hi[c]), v1 - bf16_hi(hi[c]));
+      float v0 = c < 2 ? d0[2 * (c & 1)] : d1[2 * (c & 1)], v1 = c < 2 ? d0[2 * (c & 1) + 1] : d1[2 * (c & 1) + 1];
+#pragma unroll
+      for (int i = 0; i < kCuts; ++i) {
+        cut[i][c] = __builtin_amdgcn_perm(__float_as_uint(v1), __float_as_uint(v0), 0x07060302u);
+        v0 -= bf16_lo(cut[i][c]);
+        v1 -= bf16_hi(cut[i][c]);
+      }
     }
-    s_d[wave][0][lane] = hi;
-    s_d[wave][1][lane] = lo;
+#pragma unroll
+    for (int i = 0; i < kCuts; ++i) s_d[wave][i][lane] = cut[i];
     __syncthreads();
 #pragma unroll
     for (int s = 0; s < kJoinWaves; ++s)
-      if (32 * s < a.r) {
-        low = product(s_d[s][0][lane], u[s], low, std::false_type{});
-        low = product(s_d[s][1][lane], u[s], low, std::false_type{});
-      }
+      if (32 * s < a.r)
+#pragma unroll
+        for (int i = 0; i < kCuts; ++i) low = product(s_d[s][i][lane], u[s], low, std::false_type{});
   }
   if (!mine) return;
   const float g = a.g ? __builtin_amdgcn_ldexpf(a.g[0], -exponent_of(a.g[0])) : 1.0f;
