@@ -85,3 +85,28 @@ def test_the_branch_up_to_the_largest_number(L, fmt, sign):  # noqa: F811
     torch.cuda.synchronize()
     want = np.array([sign * (2.0 ** 128 - 2.0 ** 118), 1.0])[:, None] * up[:, 3].astype(np.float64)
     assert np.all(np.abs(Y.float().cpu().numpy() - want) <= 2.0 ** -8 * np.abs(want))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M", [2, 20, 50])
+@pytest.mark.parametrize("r", [0, 8, 64, 128])
+@pytest.mark.parametrize("smooth", [False, True])
+def test_an_infinity_among_positive_numbers_is_the_result(L, fmt, M, r, smooth):  # noqa: F811
+    """Every weight, factor and channel positive: the row of the infinity is infinite, not NaN, and the
+    others are what they are without it."""
+    torch = torch_mod()
+    rng = np.random.default_rng(33)
+    N, K = 40, 1024
+    codes = (rng.integers(1, 8, (N, K // 2)) | rng.integers(1, 8, (N, K // 2)) << 4).astype(np.uint8)
+    X = np.exp(rng.standard_normal((M, K))).astype(np.float32)
+    down, up = (np.exp(rng.standard_normal(s)).astype(np.float32) for s in ((r, K), (N, r)))
+    lam = dev(np.exp(rng.standard_normal(K)).astype(np.float32)) if smooth else None
+    pw = plain_weight(L, fmt, codes, r, up)
+    d = dev_bf16(bf16_rne(down)) if r else None
+    clean = L.gemv(dev_bf16(bf16_rne(X)), pw, lam, d)
+    for at in (0, 129, 700, K - 1):
+        Z = X.copy()
+        Z[M - 1, at] = np.inf
+        Y = L.gemv(dev_bf16(bf16_rne(Z)), pw, lam, d)
+        torch.cuda.synchronize()
+        assert torch.equal(Y[:M - 1], clean[:M - 1]) and torch.isposinf(Y[M - 1]).all(), at

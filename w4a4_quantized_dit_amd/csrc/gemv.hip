@@ -393,7 +393,9 @@ __device__ __forceinline__ void down_part(const GemvArgs& a, int part, uint8_t* 
     x.load(a, p0 + CH, 0);
     lds_barrier();
 #pragma unroll
-    for (int d = 0; d < CH; ++d) {  // (the other turn's pieces are zeros, and change no sum)
+    for (int d = 0; d < CH; ++d) {
+      // (not the other turn's pieces: their zeros times an infinity would be NaN)
+      if ((d & (turns - 1)) != my) continue;
       const uint8_t* xp = s_x + d * (kPiece * 2);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -507,7 +509,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void k_gemv_join(GemvArgs a) {
     }
   }
   if (a.r) {
-    // (cut off, not rounded: a number near fp32's largest stays one)
+    // (cut off, not rounded: a number near fp32's largest stays one; of an infinity or NaN the rest is zero)
     u32x4_t cut[kCuts];
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
@@ -515,8 +517,8 @@ __global__ __launch_bounds__(64 * kJoinWaves) void k_gemv_join(GemvArgs a) {
 #pragma unroll
       for (int i = 0; i < kCuts; ++i) {
         cut[i][c] = __builtin_amdgcn_perm(__float_as_uint(v1), __float_as_uint(v0), 0x07060302u);
-        v0 -= bf16_lo(cut[i][c]);
-        v1 -= bf16_hi(cut[i][c]);
+        v0 = __builtin_isfinite(v0) ? v0 - bf16_lo(cut[i][c]) : 0.0f;
+        v1 = __builtin_isfinite(v1) ? v1 - bf16_hi(cut[i][c]) : 0.0f;
       }
     }
 #pragma unroll
