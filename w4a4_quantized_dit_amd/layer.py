@@ -342,10 +342,10 @@ class KVCache:
     bits: int = 8        # 8: E4M3 codes, a scale per page and head; 4: MXFP4, one per token and 32 channels
 
 
-def _by_bits(cache, eight, four):
-    if cache.bits not in (4, 8):
-        raise ValueError(f"a cache of {cache.bits} bits: must be 4 or 8")
-    return eight if cache.bits == 8 else four
+def _by_bits(bits, eight, four):
+    if bits not in (4, 8):
+        raise ValueError(f"a cache of {bits} bits: must be 4 or 8")
+    return eight if bits == 8 else four
 
 
 def kv_cache(n_pages, heads, dim, device="cuda", bits=8):
@@ -364,7 +364,7 @@ def kv_write(cache, K, V, block_table, cu_rows, start, max_rows):
     """Append the packed rows K, V [rows, heads·dim] bf16: sequence b's rows cu_rows[b] ..
     cu_rows[b + 1] become its tokens start[b] onward, quantised with one scale a page and head (8
     bits) or a token and 32 channels (4 bits)."""
-    _by_bits(cache, _lib.svdq_kv_write, _lib.svdq_kv4_write)(
+    _by_bits(cache.bits, _lib.svdq_kv_write, _lib.svdq_kv4_write)(
         K, V, cache.dim, cu_rows, start, max_rows, block_table, cache.k_codes, cache.v_codes,
         cache.k_scales, cache.v_scales)
 
@@ -376,7 +376,7 @@ def kv_read(cache, block_table, cu_rows, start, rows, max_rows, out=None):
         K = torch.empty(rows, cache.k_codes.shape[1] * cache.dim, dtype=torch.bfloat16,
                         device=cache.k_codes.device)
         out = [K, torch.empty_like(K)]
-    _by_bits(cache, _lib.svdq_kv_read, _lib.svdq_kv4_read)(
+    _by_bits(cache.bits, _lib.svdq_kv_read, _lib.svdq_kv4_read)(
         out[0], out[1], cache.dim, cu_rows, start, max_rows, block_table, cache.k_codes, cache.v_codes,
         cache.k_scales, cache.v_scales)
     return out[0], out[1]
@@ -385,8 +385,8 @@ def kv_read(cache, block_table, cu_rows, start, rows, max_rows, out=None):
 def attention_workspace(rows, q_heads, kv_heads, dim, B, max_rows, max_kv, device="cuda", bits=8):
     """A workspace for attention() of these sizes over a cache of `bits` bits (None when none is
     needed)."""
-    need = _lib.svdq_attn_kv8_workspace_bytes if bits == 8 else _lib.svdq_attn_kv4_workspace_bytes
-    nb = need(rows, q_heads, kv_heads, dim, B, max_rows, max_kv)
+    nb = _by_bits(bits, _lib.svdq_attn_kv8_workspace_bytes, _lib.svdq_attn_kv4_workspace_bytes)(
+        rows, q_heads, kv_heads, dim, B, max_rows, max_kv)
     if nb < 0:
         raise ValueError("unsupported attention shape")
     return _bytes(nb, device) if nb else None
@@ -406,7 +406,7 @@ def attention(Q, cache, block_table, cu_rows, kv_len, max_rows, max_kv, scale=No
     if workspace is None:
         workspace = attention_workspace(rows, q_heads, heads, dim, block_table.shape[0], max_rows,
                                         max_kv, Q.device, cache.bits)
-    _by_bits(cache, _lib.svdq_attn_kv8, _lib.svdq_attn_kv4)(
+    _by_bits(cache.bits, _lib.svdq_attn_kv8, _lib.svdq_attn_kv4)(
         Q, dim, cu_rows, kv_len, max_rows, max_kv, block_table, cache.k_codes, cache.v_codes,
         cache.k_scales, cache.v_scales, dim ** -0.5 if scale is None else scale, causal, O, lse,
         workspace)
