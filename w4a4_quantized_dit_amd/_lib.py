@@ -797,6 +797,8 @@ def svdq_qk_norm_rope(X, q_heads, k_heads, dim, gamma_q, gamma_k, eps, pos, freq
             _gamma(a, gamma_k, dim, bf, "gamma_k"), float(eps), p,
             a.vec(freq, sum(axis_dims) // 2, torch.float64, "freq"), n, arr, int(bool(interleaved)),
             y, ldy)
+    if M == 0:   # an empty tensor has no address
+        return
     a.call("svdq_qk_norm_rope", stream, *args)
 
 
@@ -828,4 +830,6 @@ def svdq_w4a16_gemv(fmt, X, lam, lora_down, r, w_codes, w_scales, g_w, lora_up, 
             a.vec(w_codes, N * K // 2, u8, "w_codes"), a.vec(w_scales, N * K // group, kind, "w_scales"),
             a.vec(g_w, 1, f32, "g_w") if fmt == NVFP4 else None, up, int(N), y, ldy,
             a.vec(workspace, 0, u8, "workspace"), workspace.numel() if workspace is not None else 0)
+    if M == 0:
+        return
     a.call("svdq_w4a16_gemv", stream, *args)

@@ -271,7 +271,7 @@ def gemv(X, pw, lam, lora_down, out=None, workspace=None):
     X2 = X if X.dim() == 2 else X.reshape(-1, X.shape[-1])
     M = X2.shape[0]
     Y = out if out is not None else torch.empty(M, pw.N, dtype=torch.bfloat16, device=X.device)
-    if workspace is None:
+    if workspace is None and M:
         workspace = gemv_workspace(M, pw, X.device)
     _lib.svdq_w4a16_gemv(pw.fmt, X2, lam, lora_down, pw.r, pw.codes, pw.scales, pw.g, pw.lora_up, pw.N,
                          Y, workspace)
