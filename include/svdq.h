@@ -673,7 +673,9 @@ svdq_status svdq_attn_kv4(const uint16_t* Q, int64_t ldq, int64_t rows, int64_t 
  * multiple of 256, at most 2^22; N in [1, 2^28]; lora_down [r, K], lora_up [N, r] bf16, r as at
  * svdq_quantize_weight; Y [M, N] bf16, leading dimension ldy >= N, not overlapping X.  X, lambda, the weight
  * and the factors 16-byte aligned.  x̂ and w enter exactly, but for NVFP4 and INT4_G64 a channel 2^29 times
- * smaller than the largest of its 256 (channels 256i to 256i + 255), which loses bits of its eight.
+ * smaller than the largest of its 256 (channels 256i to 256i + 255), which loses bits of its eight.  NVFP4
+ * scale bytes are 0 to 0x7E, as svdq_quantize_weight writes them: 0x7F, E4M3's NaN, counts as 480 here and at
+ * svdq_w4a4_gemm.
  * fp32 sums in a fixed order, no atomics: results repeat bit for bit, and a row's result does not depend
  * on the other rows or their number.  workspace: at least svdq_w4a16_gemv_workspace_bytes(M, N, K, r)
  * bytes (−1: unsupported), 256-byte aligned, the caller's, not shared with a call that may run at the

@@ -1,6 +1,8 @@
 // Softmax attention of bf16 query rows over the paged 4-bit cache (kv4_layout.h), by the formulas and in
 // the blocks of the 8-bit cache's attention (attn.hip): one pass over the pages with a running maximum,
-// Sᵀ = K·Qᵀ and Oᵀ += Vᵀ·Pᵀ on the 32x32x16 bf16 MFMA, fp32 statistics and sums, P rounded to bf16 once.
+// Sᵀ = K·Qᵀ and Oᵀ += Vᵀ·Pᵀ on the 32x32x16 bf16 MFMA, fp32 statistics and sums.  P is rounded to bf16 once, as
+// there and for the same reason (fp16 has not the range of V's powers of two): 2.1 to 2.4e-3 of O in the root
+// mean square with O's own rounding, which is 1.6 to 1.7e-3 alone.
 //
 // The codes are widened to bf16 exactly, each block of 32 channels of a token with its own power of two.
 // A lane's piece of K is one such block, so its conversions share a scale.  In a lane's piece of V the
@@ -382,35 +384,35 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void k_attn4_tile(AttnArgs a) {
   if (live) store_row<DIM>(a, st, l, s.first + tok, head, split, half);
 }
 
-// Element e of a block's [rows, DIM] outputs from its four waves' sums: the bf16, or a split's part.
+// Element e of a block's [rows, DIM] outputs from its waves' sums: the bf16, or a split's part.
 template <int DIM, int PITCH, int WAVES>
 __device__ __forceinline__ void store_joined(const AttnArgs& a, const Seq& s, const float (&s_o)[WAVES][DIM][PITCH],
                                              const float (&s_m)[WAVES][PITCH - 1],
                                              const float (&s_l)[WAVES][PITCH - 1], int e, int r0, int split) {
-      const int rr = e / DIM, d = e % DIM;
-      float sum = 0.0f, l = 0.0f;
-      float mm = s_m[0][rr];
+  const int rr = e / DIM, d = e % DIM;
+  float sum = 0.0f, l = 0.0f;
+  float mm = s_m[0][rr];
 #pragma unroll
   for (int w = 1; w < WAVES; ++w) mm = fmaxf(mm, s_m[w][rr]);
-  #pragma unroll
-      for (int w = 0; w < WAVES; ++w) {
-        sum += s_o[w][d][rr];
-        l += s_l[w][rr] * __builtin_amdgcn_exp2f(s_m[w][rr] - mm);
-      }
-      const int64_t token = s.first + (r0 + rr) / a.G;
-      const int hd = s.h * a.G + (r0 + rr) % a.G;
-      if (a.splits > 1) {
-        const int64_t at = ((int64_t)split * a.rows + token) * a.Hq + hd;
-        a.part[at * DIM + d] = sum;
-        if (d == 0) {
-          float* ml = a.part + (int64_t)a.splits * a.rows * a.Hq * DIM + at * 2;
-          ml[0] = mm;
-          ml[1] = l;
-        }
-      } else {
-        a.O[token * a.ldo + (int64_t)hd * DIM + d] = f32_to_bf16(l != 0.0f ? sum / l : 0.0f);
-        if (a.lse && d == 0) a.lse[token * a.Hq + hd] = lse_of(a, mm, l);
-      }
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w) {
+    sum += s_o[w][d][rr];
+    l += s_l[w][rr] * __builtin_amdgcn_exp2f(s_m[w][rr] - mm);
+  }
+  const int64_t token = s.first + (r0 + rr) / a.G;
+  const int hd = s.h * a.G + (r0 + rr) % a.G;
+  if (a.splits > 1) {
+    const int64_t at = ((int64_t)split * a.rows + token) * a.Hq + hd;
+    a.part[at * DIM + d] = sum;
+    if (d == 0) {
+      float* ml = a.part + (int64_t)a.splits * a.rows * a.Hq * DIM + at * 2;
+      ml[0] = mm;
+      ml[1] = l;
+    }
+  } else {
+    a.O[token * a.ldo + (int64_t)hd * DIM + d] = f32_to_bf16(l != 0.0f ? sum / l : 0.0f);
+    if (a.lse && d == 0) a.lse[token * a.Hq + hd] = lse_of(a, mm, l);
+  }
 }
 
 // Few rows (single tokens, small groups): blocks of 32, whose four waves take every fourth page each,
@@ -560,16 +562,19 @@ __global__ __launch_bounds__(256, 2) void k_attn4_few(AttnArgs a) {
 }
 
 // At most 16 rows of a key head (single tokens whose query heads share it): the same on the 16x16x32 MFMA, in
-// half the matrix instructions, exponentials and registers, so that three waves a SIMD have their loads on
-// the way and not two.  A block takes `chunk` pages (attn_chunk), its waves every eighth or fourth of them.
+// half the matrix instructions, exponentials and registers, so that with blocks of four waves three a SIMD have
+// their loads on the way and not two (of eight: two, one block a CU).  A block takes `chunk` pages (attn_chunk), its waves every eighth or fourth of them.
 //
 // The lanes of K's and V's operands differ from the stored ones in one bit of the lane and one of the dword,
 // which lane swaps of the codes exchange: lane 16·g + n of K has token n of sixteen at 8 channels, of V
 // four tokens 4·g on at channels 2·n, 2·n + 1 of 32.  V's scales come as a word a lane and pass through LDS.
 //
-// Bound by the vector instructions, 460 a page, which take a SIMD 0.9 us (a lone block of four waves or of
-// eight walks 64 pages in 15 us): 32 sequences of 8191 tokens, 8 key heads of 128 with 5 rows each, 50.2 us,
-// 5.7 TB/s (with the 32 rows' kernel 54.6), ragged ones 45.5 (53.7).
+// 32 sequences of 8191 tokens, 8 key heads of 128 with 5 rows each: 50 to 53 us in graphs over caches of more
+// than 1 GB in turn, 5.7 to 5.4 TB/s, bound by the bytes (with the 32 rows' kernel 54.6).  Ragged ones, 195 MB of
+// cache, 45.5 to 46.8 (53.7), 4.2 TB/s: the blocks of the longest sequences last longest, and such a block is
+// bound by its instructions, 460 of the vector unit a page, 0.9 us of a SIMD (a lone block of four waves or of
+// eight walks 64 pages in 15 us).  On average the SIMDs are busy 0.36 of the time, and the waves wait for loads
+// 0.4 of theirs.
 constexpr int kLeastRows = 16;
 
 struct Words2 {
@@ -821,7 +826,10 @@ __global__ __launch_bounds__(64 * WAVES, 3) void k_attn4_row16(AttnArgs a) {
 // tokens, 8 key heads of 128, 58 us for 47), blocks of four, three a CU, beyond (64 sequences of 4096 tokens,
 // 16 heads of 64, 57 us for 71; the other way round 32 ragged ones 56 for 47).  At least eight pages a
 // block, one for each wave, and none split below 24: the join is a launch (one head over 16 pages 10.7 us in two
-// splits and 9.5 in one, over 32 11.5 in four and 13.4).  More rows: as for the 8-bit cache.
+// splits and 9.5 in one, over 32 11.5 in four and 13.4).  More rows: as for the 8-bit cache, by constants that are
+// fitted to its kernels and not to these: 1008 causal rows of 40 heads of 128 over 31688 tokens take 631 us (8
+// bits: 613), two sequences of 256 rows of 24 heads over 16384 149 (135), four of 128 rows of 40 / 8 heads over
+// 8192 102 (101), 16 of 40 rows of 8 heads of 64 over 8192 39 (46), 17 rows of 40 heads of 128 over 30000 44 (61).
 static AttnPlan attn4_plan(int64_t G, int64_t Hkv, int64_t dim, int64_t rows, int64_t B, int64_t max_q,
                            int64_t max_kv) {
   constexpr int64_t kCus = 256, kLeast = 8, kLeastSplit = 24;

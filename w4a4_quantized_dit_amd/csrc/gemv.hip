@@ -15,9 +15,12 @@
 // tensor scale g is about 2^-16 of the weight, and sums without it would pass fp32's range long before the result:
 // they are scaled back with g's power of two, exactly, and the join multiplies by the rest of g, in [1, 2).
 //
-// Measured (both kernels, graphs): one row of 5120x5120 NVFP4, rank 32, 14.2 us, five of 5120x13824 MXFP4, rank
-// 128, 19.4 (without it 14.8, 2.5 TB/s), 32 of 13824x5120 int4, rank 32, 28, where widening the codes and forming
-// x̂ take the vector units longer than the bytes need; two rows of 13824x13824 NVFP4 33 us, 3.2 TB/s.
+// Measured, here and below (both kernels, in graphs over 600 MB of weights in turn, which no cache holds: a
+// token's step reads each weight once): one row of 5120x5120 NVFP4, rank 32, 14.4 us, five of 5120x13824 MXFP4,
+// rank 128, 19.5 (without it 14.8, 2.5 TB/s), 32 of 13824x5120 int4, rank 32, 28.6; two rows of 13824x13824 NVFP4
+// 33 us, 3.2 TB/s.  The 32 rows are bound by the vector instructions (widening the codes, forming x̂ in every
+// block; 0.40 of the SIMDs' time) and by the loads that these wait for, a third of the waves' time: with two tiles
+// of rows one chunk is on its way while the one before it is computed.
 //
 // Two kernels.  The first splits N among waves and K among blocks, so that even one row's weight is
 // asked for all at once, and writes fp32 sums of each part of K; x̂ is formed on the way into LDS, a part
@@ -457,7 +460,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void k_gemv_part(GemvArgs a) {
 
 // The parts' sums and the up factor's product.  A wave has 16 outputs of 16 rows; D, which the block's
 // waves share, is cut into three bf16 of eight bits each, 32 ranks a wave, so that its products are exact in
-// the fp32 sum (two would be 16 bits of it; the third takes no time that shows).  Its time is a launch and the
+// the fp32 sum (two would be 16 bits of it, and 0.1 us less).  Its time is a launch and the
 // latency of loads, so all are on their way at once: eight parts of either, the ones past the last are
 // buffer loads without a request.  (With loops that end at the last part: one row of 5120x5120 NVFP4, rank
 // 32, 14.8 us for 14.3, five of 5120x13824 MXFP4, rank 128, 20.5 for 19.4, both kernels.)
